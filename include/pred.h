@@ -330,6 +330,195 @@ int pred_decode_step(pred_t* p, int32_t layer0, int32_t n_layers, const pred_bf1
  * sorted runs, twice that for n_blocks > 8192 (pairwise merge buffers). */
 size_t pred_rank_workspace_bytes(int64_t n_blocks, int64_t n_segments);
 
+/* ------------------------------------------------------------------ the paged KV cache
+ *
+ * The operators around the predictor: putting new tokens into a paged KV cache
+ * with rotary positions, attending over that cache, and evicting from it by the
+ * attention its blocks really gathered -- the measured counterpart of the
+ * predicted block score, ranked by the same rule.  A decode or verify step runs
+ *   pred_rotate_store, pred_attend, (the caller accepts drafted tokens),
+ *   pred_accumulate_weight, pred_evict_blocks
+ * on one stream.  None of these calls allocates, synchronises or issues a
+ * memset, so a caller may capture them into a HIP graph.  They take num_q_heads,
+ * num_kv_heads, head_dim, block_size and max_blocks from the handle, and the
+ * handle's device must be the current one (PRED_ERR_OUT_OF_RANGE otherwise). */
+
+/* Element type of a KV cache: bf16, or 8-bit e4m3 (1 sign, 4 exponent, 3
+ * fraction bits, no infinities, largest value 448). */
+enum { PRED_KV_BF16 = 0, PRED_KV_FP8 = 1 };
+
+/* One layer's paged KV cache, memory of the caller's.  Token t of block b, head
+ * h is head_dim consecutive elements at
+ *   b * block_stride + t * token_stride + h * head_stride
+ * (strides in elements, the same for k and v), so both [max_blocks, block_size,
+ * num_kv_heads, head_dim] (the layout pred_project_kv_block reads) and
+ * [max_blocks, num_kv_heads, block_size, head_dim] (A_g's) are views of it.
+ * k, v and every stride must be multiples of 16 bytes (bf16) or 8 bytes (FP8),
+ * token_stride and head_stride >= head_dim, and block_stride at least one
+ * block's extent.  An element stands for scale * stored; with bf16 both scales
+ * must be 1. */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t block_stride, token_stride, head_stride;
+    int32_t dtype;
+    float k_scale, v_scale;
+} pred_kv_cache;
+
+/* How a rotation's frequencies are stretched for contexts longer than the model
+ * was trained on (pred_rope_scaling.kind). */
+enum {
+    PRED_ROPE_NONE = 0,   /* f_i = theta^(-2 i / rot_dim) */
+    PRED_ROPE_LINEAR = 1, /* f_i / factor */
+    PRED_ROPE_NTK = 2,    /* theta * factor^(rot_dim / (rot_dim - 2)) in place of theta */
+    PRED_ROPE_LLAMA3 = 3, /* f_i where its wavelength 2 pi / f_i is below original_length / high, f_i / factor
+                             where it is above original_length / low, and between them
+                             (1 - m) f_i / factor + m f_i, m = (original_length / wavelength - low) / (high - low) */
+    PRED_ROPE_YARN = 4    /* f_i / factor * ramp_i + f_i * (1 - ramp_i), ramp_i = clamp((i - a) / max(b - a, 0.001),
+                             0, 1), a = max(floor(d(high)), 0), b = min(ceil(d(low)), rot_dim - 1), d(n) = rot_dim *
+                             ln(original_length / (2 pi n)) / (2 ln theta); mscale = 0.1 ln(factor) + 1 */
+};
+typedef struct {
+    int32_t kind;
+    double factor, low, high, original_length;
+} pred_rope_scaling;
+
+/* A rotation: `turns` is the device copy of pred_rope_turns's output. */
+typedef struct {
+    const uint64_t* turns; /* device, [rot_dim / 2] */
+    int32_t rot_dim;       /* the first rot_dim values of a head turn, the others pass; even, <= head_dim */
+    int32_t interleaved;   /* pairs (2 i, 2 i + 1) if not 0, else (i, i + rot_dim / 2) */
+    int32_t backward;      /* not 0: the transposed map, the gradient of the rotation */
+    float mscale;          /* factor on cosine and sine */
+} pred_rope;
+
+/* Frequencies of a rotation, on the host (no device access): turns[i] is
+ * f_i / (2 pi), the turns a position adds to pair i, as a 64-bit binary
+ * fraction (value * 2^64, modulo whole turns).  position * turns[i] modulo 2^64
+ * is then the angle of any position without loss: its error is under
+ * |position| * 2^-53 turns, where a float32 angle would be off by radians.
+ * `scaling` NULL means PRED_ROPE_NONE.  mscale (host, may be NULL) receives the
+ * factor for pred_rope.mscale.  PRED_ERR_OUT_OF_RANGE for rot_dim odd, < 2 or
+ * > 65536, theta <= 1, a factor <= 0, an unknown kind, rot_dim 2 with NTK, or
+ * low, high, original_length that the kind cannot use (LLAMA3: 0 < low < high
+ * and original_length > 0; YARN: low, high and original_length > 0). */
+int pred_rope_turns(int32_t rot_dim, double theta, const pred_rope_scaling* scaling, uint64_t* turns, float* mscale);
+
+/* Rotary positions: for token t, head h and pair (a, b) at frequency f,
+ *   out_a = mscale * (x_a cos(pos f) - x_b sin(pos f))
+ *   out_b = mscale * (x_a sin(pos f) + x_b cos(pos f))
+ * (rope->backward: sin negated -- the gradient with respect to x of a forward
+ * call, given the gradient of its output), computed in float32 and rounded once
+ * to bf16.  Values past rot_dim are copied.
+ *   x          device, [n_tokens, n_heads, head_dim] bf16, tokens x_stride elements apart
+ *   positions  device, [n_tokens] int32 (any value, negative ones turn back)
+ *   out        device, as x with out_stride; may be x itself (same stride), else it must not overlap it
+ * x, out and the strides must be multiples of 16 bytes, strides >= n_heads *
+ * head_dim; head_dim <= 512 (PRED_ERR_UNSUPPORTED above). */
+int pred_rotate(pred_t* p, const pred_rope* rope, const pred_bf16* x, int64_t x_stride, int64_t n_tokens,
+                int32_t n_heads, const int32_t* positions, pred_bf16* out, int64_t out_stride, void* stream);
+
+/* The start of a step over the cache, in one launch: the new tokens' queries and
+ * keys rotated as by pred_rotate, the queries to q_out, the keys and the values
+ * into the cache.
+ *   q, k, v    device, [n_tokens, num_q_heads | num_kv_heads | num_kv_heads, head_dim] bf16, tokens q_stride,
+ *              k_stride, v_stride elements apart (so all three may lie side by side in one buffer)
+ *   slots      device, [n_tokens] int64: where a token goes, block * block_size + offset; -1 stores nothing
+ *              (a padding token).  Any other value outside the cache stores nothing and raises the device error
+ *              word.  Two tokens with one slot race.
+ *   q_out      device, [n_tokens, num_q_heads, head_dim] bf16; may be q itself if q_stride is num_q_heads * head_dim
+ * A bf16 cache takes keys and values rounded once; an FP8 cache takes value /
+ * scale clamped to +-448 and rounded once (nearest, ties to even), NaN kept.
+ * rope->backward must be 0. */
+int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int64_t q_stride, const pred_bf16* k,
+                      int64_t k_stride, const pred_bf16* v, int64_t v_stride, int64_t n_tokens,
+                      const int32_t* positions, const int64_t* slots, const pred_kv_cache* cache, pred_bf16* q_out,
+                      void* stream);
+
+/* Attention of each sequence's newest tokens over its cached ones: one token
+ * (n_rows = 1, a decode step) or a tree of drafted tokens to verify.  A
+ * sequence's tokens 0 .. kv_len - 1 lie in the blocks of its table in order, the
+ * drafted ones last; with d = draft_len, row i < d is token kv_len - d + i.  It
+ * sees every token before kv_len - d (the context), and drafted token j if bit j
+ * of its tree word is set.
+ *   q             device, [n_seqs, n_rows, num_q_heads, head_dim] bf16, 1 <= n_rows <= 64
+ *   tree          device, [n_seqs, n_rows] 64-bit words, or NULL for a chain (row i sees drafted tokens 0 .. i)
+ *   block_tables  device, [n_seqs, n_blocks] int32 physical ids, or NULL for the identity
+ *   kv_len        device, [n_seqs] int32 in [0, n_blocks * block_size], or NULL for that upper limit
+ *   draft_len     device, [n_seqs] int32 in [0, min(n_rows, kv_len)], or NULL for that upper limit
+ *   out           device, [n_seqs, n_rows, num_q_heads, head_dim] bf16: softmax(scale * q k) v over the row's tokens
+ *   lse           device, [n_seqs, n_rows, num_q_heads] float32 or NULL: the log of the softmax's sum
+ *   block_lse     device, [n_seqs, n_blocks, n_rows, num_q_heads] float32 or NULL: the same sum over each block's
+ *                 tokens alone, for pred_accumulate_weight; blocks at or past kv_len / block_size rounded up are left
+ *                 as they were
+ *   workspace     device scratch of pred_attend_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0)
+ * A row past draft_len and a row that sees no token have output 0 and lse -inf.
+ * Query head h reads kv head h / (num_q_heads / num_kv_heads).  Sums and the
+ * softmax are held in float32.  What a masked token holds (NaN, infinities)
+ * does not reach a row that cannot see it.  Lengths outside their range are
+ * clamped, and a block whose table entry is outside [0, max_blocks) is left out
+ * of every sum; both raise the device error word.  head_dim <= 256
+ * (PRED_ERR_UNSUPPORTED above); n_blocks * block_size <= 2^31 - 64. */
+int pred_attend(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32_t n_rows, const uint64_t* tree,
+                const int32_t* block_tables, int64_t n_blocks, int32_t n_seqs, const int32_t* kv_len,
+                const int32_t* draft_len, float scale, pred_bf16* out, float* lse, float* block_lse, void* workspace,
+                size_t ws_bytes, void* stream);
+
+/* Workspace of pred_attend for this shape on this handle (partial results of a
+ * long context split over workgroups); 0 for a NULL handle or counts < 1.  Calls
+ * that may run at the same time need workspaces of their own. */
+size_t pred_attend_workspace_bytes(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_blocks);
+
+/* Name of the kernel pred_attend runs for this handle, cache and shape (host
+ * only, static string): "attend_stream_kernel" (up to 32 queries per kv head),
+ * "attend_tree_kernel" (more) or "attend_plain_kernel" (head sizes other than
+ * 64 and 128, cache rows off 16-byte alignment, or block sizes the two do not
+ * take).  NULL for a NULL argument or n_rows outside [1, 64]. */
+const char* pred_attend_kernel_name(pred_t* p, const pred_kv_cache* cache, int32_t n_rows, int32_t with_block_lse);
+
+/* Accumulated attention weight of each block, from pred_attend's lse and
+ * block_lse:
+ *   mass_out[s, b] = decay * mass[s, b] + sum over accepted rows i, heads h of
+ *                    exp(block_lse[s, b, i, h] - lse[s, i, h])
+ * for the blocks that kv_len tokens use; the others keep their mass.  Rows with
+ * lse = -inf add nothing.
+ *   accepted   device, [n_seqs] 64-bit words, bit i = row i counts (a draft's accepted tokens), or NULL for all
+ *   kv_len     as for pred_attend
+ *   mass       device, [n_seqs, n_blocks] float32
+ *   mass_out   device, as mass; may be mass itself, else it must not overlap it
+ * The order of the sum is fixed: equal inputs give equal bits. */
+int pred_accumulate_weight(pred_t* p, const float* lse, const float* block_lse, int32_t n_rows,
+                           const uint64_t* accepted, const int32_t* kv_len, int64_t n_blocks, int32_t n_seqs,
+                           float decay, const float* mass, float* mass_out, void* stream);
+
+/* Eviction to a budget of blocks.  A sequence uses n = kv_len / block_size
+ * rounded up blocks; if that is above `budget`, the n - budget blocks of lowest
+ * mass among blocks protect_first .. n - protect_last - 1 are evicted (all of
+ * those if they are fewer), in pred_rank_victims's order: equal mass by lower
+ * index first, -0 equal to +0, NaN lowest.
+ *   tables_out   the kept blocks' entries in their order, then the evicted ones' in theirs; entries from n on as in
+ *                block_tables.  So the evicted slots are the next ones the sequence fills, or a list to give back.
+ *   mass_out     the kept blocks' mass in that order, then 0 for the evicted ones; from n on as in mass
+ *   kv_len_out   kv_len - evicted * block_size
+ *   evicted      [n_seqs] int32 output: the number of blocks evicted
+ * block_tables, tables_out [n_seqs, n_blocks] int32; mass, mass_out [n_seqs,
+ * n_blocks] float32; kv_len, kv_len_out [n_seqs] int32, kv_len never NULL.
+ * Each output may be its input itself, else it must not overlap it.  budget >=
+ * 0, protect_first >= 0, protect_last >= 1 (the last block, which may be partly
+ * filled, stays; protect as many as hold drafted tokens).  Any [n_seqs,
+ * n_blocks] float32 score works as mass, pred_score_blocks's among them.  A
+ * kv_len outside [0, n_blocks * block_size] is clamped and raises the device
+ * error word.
+ *   workspace   pred_evict_workspace_bytes() bytes, 8-byte aligned (NULL when 0) */
+int pred_evict_blocks(pred_t* p, const int32_t* block_tables, const float* mass, const int32_t* kv_len,
+                      int64_t n_blocks, int32_t n_seqs, int64_t budget, int32_t protect_first, int32_t protect_last,
+                      int32_t* tables_out, float* mass_out, int32_t* kv_len_out, int32_t* evicted, void* workspace,
+                      size_t ws_bytes, void* stream);
+
+/* Workspace of pred_evict_blocks: 0 for n_blocks <= 32768 (a sequence's entries
+ * are held in registers), else 8 bytes per entry. */
+size_t pred_evict_workspace_bytes(int64_t n_blocks, int32_t n_seqs);
+
 /* ------------------------------------------------------------------ inspection */
 
 /* The P that pred_create builds for (head_dim, r, seed), computed on the host
@@ -352,8 +541,9 @@ int pred_read_slot(pred_t* p, int32_t layer, int64_t block, pred_bf16* host_out,
 int pred_get_dims(pred_t* p, pred_dims* out);
 
 /* Synchronise `stream`, read and clear the device error word.  Returns 0, or
- * PRED_ERR_DEVICE if a kernel since the last call met an invalid table entry
- * or a last-block fill count outside [0, block_size]. */
+ * PRED_ERR_DEVICE if a kernel since the last call met an invalid table entry,
+ * a last-block fill count outside [0, block_size], a cache slot outside the
+ * cache or a sequence length outside its range. */
 int pred_device_error(pred_t* p, void* stream);
 
 /* Message for the last failing call on this thread ("" if none). */

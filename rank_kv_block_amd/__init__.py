@@ -13,8 +13,15 @@ import numpy as np
 from . import _lib
 from ._lib import (PRED_FLAG_ZERO_AG, PRED_OK, PredDims, ERROR_NAMES, PRED_NOALLOC_SCRATCH_BYTES,  # noqa: F401
                    PRED_SCORE_PATH_AUTO, PRED_SCORE_PATH_DECODE, PRED_SCORE_PATH_GENERIC,
+                   PRED_KV_BF16, PRED_KV_FP8, PRED_ROPE_NONE, PRED_ROPE_LINEAR, PRED_ROPE_NTK, PRED_ROPE_LLAMA3,
+                   PRED_ROPE_YARN,
                    PRED_ERR_INVALID_DIMS, PRED_ERR_OUT_OF_RANGE, PRED_ERR_OOM, PRED_ERR_UNSUPPORTED,
                    PRED_ERR_NULL_ARG, PRED_ERR_HIP, PRED_ERR_WORKSPACE, PRED_ERR_DEVICE)
+
+
+class PredHandle(ctypes.c_void_p):
+    """A handle with its dims beside it (they never change), so that a call need not ask for them."""
+    dims = None
 
 
 class PredError(RuntimeError):
@@ -103,8 +110,9 @@ def pred_last_error():
 # ------------------------------------------------------------------ lifetime
 
 def pred_create(d, seed, flags=0, stream=None):
-    h = ctypes.c_void_p()
+    h = PredHandle()
     _check(lib().pred_create(ctypes.byref(d), seed, flags, _stream(stream), ctypes.byref(h)))
+    h.dims = pred_get_dims(h)
     return h
 
 
@@ -112,9 +120,10 @@ def pred_create_with_projection(d, p_host, flags=0, stream=None):
     p = np.ascontiguousarray(p_host, dtype=np.uint16)
     if p.shape != (d.head_dim, d.r):
         raise ValueError(f"P must be [{d.head_dim}, {d.r}]")
-    h = ctypes.c_void_p()
+    h = PredHandle()
     _check(lib().pred_create_with_projection(ctypes.byref(d), p.ctypes.data_as(ctypes.c_void_p), flags,
                                              _stream(stream), ctypes.byref(h)))
+    h.dims = pred_get_dims(h)
     return h
 
 
@@ -310,6 +319,13 @@ def pred_decode_step(h, layer0, k_new, new_table, q, q_proj, block_tables, last_
                                   n_blocks, n_seqs, _ptr(last_fill, "last_fill", (torch.int32,)),
                                   _ptr(scores, "scores", (torch.float32,)), k, _ptr(victims, "victims", (torch.int32,)),
                                   _ptr(workspace, "workspace"), ws_bytes, _stream(stream)))
+
+
+# ------------------------------------------------------------------ the paged KV cache
+
+from .cache import (KVCache, Rope, pred_accumulate_weight, pred_attend, pred_attend_kernel_name,  # noqa: E402,F401
+                    pred_attend_workspace_bytes, pred_evict_blocks, pred_evict_workspace_bytes, pred_rope_turns,
+                    pred_rotate, pred_rotate_store)
 
 
 # ------------------------------------------------------------------ inspection

@@ -29,6 +29,15 @@ PRED_SCORE_PATH_AUTO = 0
 PRED_SCORE_PATH_DECODE = 1
 PRED_SCORE_PATH_GENERIC = 2
 
+PRED_KV_BF16 = 0
+PRED_KV_FP8 = 1
+
+PRED_ROPE_NONE = 0
+PRED_ROPE_LINEAR = 1
+PRED_ROPE_NTK = 2
+PRED_ROPE_LLAMA3 = 3
+PRED_ROPE_YARN = 4
+
 ERROR_NAMES = {
     PRED_ERR_INVALID_DIMS: "INVALID_DIMS",
     PRED_ERR_OUT_OF_RANGE: "OUT_OF_RANGE",
@@ -53,11 +62,48 @@ class PredDims(ctypes.Structure):
     ]
 
 
+class PredKvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("block_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+    ]
+
+
+class PredRopeScaling(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("factor", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+        ("original_length", ctypes.c_double),
+    ]
+
+
+class PredRope(ctypes.Structure):
+    _fields_ = [
+        ("turns", ctypes.c_void_p),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("backward", ctypes.c_int32),
+        ("mscale", ctypes.c_float),
+    ]
+
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _u64 = ctypes.c_uint64
+_f32 = ctypes.c_float
+_sz = ctypes.c_size_t
 _PD = ctypes.POINTER(PredDims)
+_PC = ctypes.POINTER(PredKvCache)
+_PR = ctypes.POINTER(PredRope)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -90,6 +136,18 @@ SIGNATURES = {
     "pred_read_slot": (ctypes.c_int, [_vp, _i32, _i64, _vp, _vp]),
     "pred_get_dims": (ctypes.c_int, [_vp, _PD]),
     "pred_device_error": (ctypes.c_int, [_vp, _vp]),
+    "pred_rope_turns": (ctypes.c_int, [_i32, ctypes.c_double, ctypes.POINTER(PredRopeScaling), _vp,
+                                       ctypes.POINTER(_f32)]),
+    "pred_rotate": (ctypes.c_int, [_vp, _PR, _vp, _i64, _i64, _i32, _vp, _vp, _i64, _vp]),
+    "pred_rotate_store": (ctypes.c_int, [_vp, _PR, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _PC, _vp, _vp]),
+    "pred_attend": (ctypes.c_int, [_vp, _PC, _vp, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _sz,
+                                   _vp]),
+    "pred_attend_workspace_bytes": (_sz, [_vp, _i32, _i32, _i64]),
+    "pred_attend_kernel_name": (ctypes.c_char_p, [_vp, _PC, _i32, _i32]),
+    "pred_accumulate_weight": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _i64, _i32, _f32, _vp, _vp, _vp]),
+    "pred_evict_blocks": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                                         _sz, _vp]),
+    "pred_evict_workspace_bytes": (_sz, [_i64, _i32]),
     "pred_last_error": (ctypes.c_char_p, []),
     "pred_version": (ctypes.c_char_p, []),
 }

@@ -8,7 +8,7 @@
 namespace pred {
 
 // Bits of the device error word.
-enum : uint32_t { DEVERR_TABLE = 1u, DEVERR_FILL = 2u };
+enum : uint32_t { DEVERR_TABLE = 1u, DEVERR_FILL = 2u, DEVERR_SLOT = 4u, DEVERR_LEN = 8u };
 
 __host__ __device__ inline uint64_t f64_bits(double x) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -97,6 +97,8 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 // 16 bytes as a plain vector (uint4 is a union-based struct, which keeps arrays
 // of it from being split into registers)
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+
+inline bool aligned_to(const void* p, uintptr_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
 
 // Eight bf16 from 16 aligned bytes.
 __device__ inline bf16x8_t load8(const uint16_t* p) {

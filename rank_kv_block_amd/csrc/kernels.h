@@ -119,4 +119,106 @@ struct RowOrder {
 hipError_t launch_rank(const float* scores, int64_t n, int64_t n_seg, int64_t k, RowOrder ro, int32_t* victims,
                        void* ws, hipStream_t stream);
 
+// ---- the paged KV cache (rope.hip, attend.hip, evict.hip) -------------------
+// One layer's cache: element strides; fp8 is 8-bit e4m3 (else bf16).
+struct CacheView {
+    void* k;
+    void* v;
+    int64_t block_stride, token_stride, head_stride;
+    int fp8;
+    float k_scale, v_scale;
+};
+
+// A rotation: turns[i] = turns per position of pair i as a 64-bit fraction.
+struct RopeArgs {
+    const uint64_t* turns;
+    int rot;
+    int interleaved, backward;
+    float mscale;
+    const int32_t* positions;
+    int64_t n_tokens;
+    int D;
+    // queries (or any rotated tensor): [n_tokens, Hq, D] at q_stride -> out at out_stride
+    const uint16_t* q;
+    uint16_t* out;
+    int64_t q_stride, out_stride;
+    int Hq;
+    // keys and values into the cache at slots (Hk = 0: none)
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t k_stride, v_stride;
+    int Hk;
+    const int64_t* slots;
+    CacheView cache;
+    int64_t N;              // max_blocks
+    int B;
+    uint32_t* err;
+};
+hipError_t launch_rotate(const RopeArgs& a, hipStream_t stream);
+
+struct AttendArgs {
+    CacheView cache;
+    const uint16_t* q;      // [S, M, Hq, D]
+    const uint64_t* tree;   // [S, M] or null (chain)
+    const int32_t* tables;  // [S, n] or null
+    const int32_t* kv_len;  // [S] or null (n * B)
+    const int32_t* draft;   // [S] or null (min(M, kv_len))
+    uint16_t* out;          // [S, M, Hq, D]
+    float* lse;             // [S, M, Hq] or null
+    float* block_lse;       // [S, n, M, Hq] or null
+    void* ws;
+    uint32_t* err;
+    float scale;
+    int64_t N;              // max_blocks
+    int n;                  // blocks per sequence
+    int S, M, Hq, Hk, D, B;
+    int n_cu;
+};
+// Tokens in a sequence's cache and how many of them are drafted rows; values
+// outside their range are clamped (flagged by attend_check_lengths).
+__device__ inline int kv_len_of(const int32_t* kv_len, int s, int64_t most) {
+    if (!kv_len) return (int)most;
+    const int v = kv_len[s];
+    return v < 0 ? 0 : (v > most ? (int)most : v);
+}
+__device__ inline int draft_len_of(const AttendArgs& a, int s, int len) {
+    const int most = a.M < len ? a.M : len;
+    if (!a.draft) return most;
+    const int v = a.draft[s];
+    return v < 0 ? 0 : (v > most ? most : v);
+}
+hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
+size_t attend_workspace_bytes(const AttendArgs& a);
+const char* attend_kernel_name(const AttendArgs& a);
+
+struct WeightArgs {
+    const float* lse;          // [S, M, Hq]
+    const float* block_lse;    // [S, n, M, Hq]
+    const uint64_t* accepted;  // [S] or null
+    const int32_t* kv_len;     // [S] or null
+    const float* mass;         // [S, n]
+    float* mass_out;
+    uint32_t* err;
+    float decay;
+    int64_t n;
+    int S, M, Hq, B;
+};
+hipError_t launch_weight(const WeightArgs& a, hipStream_t stream);
+
+struct EvictArgs {
+    const int32_t* tables;  // [S, n]
+    const float* mass;
+    const int32_t* kv_len;  // [S]
+    int32_t* tables_out;
+    float* mass_out;
+    int32_t* kv_len_out;
+    int32_t* evicted;       // [S]
+    void* ws;
+    uint32_t* err;
+    int64_t n, budget;
+    int S, B, first, last;
+};
+size_t evict_workspace_bytes(int64_t n, int64_t S);
+hipError_t launch_evict(const EvictArgs& a, hipStream_t stream);
+
 }  // namespace pred

@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "common.h"
+#include "handle.h"
 #include "kernels.h"
 #include "pred.h"
 
@@ -21,19 +22,11 @@ hipError_t launch_score_prefill(const ScoreArgs& a, hipStream_t stream);
 bool prefill_supported(const ScoreArgs& a);
 }  // namespace pred
 
-struct pred_handle {
-    pred_dims d;
-    int device;
-    int n_cu;          // compute units of that device
-    uint16_t* p_dev;   // [D, R] bf16
-    double* pf_dev;    // [D, R] float64 copy read by the projection kernels
-    uint16_t* ag_dev;  // [L, N, Hk, B, R] bf16
-    uint32_t* err_dev; // device error word
-};
-
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
+
+namespace pred {
 
 int fail(int code, const char* fmt, ...) {
     char buf[2048];
@@ -62,6 +55,16 @@ bool mul_ok(int64_t a, int64_t b, int64_t* out) {
     *out = a * b;
     return true;
 }
+
+}  // namespace pred
+
+using pred::aligned16;
+using pred::fail;
+using pred::hip_fail;
+using pred::mul_ok;
+using pred::ok;
+
+namespace {
 
 // Dims check of PredictorDims::validate (nq a multiple of nkv) plus positivity
 // and overflow of A_g's size.  Returns the A_g byte count or a negative code.
@@ -92,8 +95,6 @@ int check_supported(const pred_dims* d) {
     if (d->head_dim > 65536) return fail(PRED_ERR_UNSUPPORTED, "head_dim (%d) above 65536", d->head_dim);
     return PRED_OK;
 }
-
-bool aligned16(const void* ptr) { return ((uintptr_t)ptr & 15u) == 0; }
 
 // Run-time options, read from the environment once per process:
 //   PRED_SCORE_PATH = auto | decode | generic   which score kernel family every
@@ -656,9 +657,11 @@ int pred_device_error(pred_t* p, void* stream) {
     if (w) {
         e = hipMemset(p->err_dev, 0, 4);
         if (e != hipSuccess) return hip_fail(e, "clear error word");
-        return fail(PRED_ERR_DEVICE, "%s%s(flags 0x%x)",
-                    (w & 1u) ? "a kernel met a block-table entry outside [0, max_blocks) " : "",
-                    (w & 2u) ? "a last-block fill count was outside [0, block_size] " : "", w);
+        return fail(PRED_ERR_DEVICE, "%s%s%s%s(flags 0x%x)",
+                    (w & pred::DEVERR_TABLE) ? "a kernel met a block-table entry outside [0, max_blocks) " : "",
+                    (w & pred::DEVERR_FILL) ? "a last-block fill count was outside [0, block_size] " : "",
+                    (w & pred::DEVERR_SLOT) ? "a cache slot was outside [0, max_blocks * block_size) " : "",
+                    (w & pred::DEVERR_LEN) ? "a sequence or draft length was outside its range " : "", w);
     }
     return ok();
 }
