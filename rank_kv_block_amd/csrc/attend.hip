@@ -106,7 +106,7 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
         }
         if (a.block_lse && lane == 0)
             a.block_lse[(((int64_t)s * a.n + b) * a.M + i) * a.Hq + h] =
-                bl > 0.f || bl != bl ? (bm + log2_of(bl)) * kLn2 : -INFINITY;
+                bl <= 0.f ? -INFINITY : (bm + log2_of(bl)) * kLn2;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[wave][lane + 64 * e] = acc[e];
@@ -129,18 +129,710 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
         a.lse[((int64_t)s * a.M + i) * a.Hq + h] = none ? -INFINITY : (top + log2_of(total)) * kLn2;
 }
 
+// ---------------------------------------------------------------- splitting a context
+//
+// A sequence's tokens are cut into up to `splits` runs, a workgroup for each
+// (sequence, kv head, run); with more than one run in use the workgroups write
+// their unnormalised sums, maximum and total, and a second launch joins them.
+// The number of runs comes from the shape alone (the lengths are on the
+// device); the run's length from the sequence's own length, so that a short
+// sequence in a wide table is spread as well as a long one.
+struct Split {
+    int runs;       // most runs a sequence is cut into
+    int unit;       // a run is a multiple of this many tokens
+};
+
+// Tokens of a run of a sequence of `len` tokens.
+__device__ inline int run_of(const Split& sp, int len) {
+    const int even = (len + sp.runs - 1) / sp.runs;
+    return (even + sp.unit - 1) / sp.unit * sp.unit;
+}
+
+// Partial results: sums [S, Hk, runs, R, D], then (maximum, total) [S, Hk, runs, R].
+__device__ inline float* part_sums(const AttendArgs& a, const Split& sp, int64_t which, int R) {
+    return static_cast<float*>(a.ws) + which * R * a.D;
+}
+__device__ inline float2* part_stats(const AttendArgs& a, const Split& sp, int64_t which, int R) {
+    return reinterpret_cast<float2*>(static_cast<float*>(a.ws) + (int64_t)a.S * a.Hk * sp.runs * R * a.D) + which * R;
+}
+
+// Joins a row's runs: out = sum_r 2^(m_r - m) o_r / sum_r 2^(m_r - m) l_r.  A
+// workgroup per (sequence, row, query head); its threads take every
+// (256 / (D / 4))-th run, 4 values each.  Latency bound: a few hundred KiB.
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Split sp) {
+    __shared__ float4 sums[256];
+    __shared__ float totals[256];
+    const int h = blockIdx.x % a.Hq, i = blockIdx.x / a.Hq % a.M, s = blockIdx.x / a.Hq / a.M;
+    const int len = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B);
+    const int run = run_of(sp, len);
+    if (len <= run) return;     // one run: it wrote the result itself
+    const int runs = (len + run - 1) / run;
+    const int g = a.Hq / a.Hk, R = a.M * g, r = i * g + h % g;
+    const int64_t first = ((int64_t)s * a.Hk + h / g) * sp.runs;
+    const int lanes = a.D / 4, groups = 256 / lanes, group = threadIdx.x / lanes, d4 = threadIdx.x % lanes;
+    float m = kLowest;
+    for (int x = 0; x < runs; ++x) m = fmaxf(m, part_stats(a, sp, first + x, R)[r].x);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int x = group; x < runs; x += groups) {
+        const float2 st = part_stats(a, sp, first + x, R)[r];
+        const float f = exp2_of(st.x - m);
+        const float4 o = reinterpret_cast<const float4*>(part_sums(a, sp, first + x, R) + (int64_t)r * a.D)[d4];
+        l += f * st.y;
+        v.x += f * o.x;
+        v.y += f * o.y;
+        v.z += f * o.z;
+        v.w += f * o.w;
+    }
+    sums[threadIdx.x] = v;
+    totals[threadIdx.x] = l;
+    __syncthreads();
+    if (group != 0) return;
+    for (int x = 1; x < groups; ++x) {
+        const float4 o = sums[x * lanes + d4];
+        l += totals[x * lanes + d4];
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
+    }
+    const bool none = l == 0.f;
+    const float f = none ? 0.f : a.cache.v_scale / l;
+    const int64_t row = ((int64_t)s * a.M + i) * a.Hq + h;
+    uint16_t w[4] = {to_bf16(none ? 0.f : v.x * f), to_bf16(none ? 0.f : v.y * f), to_bf16(none ? 0.f : v.z * f),
+                     to_bf16(none ? 0.f : v.w * f)};
+    *reinterpret_cast<uint2*>(a.out + row * a.D + 4 * d4) = *reinterpret_cast<uint2*>(w);
+    if (a.lse && d4 == 0) a.lse[row] = none ? -INFINITY : (m + log2_of(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------- stream kernel
+//
+// Up to 32 queries per kv head (a token, or a small draft): HBM bound, every
+// key and value read once.  Each of a workgroup's four waves works alone on
+// every fourth tile of 32 tokens, from loads to sums, with no LDS and no
+// barrier, and the waves' sums meet at the end.
+//
+// A wave-load takes 1 KiB, whole rows of TPL tokens (row = a token's head, RB
+// bytes).  Both products run on v_mfma_f32_16x16x32_bf16, queries as the second
+// operand (column n = lane % 16 of both results is query n, c = lane / 16):
+//   scores  row m of the first operand is (token m / H, part m % H) of a load,
+//           H = RB / 64: lane (m, c) holds 16 bytes, piece 4 (m % H) + c of
+//           token m / H, so the wave-load is contiguous.  MFMA j multiplies
+//           by part j of the queries; of its 16 results rows with m % H = j
+//           count, and lane (n, c) keeps tokens W c .. W c + W - 1 of the load,
+//           W = TPL / 4.
+//   values  the tokens a lane holds scores for are its 8 places of the sum, so
+//           the weights go into the second operand as they are.  The first
+//           operand wants 8 tokens' values of one d in a lane: lane (p, c)
+//           loads values J p .. J p + J - 1 (J = D / 16) of those 8 tokens, an
+//           8 x J matrix that it transposes in registers with byte permutes.
+//           Tile j is then d = J p + j, and lane (n, c) ends with d = J (4 c +
+//           v) + j, J values side by side.
+// The weights enter as two bf16 terms (value and rest), so an output carries
+// about 16 bits of them; the matrix units are idle either way.
+//
+// The running maximum moves only when a tile exceeds it by 2^8 (every weight is
+// then at most 2^8, exact in float32 sums), so most tiles need no exchange
+// between lanes.
+template <int D_, bool FP8_>
+struct StreamLayout {
+    static constexpr int D = D_;
+    static constexpr bool FP8 = FP8_;
+    static constexpr int RB = D * (FP8 ? 1 : 2);    // bytes of a row
+    static constexpr int TPL = 1024 / RB;           // tokens of a wave-load
+    static constexpr int NK = 32 / TPL;             // key loads of a tile
+    static constexpr int W = TPL / 4;               // tokens a lane scores per load
+    static constexpr int H = RB / 64;               // 64-byte parts of a row
+    static constexpr int KP = FP8 ? 2 : 1;          // products of 32 values per part
+    static constexpr int J = D / 16;                // values a lane holds of a token
+    static constexpr int VW = RB / 64;              // 4-byte words of them as stored
+};
+
+// max / sum over the four lanes (n, 0..3) of a query
+__device__ inline float max_over_c(float x) {
+    auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ inline float sum_over_c(float x) {
+    auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+// two e4m3 values (bytes 0, 1 or 2, 3 of w) as two bf16, exact
+template <bool HI>
+__device__ inline uint32_t fp8x2_to_bf16(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI));
+}
+
+__device__ inline uint32_t bf16_pair(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){lo, hi}, bf16x2_t));
+}
+
+// whether either half of w is an infinity or a NaN
+__device__ inline bool not_finite(uint32_t w) {
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// The blocks of one sequence as a wave walks it: 64 table entries at a time in
+// a register, a lane each.
+struct TableWindow {
+    const int32_t* row;     // null: the identity
+    int n, first, entries;
+
+    __device__ inline void load(const AttendArgs& a, int block, int lane) {
+        first = block;
+        entries = block + lane;
+        if (row && block + lane < n) entries = row[block + lane];
+    }
+    __device__ inline int at(int block) const { return __builtin_amdgcn_readlane(entries, block - first); }
+};
+
+// B a power of two: shift >= 0.
+struct BlockSize {
+    int B, shift;
+    __device__ inline int block(int t) const { return shift >= 0 ? t >> shift : (int)((uint32_t)t / (uint32_t)B); }
+};
+
+// aux bits of the streamed loads: 2 = nontemporal (each byte is read once)
+constexpr int kStreamAux = 2;
+
+template <int BYTES>
+__device__ inline void buffer_load(uint32_t* dst, __amdgpu_buffer_rsrc_t r, int off) {
+    if constexpr (BYTES == 16) {
+        const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kStreamAux));
+        dst[0] = x[0];
+        dst[1] = x[1];
+        dst[2] = x[2];
+        dst[3] = x[3];
+    } else if constexpr (BYTES == 8) {
+        typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+        const u32x2_t x = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, kStreamAux));
+        dst[0] = x[0];
+        dst[1] = x[1];
+    } else {
+        dst[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, kStreamAux);
+    }
+}
+
+template <int D, bool FP8, int RT>
+__global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(AttendArgs a, Split sp, BlockSize bs) {
+    using L = StreamLayout<D, FP8>;
+    constexpr int NK = L::NK, W = L::W, H = L::H, KP = L::KP, J = L::J, TPL = L::TPL, VW = L::VW;
+    __shared__ float exchange[2][(RT * J * 4 + 2 * RT) * 64];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, c = lane >> 4;
+    const int kvh = blockIdx.x % a.Hk;
+    const int split = blockIdx.x / a.Hk % sp.runs, s = blockIdx.x / a.Hk / sp.runs;
+    const int len = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B), drafted = draft_len_of(a, s, len);
+    if (kvh == 0 && split == 0 && threadIdx.x == 0) check_lengths(a, s, len, drafted);
+    const int ctx = len - drafted;
+    const int run = run_of(sp, len);
+    const int t0 = split * run;
+    if (t0 >= len && split > 0) return;
+    const int t1 = t0 + run < len ? t0 + run : len;
+    const int g = a.Hq / a.Hk, R = a.M * g;
+
+    // queries, as second operands
+    bf16x8_t q[RT][H][KP];
+    uint64_t seen[RT];
+    bool live[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = rt * 16 + n, i = r / g;
+        live[rt] = r < R && i < drafted;
+        seen[rt] = live[rt] ? tree_word(a, s, i) : 0;
+        const uint16_t* row = a.q + (((int64_t)s * a.M + i) * a.Hq + kvh * g + r % g) * D;
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+                // a row that is not live weighs nothing: zeros, whatever it holds
+                q[rt][j][k] = bf16x8_t{};
+                if (live[rt]) q[rt][j][k] = load8(row + 8 * KP * (4 * j + c) + 8 * k);
+            }
+    }
+
+    const int64_t item = FP8 ? 1 : 2;
+    const int ts = (int)(a.cache.token_stride * item);
+    const int64_t block_bytes = a.cache.block_stride * item, head_off = kvh * a.cache.head_stride * item;
+    const char* const kp = static_cast<const char*>(a.cache.k) + head_off;
+    const char* const vp = static_cast<const char*>(a.cache.v) + head_off;
+    const int k_off = n / H * ts + 16 * (4 * (n % H) + c);
+    int v_off[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) v_off[w] = (W * c + w) * ts + n * (VW * 4);
+
+    TableWindow table;
+    table.row = a.tables ? a.tables + (int64_t)s * a.n : nullptr;
+    table.n = a.n;
+    table.first = 1 << 30;      // no entries yet
+    table.entries = 0;
+
+    // this wave's tiles: groups of `per` consecutive ones, every fourth group
+    const int per = sp.unit / 128;
+    auto tile_of = [&](int k) { return t0 + 32 * ((k / per * 4 + wave) * per + k % per); };
+
+    uint32_t kr[NK][4], vr[8][VW];
+    // Loads u's base and extent: tokens tok .. tok + TPL - 1, all of one block.  Tokens at or past the run's end
+    // and blocks with an invalid entry get an extent that ends before them, and read as zeros.
+    struct Place {
+        int64_t off;
+        int extent;
+    };
+    auto place_of = [&](int tok) {
+        Place r{0, 0};
+        if (tok < t1) {
+            const int b = bs.block(tok);
+            const int slot = table.at(b);
+            const int left = t1 - tok < TPL ? t1 - tok : TPL;
+            if (slot >= 0 && slot < a.N) {
+                r.off = slot * block_bytes + (int64_t)(tok - b * bs.B) * ts;
+                r.extent = (left - 1) * ts + L::RB;
+            }
+        }
+        return r;
+    };
+    auto window_for = [&](int t) {
+        if (t < t1) {
+            const int first = bs.block(t), last = bs.block(t + 31 < t1 ? t + 31 : t1 - 1);
+            if (first < table.first || last >= table.first + 64) table.load(a, first, lane);
+        }
+    };
+    auto load_k = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < NK; ++u) {
+            const Place pl = place_of(t + TPL * u);
+            buffer_load<16>(kr[u], __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(kp + pl.off), (short)0,
+                                                                     pl.extent, 0x00020000), k_off);
+        }
+    };
+    auto load_v = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < NK; ++u) {
+            const Place pl = place_of(t + TPL * u);
+            const __amdgpu_buffer_rsrc_t rsrc =
+                __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(vp + pl.off), (short)0, pl.extent, 0x00020000);
+#pragma unroll
+            for (int w = 0; w < W; ++w) buffer_load<VW * 4>(vr[u * W + w], rsrc, v_off[w]);
+        }
+    };
+
+    f32x4_t o[RT][J];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = kLowest;
+        l[rt] = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) o[rt][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    // block_lse of a block wider than a tile: its maximum and sum so far
+    float wide_m[RT], wide_l[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        wide_m[rt] = kLowest;
+        wide_l[rt] = 0.f;
+    }
+    const float scale = a.scale * a.cache.k_scale * kLog2e;
+
+    int t = tile_of(0);
+    window_for(t);
+    load_k(t);
+    load_v(t);
+    for (int k = 0; t < t1; ++k) {
+        const int next = tile_of(k + 1);
+        // scores of this tile's 32 tokens, in units of log2
+        float x[RT][8];
+#pragma unroll
+        for (int u = 0; u < NK; ++u) {
+            bf16x8_t key[KP];
+            if constexpr (FP8) {
+                key[0] = __builtin_bit_cast(bf16x8_t, (u32x4_t){fp8x2_to_bf16<false>(kr[u][0]), fp8x2_to_bf16<true>(kr[u][0]),
+                                                                fp8x2_to_bf16<false>(kr[u][1]), fp8x2_to_bf16<true>(kr[u][1])});
+                key[KP - 1] = __builtin_bit_cast(bf16x8_t, (u32x4_t){fp8x2_to_bf16<false>(kr[u][2]), fp8x2_to_bf16<true>(kr[u][2]),
+                                                                     fp8x2_to_bf16<false>(kr[u][3]), fp8x2_to_bf16<true>(kr[u][3])});
+            } else {
+                key[0] = __builtin_bit_cast(bf16x8_t, (u32x4_t){kr[u][0], kr[u][1], kr[u][2], kr[u][3]});
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                f32x4_t part[H];
+#pragma unroll
+                for (int j = 0; j < H; ++j) {
+                    part[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int kk = 0; kk < KP; ++kk)
+                        part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key[kk], q[rt][j][kk], part[j], 0, 0, 0);
+                }
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    float sum = part[0][w * H];
+#pragma unroll
+                    for (int j = 1; j < H; ++j) sum += part[j][w * H + j];
+                    x[rt][u * W + w] = sum * scale;
+                }
+            }
+        }
+        // which loads of this tile have an invalid table entry (before the window moves on)
+        uint32_t dead = 0;
+#pragma unroll
+        for (int u = 0; u < NK; ++u)
+            if (t + TPL * u < t1) {
+                const int slot = table.at(bs.block(t + TPL * u));
+                if (slot < 0 || slot >= a.N) dead |= 1u << u;
+            }
+        const bool masked = t + 32 > ctx || t + 32 > t1 || dead != 0;
+        // the next tile's window may replace this one's: this tile's values are already on their way
+        window_for(next);
+        load_k(next);
+
+        if (masked) {
+            if (dead && lane == 0) atomicOr(a.err, DEVERR_TABLE);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int u = e / W, tok = t + TPL * u + W * c + e % W;
+                const bool there = tok < t1 && !((dead >> u) & 1);
+                const int at = tok - ctx;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const bool sees = there && (at < 0 || ((seen[rt] >> (at & 63)) & 1));
+                    x[rt][e] = sees ? x[rt][e] : -INFINITY;
+                }
+            }
+        }
+
+        // the running maximum
+        float top[RT];
+        bool above = false;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            top[rt] = x[rt][0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) top[rt] = fmaxf(top[rt], x[rt][e]);
+            above |= top[rt] > m[rt] + 8.f;
+        }
+        if (__ballot(above)) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const float m_new = fmaxf(m[rt], max_over_c(top[rt]));
+                const float alpha = exp2_of(m[rt] - m_new);
+                m[rt] = m_new;
+                l[rt] *= alpha;
+#pragma unroll
+                for (int j = 0; j < J; ++j) o[rt][j] *= alpha;
+            }
+        }
+
+        if (a.block_lse) {
+            // blocks of 8 or 16 tokens lie side by side in a tile: places (32 / B) of the 8 each; one of 32 or more
+            // fills it
+            const int parts = bs.B >= 32 ? 1 : 32 / bs.B;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const int r = rt * 16 + n;
+                float bm[4], bl[4];
+                // the maximum of each pair of places, then of what a block covers
+                float pm[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) pm[y] = fmaxf(x[rt][2 * y], x[rt][2 * y + 1]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    float top_y = pm[y];
+                    if (parts <= 2) top_y = fmaxf(top_y, pm[y ^ 1]);
+                    if (parts == 1) top_y = fmaxf(top_y, fmaxf(pm[y ^ 2], pm[y ^ 3]));
+                    bm[y] = fmaxf(max_over_c(top_y), kLowest);
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    pm[y] = exp2_of(x[rt][2 * y] - bm[y]) + exp2_of(x[rt][2 * y + 1] - bm[y]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    float sum = pm[y];
+                    if (parts <= 2) sum += pm[y ^ 1];
+                    if (parts == 1) sum += pm[y ^ 2] + pm[y ^ 3];
+                    bl[y] = sum_over_c(sum);
+                }
+                const int i = r / g;
+                float* const to = a.block_lse + ((int64_t)s * a.n * a.M + i) * a.Hq + kvh * g + r % g;
+                const int64_t step = (int64_t)a.M * a.Hq;
+                if (parts > 1) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        // lane group c writes the block that its c-th pair of places belongs to
+                        const int tok = t + 8 * y;
+                        const bool mine = parts == 4 ? c == y : (y % 2 == 0 && c == y);
+                        if (mine && r < R && tok < t1)
+                            to[bs.block(tok) * step] =
+                                live[rt] && !(bl[y] <= 0.f) ? (bm[y] + log2_of(bl[y])) * kLn2 : -INFINITY;
+                    }
+                } else {
+                    const float top_m = fmaxf(wide_m[rt], bm[0]);
+                    wide_l[rt] = wide_l[rt] * exp2_of(wide_m[rt] - top_m) + bl[0] * exp2_of(bm[0] - top_m);
+                    wide_m[rt] = top_m;
+                    // the block's last tile, or the sequence's
+                    if (t + 32 >= t1 || (t + 32) % bs.B == 0) {
+                        const float w = wide_l[rt];
+                        if (c == 0 && r < R)
+                            to[bs.block(t) * step] = live[rt] && !(w <= 0.f) ? (wide_m[rt] + log2_of(w)) * kLn2 : -INFINITY;
+                        wide_m[rt] = kLowest;
+                        wide_l[rt] = 0.f;
+                    }
+                }
+            }
+        }
+
+        bf16x8_t hi[RT], lo[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            u32x4_t wh, wl;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[rt][e] = exp2_of(x[rt][e] - m[rt]);
+                l[rt] += x[rt][e];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                wh[e] = bf16_pair(x[rt][2 * e], x[rt][2 * e + 1]);
+                wl[e] = bf16_pair(x[rt][2 * e] - bf16_lo(wh[e]), x[rt][2 * e + 1] - bf16_hi(wh[e]));
+            }
+            hi[rt] = __builtin_bit_cast(bf16x8_t, wh);
+            lo[rt] = __builtin_bit_cast(bf16x8_t, wl);
+        }
+
+        // values as bf16 words, J / 2 of each token
+        uint32_t vw[8][J / 2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (FP8) {
+#pragma unroll
+                for (int y = 0; y < VW; ++y) {
+                    vw[e][2 * y] = fp8x2_to_bf16<false>(vr[e][y]);
+                    vw[e][2 * y + 1] = fp8x2_to_bf16<true>(vr[e][y]);
+                }
+            } else {
+#pragma unroll
+                for (int y = 0; y < VW; ++y) vw[e][y] = vr[e][y];
+            }
+        }
+        bool odd = false;       // a drafted token's value that is not finite: it must not meet the zero weights of others
+        if (masked && a.M > 1 && t + 32 > ctx) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int y = 0; y < J / 2; ++y) odd |= not_finite(vw[e][y]);
+        }
+        if (__ballot(odd) == 0) {
+#pragma unroll
+            for (int y = 0; y < J / 2; ++y) {
+                u32x4_t even, uneven;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    even[e] = __builtin_amdgcn_perm(vw[2 * e + 1][y], vw[2 * e][y], 0x05040100);
+                    uneven[e] = __builtin_amdgcn_perm(vw[2 * e + 1][y], vw[2 * e][y], 0x07060302);
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    o[rt][2 * y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, even), hi[rt],
+                                                                          o[rt][2 * y], 0, 0, 0);
+                    o[rt][2 * y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, even), lo[rt],
+                                                                          o[rt][2 * y], 0, 0, 0);
+                    o[rt][2 * y + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, uneven),
+                                                                              hi[rt], o[rt][2 * y + 1], 0, 0, 0);
+                    o[rt][2 * y + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, uneven),
+                                                                              lo[rt], o[rt][2 * y + 1], 0, 0, 0);
+                }
+            }
+        } else {
+            // token by token, adding only where a row's weight is not 0 (rare: no loop unrolling)
+            for (int from = 0; from < 4; ++from) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float w[RT];
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) w[rt] = __shfl(x[rt][e], n + 16 * from);
+#pragma unroll
+                    for (int y = 0; y < J / 2; ++y)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const uint32_t word = __shfl(vw[e][y], 4 * c + v + 16 * from);
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) {
+                                if (w[rt] != 0.f) {
+                                    o[rt][2 * y][v] += w[rt] * bf16_lo(word);
+                                    o[rt][2 * y + 1][v] += w[rt] * bf16_hi(word);
+                                }
+                            }
+                        }
+                }
+            }
+        }
+        load_v(next);
+        t = next;
+    }
+
+    // the waves' sums: 2 and 3 into 0 and 1, then 1 into 0
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) l[rt] = sum_over_c(l[rt]);
+#pragma unroll
+    for (int round = 2; round >= 1; round >>= 1) {
+        if (wave >= round && wave < 2 * round) {
+            float* const to = exchange[wave - round];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                to[(RT * J * 4 + 2 * rt) * 64 + lane] = m[rt];
+                to[(RT * J * 4 + 2 * rt + 1) * 64 + lane] = l[rt];
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) to[((rt * J + j) * 4 + v) * 64 + lane] = o[rt][j][v];
+            }
+        }
+        __syncthreads();
+        if (wave < round) {
+            const float* const from = exchange[wave];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const float m_other = from[(RT * J * 4 + 2 * rt) * 64 + lane];
+                const float m_new = fmaxf(m[rt], m_other);
+                const float f = exp2_of(m[rt] - m_new), f_other = exp2_of(m_other - m_new);
+                l[rt] = l[rt] * f + from[(RT * J * 4 + 2 * rt + 1) * 64 + lane] * f_other;
+                m[rt] = m_new;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        o[rt][j][v] = o[rt][j][v] * f + from[((rt * J + j) * 4 + v) * 64 + lane] * f_other;
+            }
+        }
+        __syncthreads();
+    }
+    if (wave != 0) return;
+    const bool whole = run >= len;      // no other run: the result
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int r = rt * 16 + n;
+        if (r >= R) continue;
+        const int64_t row = ((int64_t)s * a.M + r / g) * a.Hq + kvh * g + r % g;
+        const bool none = !live[rt] || l[rt] == 0.f;
+        if (whole) {
+            const float f = none ? 0.f : a.cache.v_scale / l[rt];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                uint32_t w[J / 2];
+#pragma unroll
+                for (int y = 0; y < J / 2; ++y)
+                    w[y] = none ? 0u : bf16_pair(o[rt][2 * y][v] * f, o[rt][2 * y + 1][v] * f);
+                uint32_t* const to = reinterpret_cast<uint32_t*>(a.out + row * D + J * (4 * c + v));
+#pragma unroll
+                for (int y = 0; y < J / 2; ++y) to[y] = w[y];
+            }
+            if (a.lse && c == 0) a.lse[row] = none ? -INFINITY : (m[rt] + log2_of(l[rt])) * kLn2;
+        } else {
+            const int64_t which = ((int64_t)s * a.Hk + kvh) * sp.runs + split;
+            float* const to = part_sums(a, sp, which, R) + (int64_t)r * D;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int y = 0; y < J / 4; ++y)
+                    *reinterpret_cast<float4*>(to + J * (4 * c + v) + 4 * y) =
+                        make_float4(none ? 0.f : o[rt][4 * y][v], none ? 0.f : o[rt][4 * y + 1][v],
+                                    none ? 0.f : o[rt][4 * y + 2][v], none ? 0.f : o[rt][4 * y + 3][v]);
+            if (c == 0) part_stats(a, sp, which, R)[r] = make_float2(none ? kLowest : m[rt], none ? 0.f : l[rt]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- choice of a kernel
+
+enum class Kind { Stream, Plain };
+
+Kind kind_of(const AttendArgs& a) {
+    const int R = a.M * (a.Hq / a.Hk);
+    const int item = a.cache.fp8 ? 1 : 2;
+    if (a.D != 64 && a.D != 128) return Kind::Plain;
+    // a wave-load's tokens lie in one block
+    const int tpl = 1024 / (a.D * item);
+    if (a.B % tpl != 0) return Kind::Plain;
+    // a block's sum is taken inside a tile, or over whole tiles
+    if (a.block_lse && !(a.B % 32 == 0 || a.B == 16 || a.B == 8)) return Kind::Plain;
+    // 16-byte loads, and 32-bit offsets inside a wave-load
+    if (!aligned_to(a.cache.k, 16) || !aligned_to(a.cache.v, 16) ||
+        ((a.cache.block_stride | a.cache.token_stride | a.cache.head_stride) * item) % 16 != 0)
+        return Kind::Plain;
+    if (a.cache.token_stride > (1 << 24)) return Kind::Plain;
+    return R <= 32 ? Kind::Stream : Kind::Plain;
+}
+
+Split split_of(const AttendArgs& a, bool with_block_lse) {
+    const int64_t base = (int64_t)a.S * a.Hk, most = (int64_t)a.n * a.B;
+    Split sp;
+    // four waves take tiles, or whole blocks where a block's sum spans tiles
+    sp.unit = with_block_lse && a.B > 32 ? 4 * a.B : 128;
+    // enough workgroups for three on every CU, and runs short enough to even out sequences of different lengths
+    int64_t runs = (3 * (int64_t)a.n_cu + base - 1) / base;
+    const int64_t even = most / 4096;
+    if (runs < even) runs = even;
+    const int64_t limit = (most + sp.unit - 1) / sp.unit;
+    if (runs > limit) runs = limit;
+    sp.runs = runs < 1 ? 1 : (int)runs;
+    return sp;
+}
+
+int log2_or_negative(int x) {
+    for (int i = 0; i < 31; ++i)
+        if (x == 1 << i) return i;
+    return -1;
+}
+
+template <int D, bool FP8>
+hipError_t launch_stream(const AttendArgs& a, const Split& sp, hipStream_t stream) {
+    const uint32_t grid = (uint32_t)((int64_t)a.S * a.Hk * sp.runs);
+    const BlockSize bs{a.B, log2_or_negative(a.B)};
+    if (a.M * (a.Hq / a.Hk) <= 16) attend_stream_kernel<D, FP8, 1><<<grid, 256, 0, stream>>>(a, sp, bs);
+    else attend_stream_kernel<D, FP8, 2><<<grid, 256, 0, stream>>>(a, sp, bs);
+    return hipGetLastError();
+}
+
 }  // namespace
 
-size_t attend_workspace_bytes(const AttendArgs&) { return 0; }
+size_t attend_workspace_bytes(const AttendArgs& a) {
+    if (a.D != 64 && a.D != 128) return 0;
+    const int R = a.M * (a.Hq / a.Hk);
+    if (R > 32) return 0;
+    // the number of runs without block_lse is the larger
+    const Split sp = split_of(a, false);
+    return sp.runs <= 1 ? 0 : (size_t)a.S * a.Hk * sp.runs * R * (a.D + 2) * sizeof(float);
+}
 
-const char* attend_kernel_name(const AttendArgs&) { return "attend_plain_kernel"; }
+const char* attend_kernel_name(const AttendArgs& a) {
+    return kind_of(a) == Kind::Stream ? "attend_stream_kernel" : "attend_plain_kernel";
+}
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
-    const int64_t groups = (int64_t)a.S * a.M;
-    if (groups > 0x7FFFFFFF / a.Hq) return hipErrorInvalidConfiguration;
-    const uint32_t grid = (uint32_t)(groups * a.Hq);
-    if (a.cache.fp8) attend_plain_kernel<true><<<grid, 256, 0, stream>>>(a);
-    else attend_plain_kernel<false><<<grid, 256, 0, stream>>>(a);
+    const int64_t rows = (int64_t)a.S * a.M;
+    if (rows > 0x7FFFFFFF / a.Hq) return hipErrorInvalidConfiguration;
+    const uint32_t row_grid = (uint32_t)(rows * a.Hq);
+    const Kind kind = kind_of(a);
+    if (kind == Kind::Plain) {
+        if (a.cache.fp8) attend_plain_kernel<true><<<row_grid, 256, 0, stream>>>(a);
+        else attend_plain_kernel<false><<<row_grid, 256, 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    const Split sp = split_of(a, a.block_lse != nullptr);
+    if (!grid_fits((int64_t)a.S * a.Hk * sp.runs)) return hipErrorInvalidConfiguration;
+    hipError_t e;
+    if (a.D == 64) e = a.cache.fp8 ? launch_stream<64, true>(a, sp, stream) : launch_stream<64, false>(a, sp, stream);
+    else e = a.cache.fp8 ? launch_stream<128, true>(a, sp, stream) : launch_stream<128, false>(a, sp, stream);
+    if (e != hipSuccess || sp.runs <= 1) return e;
+    attend_join_kernel<<<row_grid, 256, 0, stream>>>(a, sp);
     return hipGetLastError();
 }
 
