@@ -166,7 +166,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Split sp
     const int len = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B);
     const int run = run_of(sp, len);
     if (len <= run) return;     // one run: it wrote the result itself
-    const int runs = (len + run - 1) / run;
+    // a row past the draft has no partial sums: its result is that of no run
+    const int runs = i < draft_len_of(a, s, len) ? (len + run - 1) / run : 0;
     const int g = a.Hq / a.Hk, R = a.M * g, r = i * g + h % g;
     const int64_t first = ((int64_t)s * a.Hk + h / g) * sp.runs;
     const int lanes = a.D / 4, groups = 256 / lanes, group = threadIdx.x / lanes, d4 = threadIdx.x % lanes;
@@ -278,6 +279,31 @@ __device__ inline uint32_t bf16_pair(float lo, float hi) {
 // whether either half of w is an infinity or a NaN
 __device__ inline bool not_finite(uint32_t w) {
     return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// w with its halves that are not finite set to 0
+__device__ inline uint32_t finite_only(uint32_t w) {
+    return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
+}
+
+// A masked weight is 0, and 0 times a value that is not finite would be NaN in
+// the matrix cores.  So where a drafted token's values hold any, the product
+// runs over the finite ones, and three more products of indicators count, for
+// each result, the NaN, +inf and -inf values of weight above 0 (kinds 0, 1, 2).
+__device__ inline uint32_t indicator(uint32_t w, int kind) {
+    auto hit = [&](uint32_t h) {
+        return kind == 0 ? (h & 0x7FFFu) > 0x7F80u : (kind == 1 ? h == 0x7F80u : h == 0xFF80u);
+    };
+    return (hit(w & 0xFFFFu) ? 0x3F80u : 0u) | (hit(w >> 16) ? 0x3F800000u : 0u);
+}
+__device__ inline float special(int kind) { return kind == 0 ? NAN : (kind == 1 ? INFINITY : -INFINITY); }
+
+// weights as a second operand of ones where they are not 0
+__device__ inline bf16x8_t ones_of(const float* x) {
+    u32x4_t w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = (x[2 * e] != 0.f ? 0x3F80u : 0u) | (x[2 * e + 1] != 0.f ? 0x3F800000u : 0u);
+    return __builtin_bit_cast(bf16x8_t, w);
 }
 
 // The blocks of one sequence as a wave walks it: 64 table entries at a time in
@@ -629,48 +655,51 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
 #pragma unroll
                 for (int y = 0; y < J / 2; ++y) odd |= not_finite(vw[e][y]);
         }
-        if (__ballot(odd) == 0) {
+        // first operands of d = J p + 2 y and J p + 2 y + 1
+        auto transposed = [&](int y, u32x4_t& even, u32x4_t& uneven) {
 #pragma unroll
-            for (int y = 0; y < J / 2; ++y) {
-                u32x4_t even, uneven;
+            for (int e = 0; e < 4; ++e) {
+                even[e] = __builtin_amdgcn_perm(vw[2 * e + 1][y], vw[2 * e][y], 0x05040100);
+                uneven[e] = __builtin_amdgcn_perm(vw[2 * e + 1][y], vw[2 * e][y], 0x07060302);
+            }
+        };
+        if (__ballot(odd)) {
+#pragma unroll 1
+            for (int kind = 0; kind < 3; ++kind)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    even[e] = __builtin_amdgcn_perm(vw[2 * e + 1][y], vw[2 * e][y], 0x05040100);
-                    uneven[e] = __builtin_amdgcn_perm(vw[2 * e + 1][y], vw[2 * e][y], 0x07060302);
+                for (int y = 0; y < J / 2; ++y) {
+                    u32x4_t w[2];
+                    transposed(y, w[0], w[1]);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[z][e] = indicator(w[z][e], kind);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) {
+                            const f32x4_t count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8_t, w[z]), ones_of(x[rt]), f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) o[rt][2 * y + z][v] += count[v] > 0.f ? special(kind) : 0.f;
+                        }
+                    }
                 }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int y = 0; y < J / 2; ++y) vw[e][y] = finite_only(vw[e][y]);
+        }
+#pragma unroll
+        for (int y = 0; y < J / 2; ++y) {
+            u32x4_t w[2];
+            transposed(y, w[0], w[1]);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const bf16x8_t val = __builtin_bit_cast(bf16x8_t, w[z]);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    o[rt][2 * y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, even), hi[rt],
-                                                                          o[rt][2 * y], 0, 0, 0);
-                    o[rt][2 * y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, even), lo[rt],
-                                                                          o[rt][2 * y], 0, 0, 0);
-                    o[rt][2 * y + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, uneven),
-                                                                              hi[rt], o[rt][2 * y + 1], 0, 0, 0);
-                    o[rt][2 * y + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, uneven),
-                                                                              lo[rt], o[rt][2 * y + 1], 0, 0, 0);
-                }
-            }
-        } else {
-            // token by token, adding only where a row's weight is not 0 (rare: no loop unrolling)
-            for (int from = 0; from < 4; ++from) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float w[RT];
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) w[rt] = __shfl(x[rt][e], n + 16 * from);
-#pragma unroll
-                    for (int y = 0; y < J / 2; ++y)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const uint32_t word = __shfl(vw[e][y], 4 * c + v + 16 * from);
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt) {
-                                if (w[rt] != 0.f) {
-                                    o[rt][2 * y][v] += w[rt] * bf16_lo(word);
-                                    o[rt][2 * y + 1][v] += w[rt] * bf16_hi(word);
-                                }
-                            }
-                        }
+                    f32x4_t& to = o[rt][2 * y + z];
+                    to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, hi[rt], to, 0, 0, 0);
+                    to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, lo[rt], to, 0, 0, 0);
                 }
             }
         }
@@ -750,34 +779,482 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
     }
 }
 
+// ---------------------------------------------------------------- tree kernel
+//
+// More than 32 queries per kv head (a draft tree): a workgroup's four waves
+// share tiles of 64 tokens, staged through LDS as bf16 (an FP8 cache is
+// converted on the way), each wave with 32 queries of its own (WK = 1), or two
+// waves with the same 32 queries and half of each tile (WK = 2, up to 64
+// queries).  The stage is double buffered and filled through registers: a
+// tile's loads are issued before the previous tile is computed.
+//
+// Both products run on v_mfma_f32_32x32x16_bf16 with the queries as the second
+// operand, so lane (n = lane % 32, f = lane / 32) owns query n: it holds the
+// scores of tokens v % 4 + 8 (v / 4) + 4 f, v = 0 .. 15, of 32, and its 16
+// weights go into the second operand of the value product as they stand, 8 to
+// a product.  The first operand of that product wants, for the same tokens, 4
+// consecutive tokens' values of one d in a lane: the LDS transpose read gives a
+// group of 16 lanes the 4 x 16 block whose rows its lanes point at.  A softmax
+// reduction crosses lanes once (n and n + 32).
+//
+// LDS rows are 2 D bytes without padding; their 16-byte pieces are permuted by
+// the row so that the 16 rows of a key read, and the 4 rows of a transpose read,
+// fall on different banks.
+//
+// Bound: at 512 queries per kv head the matrix cores (4 flops a byte and query);
+// the weights' second bf16 term makes the value product twice as long.
+template <int D>
+struct TreeLds {
+    static constexpr int kRow = 2 * D;              // bytes of a row
+    static constexpr int kPieces = kRow / 16;
+    static constexpr int kTile = 64 * kRow;
+    // byte offset of 16-byte piece `piece` of row `row`
+    __device__ static inline int key(int row, int piece) {
+        return row * kRow + 16 * (piece ^ (D == 128 ? row & 15 : (row >> 1) & 7));
+    }
+    __device__ static inline int value(int row, int piece) {
+        return row * kRow + 16 * (piece ^ (D == 128 ? (row & 3) * 4 : ((row >> 1) & 1) * 4));
+    }
+};
+
+// max / sum over the two lanes of a query
+__device__ inline float max_over_f(float x) {
+    auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ inline float sum_over_f(float x) {
+    auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+
+// Which (sequence, kv head, run, row group) a workgroup takes: a cache region's
+// row groups are 8 workgroups apart, so they share an XCD's L2.
+struct TreePlace {
+    int s, kvh, split, group;
+};
+__device__ inline TreePlace tree_place(const AttendArgs& a, const Split& sp, int groups) {
+    const uint32_t chunk = blockIdx.x / (8u * groups), in = blockIdx.x % (8u * groups);
+    const int64_t which = (int64_t)chunk * 8 + in % 8;
+    TreePlace r;
+    r.group = in / 8;
+    r.kvh = (int)(which % a.Hk);
+    r.split = (int)(which / a.Hk % sp.runs);
+    r.s = (int)(which / a.Hk / sp.runs);
+    return r;
+}
+
+template <int D, bool FP8, int WK>
+__global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split sp, BlockSize bs, int groups) {
+    using T = TreeLds<D>;
+    constexpr int RB = D * (FP8 ? 1 : 2);       // bytes of a cache row
+    constexpr int CR = RB / 16;                 // 16-byte pieces of it
+    constexpr int NR = 64 * CR / 256;           // pieces a thread stages, of keys and of values
+    constexpr int KS = D / 16, DT = D / 32;
+    constexpr int kRowWaves = 4 / WK;
+    __shared__ __attribute__((aligned(16))) char lds[4 * T::kTile];     // keys 0, keys 1, values 0, values 1
+
+    const TreePlace at = tree_place(a, sp, groups);
+    if (at.s >= a.S) return;
+    const int s = at.s, kvh = at.kvh;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 31, f = lane >> 5;
+    const int len = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B), drafted = draft_len_of(a, s, len);
+    if (kvh == 0 && at.split == 0 && at.group == 0 && threadIdx.x == 0) check_lengths(a, s, len, drafted);
+    const int ctx = len - drafted;
+    const int run = run_of(sp, len);
+    const int t0 = at.split * run;
+    if (t0 >= len && at.split > 0) return;
+    const int t1 = t0 + run < len ? t0 + run : len;
+    const int g = a.Hq / a.Hk, R = a.M * g;
+    const int r0 = (at.group * kRowWaves + wave / WK) * 32, r = r0 + n, i = r / g;
+    const bool live = r < R && i < drafted;
+    const bool wave_live = r0 < R && r0 / g < drafted;          // rows of a wave die from the end
+    const bool group_live = at.group * kRowWaves * 32 / g < drafted;
+    const uint64_t seen = live ? tree_word(a, s, i) : 0;
+    float* const block_row =
+        a.block_lse ? a.block_lse + ((int64_t)s * a.n * a.M + i) * a.Hq + kvh * g + r % g : nullptr;
+    const int64_t block_step = (int64_t)a.M * a.Hq;
+    const bool whole = run >= len;
+    const int64_t row = ((int64_t)s * a.M + i) * a.Hq + kvh * g + r % g;
+
+    if (!group_live) {      // nothing but the empty rows' results
+        if (r >= R || (WK == 2 && wave % 2)) return;
+        if (a.block_lse)
+            for (int b = bs.block(t0) + f; b <= (t1 > t0 ? bs.block(t1 - 1) : -1); b += 2)
+                block_row[b * block_step] = -INFINITY;
+        if (whole) {
+            for (int d = 8 * f; d < D; d += 16) *reinterpret_cast<u32x4_t*>(a.out + row * D + d) = u32x4_t{0, 0, 0, 0};
+            if (a.lse && f == 0) a.lse[row] = -INFINITY;
+        }
+        return;
+    }
+
+    bf16x8_t q[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+        q[k] = bf16x8_t{};
+        if (live) q[k] = load8(a.q + row * D + 16 * k + 8 * f);
+    }
+
+    const int64_t item = FP8 ? 1 : 2;
+    const int64_t head_off = kvh * a.cache.head_stride * item;
+    const char* const kp = static_cast<const char*>(a.cache.k) + head_off;
+    const char* const vp = static_cast<const char*>(a.cache.v) + head_off;
+    const int32_t* const table = a.tables ? a.tables + (int64_t)s * a.n : nullptr;
+
+    // lane x of every wave keeps where token x of a tile lies (bytes from the cache's start), -1 if nowhere
+    auto entry_of = [&](int t) {
+        const int tok = t + lane;
+        if (tok >= t1) return -1;
+        const int b = bs.block(tok);
+        return table ? table[b] : b;
+    };
+    auto offset_of = [&](int t, int slot) -> int64_t {
+        const int tok = t + lane;
+        if (tok >= t1 || slot < 0 || slot >= a.N) return -1;
+        return (slot * a.cache.block_stride + (int64_t)(tok - bs.block(tok) * bs.B) * a.cache.token_stride) * item;
+    };
+    u32x4_t ks[NR], vs[NR];
+    auto load_tile = [&](int64_t off) {
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            const int id = threadIdx.x + 256 * x;
+            const int64_t o = __shfl(off, id / CR);
+            ks[x] = u32x4_t{0, 0, 0, 0};
+            vs[x] = u32x4_t{0, 0, 0, 0};
+            if (o >= 0) {
+                ks[x] = *reinterpret_cast<const u32x4_t*>(kp + o + 16 * (id % CR));
+                vs[x] = *reinterpret_cast<const u32x4_t*>(vp + o + 16 * (id % CR));
+            }
+        }
+    };
+    auto store_tile = [&](int buf) {
+        char* const kt = lds + buf * T::kTile;
+        char* const vt = lds + (2 + buf) * T::kTile;
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            const int id = threadIdx.x + 256 * x, tok = id / CR, piece = id % CR;
+            if constexpr (FP8) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    u32x4_t wk, wv;
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        wk[2 * z] = fp8x2_to_bf16<false>(ks[x][2 * y + z]);
+                        wk[2 * z + 1] = fp8x2_to_bf16<true>(ks[x][2 * y + z]);
+                        wv[2 * z] = fp8x2_to_bf16<false>(vs[x][2 * y + z]);
+                        wv[2 * z + 1] = fp8x2_to_bf16<true>(vs[x][2 * y + z]);
+                    }
+                    *reinterpret_cast<u32x4_t*>(kt + T::key(tok, 2 * piece + y)) = wk;
+                    *reinterpret_cast<u32x4_t*>(vt + T::value(tok, 2 * piece + y)) = wv;
+                }
+            } else {
+                *reinterpret_cast<u32x4_t*>(kt + T::key(tok, piece)) = ks[x];
+                *reinterpret_cast<u32x4_t*>(vt + T::value(tok, piece)) = vs[x];
+            }
+        }
+    };
+
+    f32x16_t o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
+    float m = kLowest, l = 0.f, wide_m = kLowest, wide_l = 0.f;
+    const float scale = a.scale * a.cache.k_scale * kLog2e;
+    const int l16 = lane & 15;
+
+    int slot = entry_of(t0);
+    int64_t off = offset_of(t0, slot);
+    uint64_t nowhere = __ballot(off < 0), nowhere_next = 0;
+    load_tile(off);
+    slot = entry_of(t0 + 64);
+    store_tile(0);
+    __syncthreads();
+    for (int t = t0, buf = 0; t < t1; t += 64, buf ^= 1) {
+        const bool more = t + 64 < t1;
+        if (more) {
+            off = offset_of(t + 64, slot);
+            nowhere_next = __ballot(off < 0);
+            load_tile(off);
+            slot = entry_of(t + 128);
+        }
+        const char* const kt = lds + buf * T::kTile;
+        const char* const vt = lds + (2 + buf) * T::kTile;
+#pragma unroll 1
+        for (int half = WK == 2 ? wave % 2 : 0; half < (WK == 2 ? wave % 2 + 1 : 2); ++half) {
+            const int th = t + 32 * half;
+            if (th >= t1) break;
+            const uint32_t dead = (uint32_t)(nowhere >> (32 * half));
+            const bool masked = th + 32 > ctx || dead != 0;
+            if (dead && th < t1 && wave == 0 && lane == 0) {
+                // past the run's end is no error
+                const uint32_t past = t1 - th < 32 ? ~0u << (t1 - th) : 0u;
+                if (dead & ~past) atomicOr(a.err, DEVERR_TABLE);
+            }
+            float x[16];
+            if (wave_live) {
+                f32x16_t acc = f32x16_t{};
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const bf16x8_t key = __builtin_bit_cast(
+                        bf16x8_t, *reinterpret_cast<const u32x4_t*>(kt + T::key(32 * half + n, 2 * k + f)));
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc, 0, 0, 0);
+                }
+#pragma unroll
+                for (int v = 0; v < 16; ++v) x[v] = acc[v] * scale;
+                if (masked) {
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) {
+                        const int in = v % 4 + 8 * (v / 4) + 4 * f, place = th + in - ctx;
+                        const bool sees = !((dead >> in) & 1) && (place < 0 || ((seen >> (place & 63)) & 1));
+                        x[v] = sees ? x[v] : -INFINITY;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < 16; ++v) x[v] = -INFINITY;
+            }
+
+            if (a.block_lse) {
+                // 8-token blocks are quads of v, 16-token ones pairs of quads; one of 32 or more fills the half
+                const int parts = bs.B >= 32 ? 1 : 32 / bs.B;
+                float bm[4], bl[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    bm[y] = fmaxf(fmaxf(x[4 * y], x[4 * y + 1]), fmaxf(x[4 * y + 2], x[4 * y + 3]));
+                if (parts <= 2) {
+                    bm[0] = bm[1] = fmaxf(bm[0], bm[1]);
+                    bm[2] = bm[3] = fmaxf(bm[2], bm[3]);
+                }
+                if (parts == 1) bm[0] = bm[1] = bm[2] = bm[3] = fmaxf(bm[0], bm[2]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    bm[y] = fmaxf(max_over_f(bm[y]), kLowest);
+                    bl[y] = 0.f;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) bl[y] += exp2_of(x[4 * y + v] - bm[y]);
+                }
+                if (parts <= 2) {
+                    bl[0] = bl[0] + bl[1];
+                    bl[2] = bl[2] + bl[3];
+                }
+                if (parts == 1) bl[0] += bl[2];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) bl[y] = sum_over_f(bl[y]);
+                if (parts > 1) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int tok = th + 8 * y;
+                        const bool mine = parts == 4 ? f == y % 2 : (y % 2 == 0 && f == y / 2);
+                        if (mine && r < R && tok < t1)
+                            block_row[bs.block(tok) * block_step] =
+                                live && !(bl[y] <= 0.f) ? (bm[y] + log2_of(bl[y])) * kLn2 : -INFINITY;
+                    }
+                } else {
+                    const float top = fmaxf(wide_m, bm[0]);
+                    wide_l = wide_l * exp2_of(wide_m - top) + bl[0] * exp2_of(bm[0] - top);
+                    wide_m = top;
+                    if (th + 32 >= t1 || (th + 32) % bs.B == 0) {
+                        if (f == 0 && r < R)
+                            block_row[bs.block(th) * block_step] =
+                                live && !(wide_l <= 0.f) ? (wide_m + log2_of(wide_l)) * kLn2 : -INFINITY;
+                        wide_m = kLowest;
+                        wide_l = 0.f;
+                    }
+                }
+            }
+            if (!wave_live) continue;
+
+            float top = x[0];
+#pragma unroll
+            for (int v = 1; v < 16; ++v) top = fmaxf(top, x[v]);
+            if (__ballot(top > m + 8.f)) {
+                const float m_new = fmaxf(m, max_over_f(top));
+                const float alpha = exp2_of(m - m_new);
+                m = m_new;
+                l *= alpha;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d] *= alpha;
+            }
+            bf16x8_t hi[2], lo[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                u32x4_t wh, wl;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[8 * y + e] = exp2_of(x[8 * y + e] - m);
+                    l += x[8 * y + e];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    wh[e] = bf16_pair(x[8 * y + 2 * e], x[8 * y + 2 * e + 1]);
+                    wl[e] = bf16_pair(x[8 * y + 2 * e] - bf16_lo(wh[e]), x[8 * y + 2 * e + 1] - bf16_hi(wh[e]));
+                }
+                hi[y] = __builtin_bit_cast(bf16x8_t, wh);
+                lo[y] = __builtin_bit_cast(bf16x8_t, wl);
+            }
+            // 8 tokens' values of one d: two transpose reads
+            auto value_of = [&](int d, int y) {
+                bf16x8_t out;
+                i16x4_t part[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const int tok = 32 * half + 16 * y + 8 * z + 4 * f + l16 / 4;
+                    const int col = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (l16 % 4);
+                    part[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (lds_i16x4_t*)(vt + T::value(tok, col / 8) + 2 * (col % 8)));
+                }
+                struct { i16x4_t p[2]; } both = {{part[0], part[1]}};
+                out = __builtin_bit_cast(bf16x8_t, both);
+                return out;
+            };
+            bool odd = false;       // as in the stream kernel: a drafted token's value that is not finite
+            if (masked && th + 32 > ctx) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const u32x4_t w = __builtin_bit_cast(u32x4_t, value_of(d, y));
+                        odd |= not_finite(w[0]) || not_finite(w[1]) || not_finite(w[2]) || not_finite(w[3]);
+                    }
+            }
+            auto product = [&](bool clean) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) {
+                        bf16x8_t val = value_of(d, y);
+                        if (clean) {
+                            u32x4_t w = __builtin_bit_cast(u32x4_t, val);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = finite_only(w[e]);
+                            val = __builtin_bit_cast(bf16x8_t, w);
+                        }
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val, hi[y], o[d], 0, 0, 0);
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val, lo[y], o[d], 0, 0, 0);
+                    }
+            };
+            if (__ballot(odd) == 0) {
+                product(false);
+            } else {
+#pragma unroll 1
+                for (int kind = 0; kind < 3; ++kind)
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) {
+                        f32x16_t count = f32x16_t{};
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            u32x4_t w = __builtin_bit_cast(u32x4_t, value_of(d, y));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = indicator(w[e], kind);
+                            count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, w),
+                                                                            ones_of(x + 8 * y), count, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int v = 0; v < 16; ++v) o[d][v] += count[v] > 0.f ? special(kind) : 0.f;
+                    }
+                product(true);
+            }
+        }
+        if (more) store_tile(buf ^ 1);
+        nowhere = nowhere_next;
+        __syncthreads();
+    }
+
+    l = sum_over_f(l);
+    if constexpr (WK == 2) {
+        // the pair's sums, through the (now unused) stage
+        float* const x = reinterpret_cast<float*>(lds) + (wave / 2) * (16 * DT + 2) * 64;
+        if (wave % 2) {
+            x[lane] = m;
+            x[64 + lane] = l;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) x[(2 + 16 * d + v) * 64 + lane] = o[d][v];
+        }
+        __syncthreads();
+        if (wave % 2) return;
+        const float m_other = x[lane], m_new = fmaxf(m, m_other);
+        const float mine = exp2_of(m - m_new), other = exp2_of(m_other - m_new);
+        l = l * mine + x[64 + lane] * other;
+        m = m_new;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) o[d][v] = o[d][v] * mine + x[(2 + 16 * d + v) * 64 + lane] * other;
+    }
+    if (r >= R) return;
+    const bool none = !live || l == 0.f;
+    if (whole) {
+        const float inv = none ? 0.f : a.cache.v_scale / l;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                uint2 w = make_uint2(bf16_pair(o[d][4 * y] * inv, o[d][4 * y + 1] * inv),
+                                     bf16_pair(o[d][4 * y + 2] * inv, o[d][4 * y + 3] * inv));
+                if (none) w = make_uint2(0, 0);
+                *reinterpret_cast<uint2*>(a.out + row * D + 32 * d + 8 * y + 4 * f) = w;
+            }
+        if (a.lse && f == 0) a.lse[row] = none ? -INFINITY : (m + log2_of(l)) * kLn2;
+    } else if (live) {
+        const int64_t which = ((int64_t)s * a.Hk + kvh) * sp.runs + at.split;
+        float* const to = part_sums(a, sp, which, R) + (int64_t)r * D;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                *reinterpret_cast<float4*>(to + 32 * d + 8 * y + 4 * f) =
+                    make_float4(o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]);
+        if (f == 0) part_stats(a, sp, which, R)[r] = make_float2(m, l);
+    }
+}
+
 // ---------------------------------------------------------------- choice of a kernel
 
-enum class Kind { Stream, Plain };
+enum class Kind { Stream, Tree, Plain };
+
+int queries_of(const AttendArgs& a) { return a.M * (a.Hq / a.Hk); }
+
+constexpr int kStreamQueries = 32;      // queries per kv head of the stream kernel
 
 Kind kind_of(const AttendArgs& a) {
-    const int R = a.M * (a.Hq / a.Hk);
     const int item = a.cache.fp8 ? 1 : 2;
     if (a.D != 64 && a.D != 128) return Kind::Plain;
-    // a wave-load's tokens lie in one block
-    const int tpl = 1024 / (a.D * item);
-    if (a.B % tpl != 0) return Kind::Plain;
     // a block's sum is taken inside a tile, or over whole tiles
     if (a.block_lse && !(a.B % 32 == 0 || a.B == 16 || a.B == 8)) return Kind::Plain;
-    // 16-byte loads, and 32-bit offsets inside a wave-load
+    // 16-byte loads
     if (!aligned_to(a.cache.k, 16) || !aligned_to(a.cache.v, 16) ||
         ((a.cache.block_stride | a.cache.token_stride | a.cache.head_stride) * item) % 16 != 0)
         return Kind::Plain;
-    if (a.cache.token_stride > (1 << 24)) return Kind::Plain;
-    return R <= 32 ? Kind::Stream : Kind::Plain;
+    if (queries_of(a) > kStreamQueries) return Kind::Tree;
+    // a wave-load's tokens lie in one block, within 32-bit offsets of its first
+    const int tpl = 1024 / (a.D * item);
+    if (a.B % tpl != 0 || a.cache.token_stride > (1 << 24)) return Kind::Plain;
+    return Kind::Stream;
+}
+
+// Two waves to 32 queries where the queries would leave half of the workgroup
+// idle; not where a block's sum spans the halves of a tile that they take.
+bool tree_pairs(const AttendArgs& a) { return queries_of(a) <= 64 && !(a.block_lse && a.B > 32); }
+
+int tree_groups(const AttendArgs& a) {
+    const int rows = tree_pairs(a) ? 64 : 128;
+    return (queries_of(a) + rows - 1) / rows;
 }
 
 Split split_of(const AttendArgs& a, bool with_block_lse) {
-    const int64_t base = (int64_t)a.S * a.Hk, most = (int64_t)a.n * a.B;
+    const bool tree = queries_of(a) > kStreamQueries;
+    const int64_t base = (int64_t)a.S * a.Hk * (tree ? tree_groups(a) : 1), most = (int64_t)a.n * a.B;
     Split sp;
-    // four waves take tiles, or whole blocks where a block's sum spans tiles
-    sp.unit = with_block_lse && a.B > 32 ? 4 * a.B : 128;
-    // enough workgroups for three on every CU, and runs short enough to even out sequences of different lengths
-    int64_t runs = (3 * (int64_t)a.n_cu + base - 1) / base;
+    // whole tiles (four waves take one each in the stream kernel), or whole blocks where a block's sum spans tiles
+    sp.unit = tree ? 64 : 128;
+    if (with_block_lse && a.B > 32) sp.unit = tree ? (a.B % 64 == 0 ? a.B : 2 * a.B) : 4 * a.B;
+    // enough workgroups to fill the chip, and runs short enough to even out sequences of different lengths
+    int64_t runs = ((tree ? 2 : 3) * (int64_t)a.n_cu + base - 1) / base;
     const int64_t even = most / 4096;
     if (runs < even) runs = even;
     const int64_t limit = (most + sp.unit - 1) / sp.unit;
@@ -793,11 +1270,20 @@ int log2_or_negative(int x) {
 }
 
 template <int D, bool FP8>
-hipError_t launch_stream(const AttendArgs& a, const Split& sp, hipStream_t stream) {
-    const uint32_t grid = (uint32_t)((int64_t)a.S * a.Hk * sp.runs);
+hipError_t launch_fast(const AttendArgs& a, Kind kind, const Split& sp, hipStream_t stream) {
     const BlockSize bs{a.B, log2_or_negative(a.B)};
-    if (a.M * (a.Hq / a.Hk) <= 16) attend_stream_kernel<D, FP8, 1><<<grid, 256, 0, stream>>>(a, sp, bs);
-    else attend_stream_kernel<D, FP8, 2><<<grid, 256, 0, stream>>>(a, sp, bs);
+    int64_t grid = (int64_t)a.S * a.Hk * sp.runs;
+    if (kind == Kind::Stream) {
+        if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
+        if (queries_of(a) <= 16) attend_stream_kernel<D, FP8, 1><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs);
+        else attend_stream_kernel<D, FP8, 2><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs);
+        return hipGetLastError();
+    }
+    const int groups = tree_groups(a);
+    grid = (grid + 7) / 8 * 8 * groups;
+    if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
+    if (tree_pairs(a)) attend_tree_kernel<D, FP8, 2><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs, groups);
+    else attend_tree_kernel<D, FP8, 1><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs, groups);
     return hipGetLastError();
 }
 
@@ -805,15 +1291,19 @@ hipError_t launch_stream(const AttendArgs& a, const Split& sp, hipStream_t strea
 
 size_t attend_workspace_bytes(const AttendArgs& a) {
     if (a.D != 64 && a.D != 128) return 0;
-    const int R = a.M * (a.Hq / a.Hk);
-    if (R > 32) return 0;
-    // the number of runs without block_lse is the larger
-    const Split sp = split_of(a, false);
-    return sp.runs <= 1 ? 0 : (size_t)a.S * a.Hk * sp.runs * R * (a.D + 2) * sizeof(float);
+    // with block_lse the runs are as many or fewer, but up to 64 queries take more workgroups (tree_pairs)
+    AttendArgs b = a;
+    float any;
+    b.block_lse = &any;
+    const int64_t runs[2] = {split_of(a, false).runs, split_of(b, true).runs};
+    const int64_t most = runs[0] > runs[1] ? runs[0] : runs[1];
+    return most <= 1 ? 0 : (size_t)a.S * a.Hk * most * queries_of(a) * (a.D + 2) * sizeof(float);
 }
 
 const char* attend_kernel_name(const AttendArgs& a) {
-    return kind_of(a) == Kind::Stream ? "attend_stream_kernel" : "attend_plain_kernel";
+    const Kind kind = kind_of(a);
+    return kind == Kind::Stream ? "attend_stream_kernel"
+                                : (kind == Kind::Tree ? "attend_tree_kernel" : "attend_plain_kernel");
 }
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
@@ -827,10 +1317,9 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
         return hipGetLastError();
     }
     const Split sp = split_of(a, a.block_lse != nullptr);
-    if (!grid_fits((int64_t)a.S * a.Hk * sp.runs)) return hipErrorInvalidConfiguration;
     hipError_t e;
-    if (a.D == 64) e = a.cache.fp8 ? launch_stream<64, true>(a, sp, stream) : launch_stream<64, false>(a, sp, stream);
-    else e = a.cache.fp8 ? launch_stream<128, true>(a, sp, stream) : launch_stream<128, false>(a, sp, stream);
+    if (a.D == 64) e = a.cache.fp8 ? launch_fast<64, true>(a, kind, sp, stream) : launch_fast<64, false>(a, kind, sp, stream);
+    else e = a.cache.fp8 ? launch_fast<128, true>(a, kind, sp, stream) : launch_fast<128, false>(a, kind, sp, stream);
     if (e != hipSuccess || sp.runs <= 1) return e;
     attend_join_kernel<<<row_grid, 256, 0, stream>>>(a, sp);
     return hipGetLastError();
