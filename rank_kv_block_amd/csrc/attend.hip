@@ -1,5 +1,7 @@
 // Attention of a sequence's newest tokens (one, or a tree of drafted ones) over
 // its paged cache.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -156,13 +158,19 @@ __device__ inline float2* part_stats(const AttendArgs& a, const Split& sp, int64
     return reinterpret_cast<float2*>(static_cast<float*>(a.ws) + (int64_t)a.S * a.Hk * sp.runs * R * a.D) + which * R;
 }
 
-// Joins a row's runs: out = sum_r 2^(m_r - m) o_r / sum_r 2^(m_r - m) l_r.  A
-// workgroup per (sequence, row, query head); its threads take every
-// (256 / (D / 4))-th run, 4 values each.  Latency bound: a few hundred KiB.
+// Joins a row's runs: out = sum_r 2^(m_r - m) o_r / sum_r 2^(m_r - m) l_r.
+// WAVES waves share a row (sequence, drafted row, query head), wave w taking
+// runs w, w + WAVES, ..: a lane reads one run's (maximum, total), then the
+// wave adds the runs' sums, 4 values a lane and 64 / (D / 4) runs at a time.
+// Latency bound, so a row with many runs gets four waves.
+template <int WAVES>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Split sp) {
-    __shared__ float4 sums[256];
-    __shared__ float totals[256];
-    const int h = blockIdx.x % a.Hq, i = blockIdx.x / a.Hq % a.M, s = blockIdx.x / a.Hq / a.M;
+    __shared__ float4 sums[4][64];
+    __shared__ float2 stats[4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row = (int64_t)blockIdx.x * (4 / WAVES) + wave / WAVES;      // [S, M, Hq]
+    if (row >= (int64_t)a.S * a.M * a.Hq) return;       // WAVES = 1 only: no barrier follows
+    const int h = (int)(row % a.Hq), i = (int)(row / a.Hq % a.M), s = (int)(row / a.Hq / a.M);
     const int len = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B);
     const int run = run_of(sp, len);
     if (len <= run) return;     // one run: it wrote the result itself
@@ -170,36 +178,68 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Split sp
     const int runs = i < draft_len_of(a, s, len) ? (len + run - 1) / run : 0;
     const int g = a.Hq / a.Hk, R = a.M * g, r = i * g + h % g;
     const int64_t first = ((int64_t)s * a.Hk + h / g) * sp.runs;
-    const int lanes = a.D / 4, groups = 256 / lanes, group = threadIdx.x / lanes, d4 = threadIdx.x % lanes;
-    float m = kLowest;
-    for (int x = 0; x < runs; ++x) m = fmaxf(m, part_stats(a, sp, first + x, R)[r].x);
+    const int lanes = a.D / 4, groups = 64 / lanes, group = lane / lanes, d4 = lane % lanes;
+    float m = kLowest, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    for (int x = group; x < runs; x += groups) {
-        const float2 st = part_stats(a, sp, first + x, R)[r];
-        const float f = exp2_of(st.x - m);
-        const float4 o = reinterpret_cast<const float4*>(part_sums(a, sp, first + x, R) + (int64_t)r * a.D)[d4];
-        l += f * st.y;
-        v.x += f * o.x;
-        v.y += f * o.y;
-        v.z += f * o.z;
-        v.w += f * o.w;
+    for (int x0 = wave % WAVES; x0 < runs; x0 += 64 * WAVES) {
+        const int x = x0 + lane * WAVES, count = (runs - x0 + WAVES - 1) / WAVES < 64 ? (runs - x0 + WAVES - 1) / WAVES : 64;
+        const float2 st = x < runs ? part_stats(a, sp, first + x, R)[r] : make_float2(kLowest, 0.f);
+        float top = fmaxf(m, st.x);
+        for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        const float alpha = exp2_of(m - top), weight = exp2_of(st.x - top);
+        m = top;
+        l = l * alpha + weight * st.y;
+        v.x *= alpha;
+        v.y *= alpha;
+        v.z *= alpha;
+        v.w *= alpha;
+#pragma unroll 8
+        for (int y = 0; y < count; y += groups) {
+            const int at = y + group;
+            const float f = __shfl(weight, at);
+            if (at < count) {
+                const float4 o = reinterpret_cast<const float4*>(part_sums(a, sp, first + x0 + at * WAVES, R) +
+                                                                 (int64_t)r * a.D)[d4];
+                v.x += f * o.x;
+                v.y += f * o.y;
+                v.z += f * o.z;
+                v.w += f * o.w;
+            }
+        }
     }
-    sums[threadIdx.x] = v;
-    totals[threadIdx.x] = l;
-    __syncthreads();
+    for (int o = 32; o >= 1; o >>= 1) l += __shfl_xor(l, o);
+    for (int o = lanes; o < 64; o <<= 1) {
+        v.x += __shfl_xor(v.x, o);
+        v.y += __shfl_xor(v.y, o);
+        v.z += __shfl_xor(v.z, o);
+        v.w += __shfl_xor(v.w, o);
+    }
+    if constexpr (WAVES > 1) {
+        sums[wave][lane] = v;
+        if (lane == 0) stats[wave] = make_float2(m, l);
+        __syncthreads();
+        if (wave != 0) return;
+        const float mine = m;
+        for (int w = 1; w < WAVES; ++w) m = fmaxf(m, stats[w].x);
+        const float f = exp2_of(mine - m);
+        l *= f;
+        v.x *= f;
+        v.y *= f;
+        v.z *= f;
+        v.w *= f;
+        for (int w = 1; w < WAVES; ++w) {
+            const float fw = exp2_of(stats[w].x - m);
+            const float4 o = sums[w][lane];
+            l += fw * stats[w].y;
+            v.x += fw * o.x;
+            v.y += fw * o.y;
+            v.z += fw * o.z;
+            v.w += fw * o.w;
+        }
+    }
     if (group != 0) return;
-    for (int x = 1; x < groups; ++x) {
-        const float4 o = sums[x * lanes + d4];
-        l += totals[x * lanes + d4];
-        v.x += o.x;
-        v.y += o.y;
-        v.z += o.z;
-        v.w += o.w;
-    }
     const bool none = l == 0.f;
     const float f = none ? 0.f : a.cache.v_scale / l;
-    const int64_t row = ((int64_t)s * a.M + i) * a.Hq + h;
     uint16_t w[4] = {to_bf16(none ? 0.f : v.x * f), to_bf16(none ? 0.f : v.y * f), to_bf16(none ? 0.f : v.z * f),
                      to_bf16(none ? 0.f : v.w * f)};
     *reinterpret_cast<uint2*>(a.out + row * a.D + 4 * d4) = *reinterpret_cast<uint2*>(w);
@@ -266,6 +306,12 @@ __device__ inline float sum_over_c(float x) {
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
+// x, or -x where scale is negative
+__device__ inline bf16x8_t signed_by(float scale, bf16x8_t x) {
+    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
+    return __builtin_bit_cast(bf16x8_t, __builtin_bit_cast(u32x4_t, x) ^ (u32x4_t){flip, flip, flip, flip});
+}
+
 // two e4m3 values (bytes 0, 1 or 2, 3 of w) as two bf16, exact
 template <bool HI>
 __device__ inline uint32_t fp8x2_to_bf16(uint32_t w) {
@@ -306,44 +352,67 @@ __device__ inline bf16x8_t ones_of(const float* x) {
     return __builtin_bit_cast(bf16x8_t, w);
 }
 
-// The blocks of one sequence as a wave walks it: 64 table entries at a time in
-// a register, a lane each.
+// The blocks of one sequence as a wave walks it: 64 blocks at a time, a lane
+// each holding where its block lies (bytes from the head's start of the cache).
+// Entries that are invalid, or of blocks the sequence does not use, stand for
+// block 0: every address is inside the cache, and what is loaded there is masked.
 struct TableWindow {
     const int32_t* row;     // null: the identity
-    int n, first, entries;
+    int used, first;
+    uint32_t lo, hi;
+    uint64_t bad;           // used blocks with an invalid entry
 
-    __device__ inline void load(const AttendArgs& a, int block, int lane) {
+    __device__ inline void load(const AttendArgs& a, int block, int64_t block_bytes, int lane) {
         first = block;
-        entries = block + lane;
-        if (row && block + lane < n) entries = row[block + lane];
+        int e = 0;
+        if (block + lane < used) e = row ? row[block + lane] : block + lane;
+        const bool invalid = e < 0 || e >= a.N;
+        bad = __ballot(invalid);
+        if (bad && lane == 0) atomicOr(a.err, DEVERR_TABLE);
+        const int64_t at = invalid ? 0 : e * block_bytes;
+        lo = (uint32_t)at;
+        hi = (uint32_t)(at >> 32);
     }
-    __device__ inline int at(int block) const { return __builtin_amdgcn_readlane(entries, block - first); }
+    // uniform; any index gives an address inside the cache
+    __device__ inline int64_t at(int index) const {
+        return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, index & 63) << 32 |
+                         (uint32_t)__builtin_amdgcn_readlane((int)lo, index & 63));
+    }
 };
 
-// B a power of two: shift >= 0.
+// Division of a token's index by the block size: one 64-bit product.  With
+// 2^(s-1) < B <= 2^s and magic = ceil(2^(31+s) / B), magic * B - 2^(31+s) < B <=
+// 2^s, so t * magic >> (31 + s) is t / B for every t < 2^31.
 struct BlockSize {
-    int B, shift;
-    __device__ inline int block(int t) const { return shift >= 0 ? t >> shift : (int)((uint32_t)t / (uint32_t)B); }
+    int B, shift;           // shift = 31 + s
+    uint32_t magic;
+    __host__ __device__ inline int block(int t) const { return (int)((uint64_t)(uint32_t)t * magic >> shift); }
 };
 
-// aux bits of the streamed loads: 2 = nontemporal (each byte is read once)
-constexpr int kStreamAux = 2;
+inline BlockSize block_size(int B) {
+    int s = 0;
+    while (s < 31 && (1u << s) < (uint32_t)B) ++s;
+    const uint64_t one = 1ull << (31 + s);
+    return BlockSize{B, 31 + s, (uint32_t)((one + B - 1) / B)};
+}
 
+// BYTES from a uniform address and a lane's offset, nontemporal (each byte is
+// read once).
 template <int BYTES>
-__device__ inline void buffer_load(uint32_t* dst, __amdgpu_buffer_rsrc_t r, int off) {
+__device__ inline void stream_load(uint32_t* dst, const char* base, uint32_t off) {
     if constexpr (BYTES == 16) {
-        const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kStreamAux));
+        const u32x4_t x = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(base + off));
         dst[0] = x[0];
         dst[1] = x[1];
         dst[2] = x[2];
         dst[3] = x[3];
     } else if constexpr (BYTES == 8) {
         typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
-        const u32x2_t x = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, kStreamAux));
+        const u32x2_t x = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(base + off));
         dst[0] = x[0];
         dst[1] = x[1];
     } else {
-        dst[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, kStreamAux);
+        dst[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(base + off));
     }
 }
 
@@ -382,73 +451,53 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
             for (int k = 0; k < KP; ++k) {
                 // a row that is not live weighs nothing: zeros, whatever it holds
                 q[rt][j][k] = bf16x8_t{};
-                if (live[rt]) q[rt][j][k] = load8(row + 8 * KP * (4 * j + c) + 8 * k);
+                if (live[rt]) q[rt][j][k] = signed_by(a.scale, load8(row + 8 * KP * (4 * j + c) + 8 * k));
             }
     }
 
     const int64_t item = FP8 ? 1 : 2;
-    const int ts = (int)(a.cache.token_stride * item);
+    const int ts = (int)(a.cache.token_stride * item), block_ts = bs.B * ts;
     const int64_t block_bytes = a.cache.block_stride * item, head_off = kvh * a.cache.head_stride * item;
     const char* const kp = static_cast<const char*>(a.cache.k) + head_off;
     const char* const vp = static_cast<const char*>(a.cache.v) + head_off;
-    const int k_off = n / H * ts + 16 * (4 * (n % H) + c);
-    int v_off[W];
+    const uint32_t k_off = n / H * ts + 16 * (4 * (n % H) + c);
+    uint32_t v_off[W];
 #pragma unroll
     for (int w = 0; w < W; ++w) v_off[w] = (W * c + w) * ts + n * (VW * 4);
 
     TableWindow table;
     table.row = a.tables ? a.tables + (int64_t)s * a.n : nullptr;
-    table.n = a.n;
-    table.first = 1 << 30;      // no entries yet
-    table.entries = 0;
+    table.used = t1 > 0 ? bs.block(t1 - 1) + 1 : 0;
 
     // this wave's tiles: groups of `per` consecutive ones, every fourth group
     const int per = sp.unit / 128;
-    auto tile_of = [&](int k) { return t0 + 32 * ((k / per * 4 + wave) * per + k % per); };
+    auto tile_of = [&](int k) { return per == 1 ? t0 + 32 * (4 * k + wave) : t0 + 32 * ((k / per * 4 + wave) * per + k % per); };
 
+    // Where a tile's wave-loads begin (each inside one block), moving the window if the tile is past it.
+    int64_t place[NK];
     uint32_t kr[NK][4], vr[8][VW];
-    // Loads u's base and extent: tokens tok .. tok + TPL - 1, all of one block.  Tokens at or past the run's end
-    // and blocks with an invalid entry get an extent that ends before them, and read as zeros.
-    struct Place {
-        int64_t off;
-        int extent;
-    };
-    auto place_of = [&](int tok) {
-        Place r{0, 0};
-        if (tok < t1) {
-            const int b = bs.block(tok);
-            const int slot = table.at(b);
-            const int left = t1 - tok < TPL ? t1 - tok : TPL;
-            if (slot >= 0 && slot < a.N) {
-                r.off = slot * block_bytes + (int64_t)(tok - b * bs.B) * ts;
-                r.extent = (left - 1) * ts + L::RB;
-            }
-        }
-        return r;
-    };
-    auto window_for = [&](int t) {
-        if (t < t1) {
-            const int first = bs.block(t), last = bs.block(t + 31 < t1 ? t + 31 : t1 - 1);
-            if (first < table.first || last >= table.first + 64) table.load(a, first, lane);
-        }
-    };
-    auto load_k = [&](int t) {
+    auto places = [&](int t) {
+        const int b = bs.block(t), last = bs.block(t + 31 < t1 ? t + 31 : t1 - 1);
+        if (last >= table.first + 64) table.load(a, b, block_bytes, lane);
+        int index = b - table.first, off = (t - b * bs.B) * ts;
 #pragma unroll
         for (int u = 0; u < NK; ++u) {
-            const Place pl = place_of(t + TPL * u);
-            buffer_load<16>(kr[u], __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(kp + pl.off), (short)0,
-                                                                     pl.extent, 0x00020000), k_off);
+            place[u] = table.at(index) + off;
+            off += TPL * ts;
+            const bool over = off == block_ts;
+            off = over ? 0 : off;
+            index += over;
         }
     };
-    auto load_v = [&](int t) {
+    auto load_k = [&]() {
 #pragma unroll
-        for (int u = 0; u < NK; ++u) {
-            const Place pl = place_of(t + TPL * u);
-            const __amdgpu_buffer_rsrc_t rsrc =
-                __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(vp + pl.off), (short)0, pl.extent, 0x00020000);
+        for (int u = 0; u < NK; ++u) stream_load<16>(kr[u], kp + place[u], k_off);
+    };
+    auto load_v = [&]() {
 #pragma unroll
-            for (int w = 0; w < W; ++w) buffer_load<VW * 4>(vr[u * W + w], rsrc, v_off[w]);
-        }
+        for (int u = 0; u < NK; ++u)
+#pragma unroll
+            for (int w = 0; w < W; ++w) stream_load<VW * 4>(vr[u * W + w], vp + place[u], v_off[w]);
     };
 
     f32x4_t o[RT][J];
@@ -467,15 +516,19 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
         wide_m[rt] = kLowest;
         wide_l[rt] = 0.f;
     }
-    const float scale = a.scale * a.cache.k_scale * kLog2e;
+    // scores stay in units of q k; `scale` (not negative, the queries carry the sign) turns them into log2 units
+    const float scale = fabsf(a.scale) * a.cache.k_scale * kLog2e, slack = 8.f / scale;
 
     int t = tile_of(0);
-    window_for(t);
-    load_k(t);
-    load_v(t);
+    if (t < t1) {
+        table.load(a, bs.block(t), block_bytes, lane);
+        places(t);
+        load_k();
+        load_v();
+    }
     for (int k = 0; t < t1; ++k) {
         const int next = tile_of(k + 1);
-        // scores of this tile's 32 tokens, in units of log2
+        // scores of this tile's 32 tokens
         float x[RT][8];
 #pragma unroll
         for (int u = 0; u < NK; ++u) {
@@ -503,25 +556,24 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
                     float sum = part[0][w * H];
 #pragma unroll
                     for (int j = 1; j < H; ++j) sum += part[j][w * H + j];
-                    x[rt][u * W + w] = sum * scale;
+                    x[rt][u * W + w] = sum;
                 }
             }
         }
-        // which loads of this tile have an invalid table entry (before the window moves on)
+        // which loads of this tile lie in a block with an invalid entry (before the window moves on)
         uint32_t dead = 0;
+        if (table.bad) {
 #pragma unroll
-        for (int u = 0; u < NK; ++u)
-            if (t + TPL * u < t1) {
-                const int slot = table.at(bs.block(t + TPL * u));
-                if (slot < 0 || slot >= a.N) dead |= 1u << u;
-            }
+            for (int u = 0; u < NK; ++u)
+                dead |= (uint32_t)((table.bad >> ((bs.block(t + TPL * u) - table.first) & 63)) & 1) << u;
+        }
         const bool masked = t + 32 > ctx || t + 32 > t1 || dead != 0;
-        // the next tile's window may replace this one's: this tile's values are already on their way
-        window_for(next);
-        load_k(next);
+        if (next < t1) {
+            places(next);
+            load_k();
+        }
 
         if (masked) {
-            if (dead && lane == 0) atomicOr(a.err, DEVERR_TABLE);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int u = e / W, tok = t + TPL * u + W * c + e % W;
@@ -532,6 +584,8 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
                     const bool sees = there && (at < 0 || ((seen[rt] >> (at & 63)) & 1));
                     x[rt][e] = sees ? x[rt][e] : -INFINITY;
                 }
+#pragma unroll
+                for (int y = 0; y < VW; ++y) vr[e][y] = there ? vr[e][y] : 0u;     // no value there at all
             }
         }
 
@@ -543,13 +597,13 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
             top[rt] = x[rt][0];
 #pragma unroll
             for (int e = 1; e < 8; ++e) top[rt] = fmaxf(top[rt], x[rt][e]);
-            above |= top[rt] > m[rt] + 8.f;
+            above |= top[rt] > m[rt] + slack;
         }
         if (__ballot(above)) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 const float m_new = fmaxf(m[rt], max_over_c(top[rt]));
-                const float alpha = exp2_of(m[rt] - m_new);
+                const float alpha = exp2_of((m[rt] - m_new) * scale);
                 m[rt] = m_new;
                 l[rt] *= alpha;
 #pragma unroll
@@ -558,60 +612,48 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
         }
 
         if (a.block_lse) {
-            // blocks of 8 or 16 tokens lie side by side in a tile: places (32 / B) of the 8 each; one of 32 or more
-            // fills it
-            const int parts = bs.B >= 32 ? 1 : 32 / bs.B;
+            // blocks of 8 or 16 tokens lie side by side in a tile, in 2 or 4 of a lane's 8 places; one of 32 or more
+            // fills it.  `parts` of them; c-th lane groups write the c-th.
+            auto blocks = [&](auto parts_, int rt) {
+                constexpr int parts = decltype(parts_)::value, places_each = 8 / parts;
+                const int r = rt * 16 + n;
+                float* const to = a.block_lse + ((int64_t)s * a.n * a.M + r / g) * a.Hq + kvh * g + r % g;
+                const int64_t step = (int64_t)a.M * a.Hq;
+                float mine = -INFINITY;
+#pragma unroll
+                for (int y = 0; y < parts; ++y) {
+                    float bm = x[rt][y * places_each];
+#pragma unroll
+                    for (int e = 1; e < places_each; ++e) bm = fmaxf(bm, x[rt][y * places_each + e]);
+                    bm = fmaxf(max_over_c(bm), kLowest);
+                    float bl = 0.f;
+#pragma unroll
+                    for (int e = 0; e < places_each; ++e) bl += exp2_of((x[rt][y * places_each + e] - bm) * scale);
+                    bl = sum_over_c(bl);
+                    if constexpr (parts == 1) {
+                        const float both = fmaxf(wide_m[rt], bm);
+                        wide_l[rt] = wide_l[rt] * exp2_of((wide_m[rt] - both) * scale) + bl * exp2_of((bm - both) * scale);
+                        wide_m[rt] = both;
+                        bl = wide_l[rt];
+                        bm = both;
+                    }
+                    const float log = live[rt] && !(bl <= 0.f) ? (bm * scale + log2_of(bl)) * kLn2 : -INFINITY;
+                    mine = y == c ? log : mine;
+                }
+                const int tok = t + 32 / parts * c;
+                // of a block wider than a tile: with its last tile, or the sequence's
+                const bool done = parts > 1 || t + 32 >= t1 || bs.block(t + 32) != bs.block(t);
+                if (done && c < parts && r < R && tok < t1) to[bs.block(tok) * step] = mine;
+                if (parts == 1 && done) {
+                    wide_m[rt] = kLowest;
+                    wide_l[rt] = 0.f;
+                }
+            };
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const int r = rt * 16 + n;
-                float bm[4], bl[4];
-                // the maximum of each pair of places, then of what a block covers
-                float pm[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) pm[y] = fmaxf(x[rt][2 * y], x[rt][2 * y + 1]);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    float top_y = pm[y];
-                    if (parts <= 2) top_y = fmaxf(top_y, pm[y ^ 1]);
-                    if (parts == 1) top_y = fmaxf(top_y, fmaxf(pm[y ^ 2], pm[y ^ 3]));
-                    bm[y] = fmaxf(max_over_c(top_y), kLowest);
-                }
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    pm[y] = exp2_of(x[rt][2 * y] - bm[y]) + exp2_of(x[rt][2 * y + 1] - bm[y]);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    float sum = pm[y];
-                    if (parts <= 2) sum += pm[y ^ 1];
-                    if (parts == 1) sum += pm[y ^ 2] + pm[y ^ 3];
-                    bl[y] = sum_over_c(sum);
-                }
-                const int i = r / g;
-                float* const to = a.block_lse + ((int64_t)s * a.n * a.M + i) * a.Hq + kvh * g + r % g;
-                const int64_t step = (int64_t)a.M * a.Hq;
-                if (parts > 1) {
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        // lane group c writes the block that its c-th pair of places belongs to
-                        const int tok = t + 8 * y;
-                        const bool mine = parts == 4 ? c == y : (y % 2 == 0 && c == y);
-                        if (mine && r < R && tok < t1)
-                            to[bs.block(tok) * step] =
-                                live[rt] && !(bl[y] <= 0.f) ? (bm[y] + log2_of(bl[y])) * kLn2 : -INFINITY;
-                    }
-                } else {
-                    const float top_m = fmaxf(wide_m[rt], bm[0]);
-                    wide_l[rt] = wide_l[rt] * exp2_of(wide_m[rt] - top_m) + bl[0] * exp2_of(bm[0] - top_m);
-                    wide_m[rt] = top_m;
-                    // the block's last tile, or the sequence's
-                    if (t + 32 >= t1 || (t + 32) % bs.B == 0) {
-                        const float w = wide_l[rt];
-                        if (c == 0 && r < R)
-                            to[bs.block(t) * step] = live[rt] && !(w <= 0.f) ? (wide_m[rt] + log2_of(w)) * kLn2 : -INFINITY;
-                        wide_m[rt] = kLowest;
-                        wide_l[rt] = 0.f;
-                    }
-                }
+                if (bs.B == 16) blocks(std::integral_constant<int, 2>(), rt);
+                else if (bs.B == 8) blocks(std::integral_constant<int, 4>(), rt);
+                else blocks(std::integral_constant<int, 1>(), rt);
             }
         }
 
@@ -621,7 +663,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
             u32x4_t wh, wl;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                x[rt][e] = exp2_of(x[rt][e] - m[rt]);
+                x[rt][e] = exp2_of((x[rt][e] - m[rt]) * scale);
                 l[rt] += x[rt][e];
             }
 #pragma unroll
@@ -655,57 +697,55 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
 #pragma unroll
                 for (int y = 0; y < J / 2; ++y) odd |= not_finite(vw[e][y]);
         }
-        // first operands of d = J p + 2 y and J p + 2 y + 1
-        auto transposed = [&](int y, u32x4_t& even, u32x4_t& uneven) {
+        // first operands of d = J p + 2 y (z = 0) and J p + 2 y + 1 (z = 1)
+        auto transposed = [&](int y, int z) {
+            u32x4_t w;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                even[e] = __builtin_amdgcn_perm(vw[2 * e + 1][y], vw[2 * e][y], 0x05040100);
-                uneven[e] = __builtin_amdgcn_perm(vw[2 * e + 1][y], vw[2 * e][y], 0x07060302);
+            for (int e = 0; e < 4; ++e)
+                w[e] = __builtin_amdgcn_perm(vw[2 * e + 1][y], vw[2 * e][y], z ? 0x07060302 : 0x05040100);
+            return w;
+        };
+        auto product = [&](u32x4_t w, int j) {
+            const bf16x8_t val = __builtin_bit_cast(bf16x8_t, w);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                o[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, hi[rt], o[rt][j], 0, 0, 0);
+                o[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, lo[rt], o[rt][j], 0, 0, 0);
             }
         };
-        if (__ballot(odd)) {
+        if (__ballot(odd) == 0) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) product(transposed(j / 2, j % 2), j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const u32x4_t w = transposed(j / 2, j % 2);
 #pragma unroll 1
-            for (int kind = 0; kind < 3; ++kind)
+                for (int kind = 0; kind < 3; ++kind) {
+                    u32x4_t hit;
 #pragma unroll
-                for (int y = 0; y < J / 2; ++y) {
-                    u32x4_t w[2];
-                    transposed(y, w[0], w[1]);
+                    for (int e = 0; e < 4; ++e) hit[e] = indicator(w[e], kind);
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const f32x4_t count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8_t, hit), ones_of(x[rt]), f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) w[z][e] = indicator(w[z][e], kind);
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
-                            const f32x4_t count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(bf16x8_t, w[z]), ones_of(x[rt]), f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) o[rt][2 * y + z][v] += count[v] > 0.f ? special(kind) : 0.f;
-                        }
+                        for (int v = 0; v < 4; ++v) o[rt][j][v] += count[v] > 0.f ? special(kind) : 0.f;
                     }
                 }
+                u32x4_t clean;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-#pragma unroll
-                for (int y = 0; y < J / 2; ++y) vw[e][y] = finite_only(vw[e][y]);
-        }
-#pragma unroll
-        for (int y = 0; y < J / 2; ++y) {
-            u32x4_t w[2];
-            transposed(y, w[0], w[1]);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                const bf16x8_t val = __builtin_bit_cast(bf16x8_t, w[z]);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    f32x4_t& to = o[rt][2 * y + z];
-                    to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, hi[rt], to, 0, 0, 0);
-                    to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, lo[rt], to, 0, 0, 0);
-                }
+                for (int e = 0; e < 4; ++e) clean[e] = finite_only(w[e]);
+                product(clean, j);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        load_v(next);
+        if (next < t1) load_v();
         t = next;
     }
+
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) m[rt] = fmaxf(m[rt] * scale, kLowest);     // log2 units from here on
 
     // the waves' sums: 2 and 3 into 0 and 1, then 1 into 0
 #pragma unroll
@@ -1253,8 +1293,8 @@ Split split_of(const AttendArgs& a, bool with_block_lse) {
     // whole tiles (four waves take one each in the stream kernel), or whole blocks where a block's sum spans tiles
     sp.unit = tree ? 64 : 128;
     if (with_block_lse && a.B > 32) sp.unit = tree ? (a.B % 64 == 0 ? a.B : 2 * a.B) : 4 * a.B;
-    // enough workgroups to fill the chip, and runs short enough to even out sequences of different lengths
-    int64_t runs = ((tree ? 2 : 3) * (int64_t)a.n_cu + base - 1) / base;
+    // two workgroups on every CU, and runs short enough to even out sequences of different lengths
+    int64_t runs = (2 * (int64_t)a.n_cu + base - 1) / base;
     const int64_t even = most / 4096;
     if (runs < even) runs = even;
     const int64_t limit = (most + sp.unit - 1) / sp.unit;
@@ -1263,15 +1303,9 @@ Split split_of(const AttendArgs& a, bool with_block_lse) {
     return sp;
 }
 
-int log2_or_negative(int x) {
-    for (int i = 0; i < 31; ++i)
-        if (x == 1 << i) return i;
-    return -1;
-}
-
 template <int D, bool FP8>
 hipError_t launch_fast(const AttendArgs& a, Kind kind, const Split& sp, hipStream_t stream) {
-    const BlockSize bs{a.B, log2_or_negative(a.B)};
+    const BlockSize bs = block_size(a.B);
     int64_t grid = (int64_t)a.S * a.Hk * sp.runs;
     if (kind == Kind::Stream) {
         if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
@@ -1321,7 +1355,10 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     if (a.D == 64) e = a.cache.fp8 ? launch_fast<64, true>(a, kind, sp, stream) : launch_fast<64, false>(a, kind, sp, stream);
     else e = a.cache.fp8 ? launch_fast<128, true>(a, kind, sp, stream) : launch_fast<128, false>(a, kind, sp, stream);
     if (e != hipSuccess || sp.runs <= 1) return e;
-    attend_join_kernel<<<row_grid, 256, 0, stream>>>(a, sp);
+    // four waves a row where there are runs enough for them (131072 tokens of one sequence in 64 runs: 15.6 us with one
+    // thread after another reading the maxima; 65536 rows of 4 runs want one wave each)
+    if (sp.runs > 8) attend_join_kernel<4><<<row_grid, 256, 0, stream>>>(a, sp);
+    else attend_join_kernel<1><<<(row_grid + 3) / 4, 256, 0, stream>>>(a, sp);
     return hipGetLastError();
 }
 
