@@ -163,7 +163,7 @@ __device__ inline float2* part_stats(const AttendArgs& a, const Split& sp, int64
 // runs w, w + WAVES, ..: a lane reads one run's (maximum, total), then the
 // wave adds the runs' sums, 4 values a lane and 64 / (D / 4) runs at a time.
 // Latency bound, so a row with many runs gets four waves.
-template <int WAVES>
+template <int D, int WAVES>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Split sp) {
     __shared__ float4 sums[4][64];
     __shared__ float2 stats[4];
@@ -178,32 +178,39 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Split sp
     const int runs = i < draft_len_of(a, s, len) ? (len + run - 1) / run : 0;
     const int g = a.Hq / a.Hk, R = a.M * g, r = i * g + h % g;
     const int64_t first = ((int64_t)s * a.Hk + h / g) * sp.runs;
-    const int lanes = a.D / 4, groups = 64 / lanes, group = lane / lanes, d4 = lane % lanes;
+    constexpr int lanes = D / 4, groups = 64 / lanes, kAhead = 8;       // kAhead loads in flight a lane
+    const int group = lane / lanes, d4 = lane % lanes;
     float m = kLowest, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = wave % WAVES; x0 < runs; x0 += 64 * WAVES) {
-        const int x = x0 + lane * WAVES, count = (runs - x0 + WAVES - 1) / WAVES < 64 ? (runs - x0 + WAVES - 1) / WAVES : 64;
-        const float2 st = x < runs ? part_stats(a, sp, first + x, R)[r] : make_float2(kLowest, 0.f);
-        float top = fmaxf(m, st.x);
-        for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-        const float alpha = exp2_of(m - top), weight = exp2_of(st.x - top);
-        m = top;
-        l = l * alpha + weight * st.y;
-        v.x *= alpha;
-        v.y *= alpha;
-        v.z *= alpha;
-        v.w *= alpha;
-#pragma unroll 8
-        for (int y = 0; y < count; y += groups) {
-            const int at = y + group;
-            const float f = __shfl(weight, at);
-            if (at < count) {
-                const float4 o = reinterpret_cast<const float4*>(part_sums(a, sp, first + x0 + at * WAVES, R) +
-                                                                 (int64_t)r * a.D)[d4];
-                v.x += f * o.x;
-                v.y += f * o.y;
-                v.z += f * o.z;
-                v.w += f * o.w;
+    // this wave's runs: w, w + WAVES, ..; 64 at a time for the statistics, groups * kAhead for the sums
+    const int mine = (runs - wave % WAVES + WAVES - 1) / WAVES;
+    for (int x0 = 0; x0 < mine; x0 += 64) {
+        auto run_at = [&](int x) { return first + wave % WAVES + (int64_t)x * WAVES; };
+        const int count = mine - x0 < 64 ? mine - x0 : 64;
+        const float2 st = lane < count ? part_stats(a, sp, run_at(x0 + lane), R)[r] : make_float2(kLowest, 0.f);
+        float top = m, weight = 0.f;
+        for (int y0 = 0; y0 < count; y0 += groups * kAhead) {
+            float4 o[kAhead];
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const int x = y0 + e * groups + group;
+                o[e] = reinterpret_cast<const float4*>(part_sums(a, sp, run_at(x0 + (x < count ? x : 0)), R) +
+                                                       (int64_t)r * D)[d4];
+            }
+            if (y0 == 0) {
+                top = fmaxf(m, st.x);
+                for (int e = 32; e >= 1; e >>= 1) top = fmaxf(top, __shfl_xor(top, e));
+                const float alpha = exp2_of(m - top);
+                weight = lane < count ? exp2_of(st.x - top) : 0.f;
+                m = top;
+                l = l * alpha + weight * st.y;
+                v = make_float4(v.x * alpha, v.y * alpha, v.z * alpha, v.w * alpha);
+            }
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const int x = y0 + e * groups + group;
+                const float f = __shfl(weight, x & 63);
+                if (x < count) v = make_float4(v.x + f * o[e].x, v.y + f * o[e].y, v.z + f * o[e].z, v.w + f * o[e].w);
             }
         }
     }
@@ -219,9 +226,9 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Split sp
         if (lane == 0) stats[wave] = make_float2(m, l);
         __syncthreads();
         if (wave != 0) return;
-        const float mine = m;
+        const float own = m;
         for (int w = 1; w < WAVES; ++w) m = fmaxf(m, stats[w].x);
-        const float f = exp2_of(mine - m);
+        const float f = exp2_of(own - m);
         l *= f;
         v.x *= f;
         v.y *= f;
@@ -322,9 +329,20 @@ __device__ inline uint32_t bf16_pair(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){lo, hi}, bf16x2_t));
 }
 
-// whether either half of w is an infinity or a NaN
-__device__ inline bool not_finite(uint32_t w) {
-    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+// Division of a token's index by the block size: one 64-bit product.  With
+// 2^(s-1) < B <= 2^s and magic = ceil(2^(31+s) / B), magic * B - 2^(31+s) < B <=
+// 2^s, so t * magic >> (31 + s) is t / B for every t < 2^31.
+struct BlockSize {
+    int B, shift;           // shift = 31 + s
+    uint32_t magic;
+    __host__ __device__ inline int block(int t) const { return (int)((uint64_t)(uint32_t)t * magic >> shift); }
+};
+
+inline BlockSize block_size(int B) {
+    int s = 0;
+    while (s < 31 && (1u << s) < (uint32_t)B) ++s;
+    const uint64_t one = 1ull << (31 + s);
+    return BlockSize{B, 31 + s, (uint32_t)((one + B - 1) / B)};
 }
 
 // w with its halves that are not finite set to 0
@@ -332,24 +350,33 @@ __device__ inline uint32_t finite_only(uint32_t w) {
     return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
 }
 
-// A masked weight is 0, and 0 times a value that is not finite would be NaN in
-// the matrix cores.  So where a drafted token's values hold any, the product
-// runs over the finite ones, and three more products of indicators count, for
-// each result, the NaN, +inf and -inf values of weight above 0 (kinds 0, 1, 2).
-__device__ inline uint32_t indicator(uint32_t w, int kind) {
-    auto hit = [&](uint32_t h) {
-        return kind == 0 ? (h & 0x7FFFu) > 0x7F80u : (kind == 1 ? h == 0x7F80u : h == 0xFF80u);
-    };
-    return (hit(w & 0xFFFFu) ? 0x3F80u : 0u) | (hit(w >> 16) ? 0x3F800000u : 0u);
-}
-__device__ inline float special(int kind) { return kind == 0 ? NAN : (kind == 1 ? INFINITY : -INFINITY); }
-
-// weights as a second operand of ones where they are not 0
-__device__ inline bf16x8_t ones_of(const float* x) {
-    u32x4_t w;
+// the same for four e4m3 values, whose only such pattern is NaN (0x7F, 0xFF)
+__device__ inline uint32_t finite_only_fp8(uint32_t w) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = (x[2 * e] != 0.f ? 0x3F80u : 0u) | (x[2 * e + 1] != 0.f ? 0x3F800000u : 0u);
-    return __builtin_bit_cast(bf16x8_t, w);
+    for (int i = 0; i < 32; i += 8)
+        if (((w >> i) & 0x7Fu) == 0x7Fu) w &= ~(0xFFu << i);
+    return w;
+}
+
+// A masked weight is 0, and 0 times a value that is not finite would be NaN in
+// the matrix cores.  So drafted tokens' values enter the products with 0 in the
+// place of what is not finite, and a sequence that holds any adds it afterwards
+// to the rows that see its token: the sum of weight times value is then that
+// infinity or NaN whatever the (positive) weight. 
+template <bool FP8>
+__device__ inline float not_finite_part(const char* row, int d) {
+    if constexpr (FP8) return (static_cast<uint8_t>(row[d]) & 0x7F) == 0x7F ? NAN : 0.f;
+    const uint32_t w = reinterpret_cast<const uint16_t*>(row)[d];
+    return (w & 0x7F80u) == 0x7F80u ? bf16_lo(w) : 0.f;
+}
+// The values of a token's head, null where its block has an invalid entry.
+__device__ inline const char* value_row(const AttendArgs& a, const BlockSize& bs, int s, int kvh, int tok, int64_t item) {
+    const int b = bs.block(tok);
+    const int64_t slot = a.tables ? a.tables[(int64_t)s * a.n + b] : b;
+    if (slot < 0 || slot >= a.N) return nullptr;
+    return static_cast<const char*>(a.cache.v) +
+           (slot * a.cache.block_stride + (int64_t)(tok - b * bs.B) * a.cache.token_stride +
+            (int64_t)kvh * a.cache.head_stride) * item;
 }
 
 // The blocks of one sequence as a wave walks it: 64 blocks at a time, a lane
@@ -380,22 +407,6 @@ struct TableWindow {
     }
 };
 
-// Division of a token's index by the block size: one 64-bit product.  With
-// 2^(s-1) < B <= 2^s and magic = ceil(2^(31+s) / B), magic * B - 2^(31+s) < B <=
-// 2^s, so t * magic >> (31 + s) is t / B for every t < 2^31.
-struct BlockSize {
-    int B, shift;           // shift = 31 + s
-    uint32_t magic;
-    __host__ __device__ inline int block(int t) const { return (int)((uint64_t)(uint32_t)t * magic >> shift); }
-};
-
-inline BlockSize block_size(int B) {
-    int s = 0;
-    while (s < 31 && (1u << s) < (uint32_t)B) ++s;
-    const uint64_t one = 1ull << (31 + s);
-    return BlockSize{B, 31 + s, (uint32_t)((one + B - 1) / B)};
-}
-
 // BYTES from a uniform address and a lane's offset, nontemporal (each byte is
 // read once).
 template <int BYTES>
@@ -416,18 +427,24 @@ __device__ inline void stream_load(uint32_t* dst, const char* base, uint32_t off
     }
 }
 
-template <int D, bool FP8, int RT>
-__global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(AttendArgs a, Split sp, BlockSize bs) {
+template <int D, bool FP8>
+__global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Split sp, BlockSize bs, int groups) {
     using L = StreamLayout<D, FP8>;
     constexpr int NK = L::NK, W = L::W, H = L::H, KP = L::KP, J = L::J, TPL = L::TPL, VW = L::VW;
-    __shared__ float exchange[2][(RT * J * 4 + 2 * RT) * 64];
+    __shared__ float exchange[2][(J * 4 + 2) * 64];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, c = lane >> 4;
-    const int kvh = blockIdx.x % a.Hk;
-    const int split = blockIdx.x / a.Hk % sp.runs, s = blockIdx.x / a.Hk / sp.runs;
+    // the kv heads of a run are 8 workgroups apart: one XCD reads the heads of a token, which lie side by side in
+    // HBM, at about the same time (64 sequences, FP8: 457 us, against 499 with the heads on XCDs of their own)
+    // (and so are the row groups of a head, which read the same bytes)
+    const uint32_t each = 8u * a.Hk * groups, chunk = blockIdx.x / each, in = blockIdx.x % each;
+    const int kvh = in / 8 / groups, group = in / 8 % groups;
+    const int64_t item_run = (int64_t)chunk * 8 + in % 8;
+    const int split = (int)(item_run % sp.runs), s = (int)(item_run / sp.runs);
+    if (s >= a.S) return;
     const int len = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B), drafted = draft_len_of(a, s, len);
-    if (kvh == 0 && split == 0 && threadIdx.x == 0) check_lengths(a, s, len, drafted);
+    if (kvh == 0 && group == 0 && split == 0 && threadIdx.x == 0) check_lengths(a, s, len, drafted);
     const int ctx = len - drafted;
     const int run = run_of(sp, len);
     const int t0 = split * run;
@@ -435,25 +452,20 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
     const int t1 = t0 + run < len ? t0 + run : len;
     const int g = a.Hq / a.Hk, R = a.M * g;
 
-    // queries, as second operands
-    bf16x8_t q[RT][H][KP];
-    uint64_t seen[RT];
-    bool live[RT];
+    // the lane's row, and the queries as second operands
+    const int r = 16 * group + n, i = r / g;
+    const bool live = r < R && i < drafted;
+    const uint64_t seen = live ? tree_word(a, s, i) : 0;
+    const int64_t row = ((int64_t)s * a.M + i) * a.Hq + kvh * g + r % g;
+    bf16x8_t q[H][KP];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = rt * 16 + n, i = r / g;
-        live[rt] = r < R && i < drafted;
-        seen[rt] = live[rt] ? tree_word(a, s, i) : 0;
-        const uint16_t* row = a.q + (((int64_t)s * a.M + i) * a.Hq + kvh * g + r % g) * D;
+    for (int j = 0; j < H; ++j)
 #pragma unroll
-        for (int j = 0; j < H; ++j)
-#pragma unroll
-            for (int k = 0; k < KP; ++k) {
-                // a row that is not live weighs nothing: zeros, whatever it holds
-                q[rt][j][k] = bf16x8_t{};
-                if (live[rt]) q[rt][j][k] = signed_by(a.scale, load8(row + 8 * KP * (4 * j + c) + 8 * k));
-            }
-    }
+        for (int k = 0; k < KP; ++k) {
+            // a row that is not live weighs nothing: zeros, whatever it holds
+            q[j][k] = bf16x8_t{};
+            if (live) q[j][k] = signed_by(a.scale, load8(a.q + row * D + 8 * KP * (4 * j + c) + 8 * k));
+        }
 
     const int64_t item = FP8 ? 1 : 2;
     const int ts = (int)(a.cache.token_stride * item), block_ts = bs.B * ts;
@@ -500,25 +512,15 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
             for (int w = 0; w < W; ++w) stream_load<VW * 4>(vr[u * W + w], vp + place[u], v_off[w]);
     };
 
-    f32x4_t o[RT][J];
-    float m[RT], l[RT];
+    f32x4_t o[J];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = kLowest;
-        l[rt] = 0.f;
-#pragma unroll
-        for (int j = 0; j < J; ++j) o[rt][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
-    // block_lse of a block wider than a tile: its maximum and sum so far
-    float wide_m[RT], wide_l[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        wide_m[rt] = kLowest;
-        wide_l[rt] = 0.f;
-    }
+    for (int j = 0; j < J; ++j) o[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    float m = kLowest, l = 0.f;
+    float wide_m = kLowest, wide_l = 0.f;       // block_lse of a block wider than a tile: its maximum and sum so far
     // scores stay in units of q k; `scale` (not negative, the queries carry the sign) turns them into log2 units
     const float scale = fabsf(a.scale) * a.cache.k_scale * kLog2e, slack = 8.f / scale;
 
+    bool odd = false;       // a drafted token's value is not finite
     int t = tile_of(0);
     if (t < t1) {
         table.load(a, bs.block(t), block_bytes, lane);
@@ -529,7 +531,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
     for (int k = 0; t < t1; ++k) {
         const int next = tile_of(k + 1);
         // scores of this tile's 32 tokens
-        float x[RT][8];
+        float x[8];
 #pragma unroll
         for (int u = 0; u < NK; ++u) {
             bf16x8_t key[KP];
@@ -541,23 +543,20 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
             } else {
                 key[0] = __builtin_bit_cast(bf16x8_t, (u32x4_t){kr[u][0], kr[u][1], kr[u][2], kr[u][3]});
             }
+            f32x4_t part[H];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                f32x4_t part[H];
+            for (int j = 0; j < H; ++j) {
+                part[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < H; ++j) {
-                    part[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                for (int kk = 0; kk < KP; ++kk)
+                    part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key[kk], q[j][kk], part[j], 0, 0, 0);
+            }
 #pragma unroll
-                    for (int kk = 0; kk < KP; ++kk)
-                        part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(key[kk], q[rt][j][kk], part[j], 0, 0, 0);
-                }
+            for (int w = 0; w < W; ++w) {
+                float sum = part[0][w * H];
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    float sum = part[0][w * H];
-#pragma unroll
-                    for (int j = 1; j < H; ++j) sum += part[j][w * H + j];
-                    x[rt][u * W + w] = sum;
-                }
+                for (int j = 1; j < H; ++j) sum += part[j][w * H + j];
+                x[u * W + w] = sum;
             }
         }
         // which loads of this tile lie in a block with an invalid entry (before the window moves on)
@@ -579,101 +578,94 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
                 const int u = e / W, tok = t + TPL * u + W * c + e % W;
                 const bool there = tok < t1 && !((dead >> u) & 1);
                 const int at = tok - ctx;
+                const bool sees = there && (at < 0 || ((seen >> (at & 63)) & 1));
+                x[e] = sees ? x[e] : -INFINITY;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const bool sees = there && (at < 0 || ((seen[rt] >> (at & 63)) & 1));
-                    x[rt][e] = sees ? x[rt][e] : -INFINITY;
+                for (int y = 0; y < VW; ++y) {
+                    vr[e][y] = there ? vr[e][y] : 0u;       // no value there at all
+                    const uint32_t finite = FP8 ? finite_only_fp8(vr[e][y]) : finite_only(vr[e][y]);
+                    if (at >= 0 && finite != vr[e][y]) {
+                        vr[e][y] = finite;
+                        odd = true;
+                    }
                 }
-#pragma unroll
-                for (int y = 0; y < VW; ++y) vr[e][y] = there ? vr[e][y] : 0u;     // no value there at all
             }
         }
 
         // the running maximum
-        float top[RT];
-        bool above = false;
+        float top = x[0];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            top[rt] = x[rt][0];
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+        if (__ballot(top > m + slack)) {
+            const float m_new = fmaxf(m, max_over_c(top));
+            const float alpha = exp2_of((m - m_new) * scale);
+            m = m_new;
+            l *= alpha;
 #pragma unroll
-            for (int e = 1; e < 8; ++e) top[rt] = fmaxf(top[rt], x[rt][e]);
-            above |= top[rt] > m[rt] + slack;
-        }
-        if (__ballot(above)) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const float m_new = fmaxf(m[rt], max_over_c(top[rt]));
-                const float alpha = exp2_of((m[rt] - m_new) * scale);
-                m[rt] = m_new;
-                l[rt] *= alpha;
-#pragma unroll
-                for (int j = 0; j < J; ++j) o[rt][j] *= alpha;
-            }
+            for (int j = 0; j < J; ++j) o[j] *= alpha;
         }
 
+        // weights: x becomes 2^(score - running maximum)
         if (a.block_lse) {
-            // blocks of 8 or 16 tokens lie side by side in a tile, in 2 or 4 of a lane's 8 places; one of 32 or more
-            // fills it.  `parts` of them; c-th lane groups write the c-th.
-            auto blocks = [&](auto parts_, int rt) {
-                constexpr int parts = decltype(parts_)::value, places_each = 8 / parts;
-                const int r = rt * 16 + n;
-                float* const to = a.block_lse + ((int64_t)s * a.n * a.M + r / g) * a.Hq + kvh * g + r % g;
-                const int64_t step = (int64_t)a.M * a.Hq;
+            // Blocks of 8 or 16 tokens lie side by side in a tile, in 2 or 4 of a lane's 8 places; one of 32 or more
+            // fills it.  Weights are taken against their block's own maximum, summed, and then brought to the running
+            // one, so a block far below the rest still has its sum.
+            auto blocks = [&](auto parts_) {
+                constexpr int parts = decltype(parts_)::value, each = 8 / parts;
+                float* const to = a.block_lse + ((int64_t)s * a.n * a.M + i) * a.Hq + kvh * g + r % g;
                 float mine = -INFINITY;
 #pragma unroll
                 for (int y = 0; y < parts; ++y) {
-                    float bm = x[rt][y * places_each];
+                    float* const xb = x + y * each;
+                    float bm = xb[0];
 #pragma unroll
-                    for (int e = 1; e < places_each; ++e) bm = fmaxf(bm, x[rt][y * places_each + e]);
+                    for (int e = 1; e < each; ++e) bm = fmaxf(bm, xb[e]);
                     bm = fmaxf(max_over_c(bm), kLowest);
                     float bl = 0.f;
+                    const float to_running = exp2_of((bm - m) * scale);
 #pragma unroll
-                    for (int e = 0; e < places_each; ++e) bl += exp2_of((x[rt][y * places_each + e] - bm) * scale);
+                    for (int e = 0; e < each; ++e) {
+                        xb[e] = exp2_of((xb[e] - bm) * scale);
+                        bl += xb[e];
+                        xb[e] *= to_running;
+                    }
                     bl = sum_over_c(bl);
                     if constexpr (parts == 1) {
-                        const float both = fmaxf(wide_m[rt], bm);
-                        wide_l[rt] = wide_l[rt] * exp2_of((wide_m[rt] - both) * scale) + bl * exp2_of((bm - both) * scale);
-                        wide_m[rt] = both;
-                        bl = wide_l[rt];
+                        const float both = fmaxf(wide_m, bm);
+                        wide_l = wide_l * exp2_of((wide_m - both) * scale) + bl * exp2_of((bm - both) * scale);
+                        wide_m = both;
+                        bl = wide_l;
                         bm = both;
                     }
-                    const float log = live[rt] && !(bl <= 0.f) ? (bm * scale + log2_of(bl)) * kLn2 : -INFINITY;
+                    const float log = live && !(bl <= 0.f) ? (bm * scale + log2_of(bl)) * kLn2 : -INFINITY;
                     mine = y == c ? log : mine;
                 }
                 const int tok = t + 32 / parts * c;
                 // of a block wider than a tile: with its last tile, or the sequence's
                 const bool done = parts > 1 || t + 32 >= t1 || bs.block(t + 32) != bs.block(t);
-                if (done && c < parts && r < R && tok < t1) to[bs.block(tok) * step] = mine;
+                if (done && c < parts && r < R && tok < t1) to[bs.block(tok) * (int64_t)a.M * a.Hq] = mine;
                 if (parts == 1 && done) {
-                    wide_m[rt] = kLowest;
-                    wide_l[rt] = 0.f;
+                    wide_m = kLowest;
+                    wide_l = 0.f;
                 }
             };
+            if (bs.B == 16) blocks(std::integral_constant<int, 2>());
+            else if (bs.B == 8) blocks(std::integral_constant<int, 4>());
+            else blocks(std::integral_constant<int, 1>());
+        } else {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                if (bs.B == 16) blocks(std::integral_constant<int, 2>(), rt);
-                else if (bs.B == 8) blocks(std::integral_constant<int, 4>(), rt);
-                else blocks(std::integral_constant<int, 1>(), rt);
-            }
+            for (int e = 0; e < 8; ++e) x[e] = exp2_of((x[e] - m) * scale);
         }
 
-        bf16x8_t hi[RT], lo[RT];
+        u32x4_t wh, wl;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            u32x4_t wh, wl;
+        for (int e = 0; e < 8; ++e) l += x[e];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[rt][e] = exp2_of((x[rt][e] - m[rt]) * scale);
-                l[rt] += x[rt][e];
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                wh[e] = bf16_pair(x[rt][2 * e], x[rt][2 * e + 1]);
-                wl[e] = bf16_pair(x[rt][2 * e] - bf16_lo(wh[e]), x[rt][2 * e + 1] - bf16_hi(wh[e]));
-            }
-            hi[rt] = __builtin_bit_cast(bf16x8_t, wh);
-            lo[rt] = __builtin_bit_cast(bf16x8_t, wl);
+        for (int e = 0; e < 4; ++e) {
+            wh[e] = bf16_pair(x[2 * e], x[2 * e + 1]);
+            wl[e] = bf16_pair(x[2 * e] - bf16_lo(wh[e]), x[2 * e + 1] - bf16_hi(wh[e]));
         }
+        const bf16x8_t hi = __builtin_bit_cast(bf16x8_t, wh), lo = __builtin_bit_cast(bf16x8_t, wl);
 
         // values as bf16 words, J / 2 of each token
         uint32_t vw[8][J / 2];
@@ -690,132 +682,86 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void attend_stream_kernel(Att
                 for (int y = 0; y < VW; ++y) vw[e][y] = vr[e][y];
             }
         }
-        bool odd = false;       // a drafted token's value that is not finite: it must not meet the zero weights of others
-        if (masked && a.M > 1 && t + 32 > ctx) {
+        // first operand of d = J p + j: that value of the lane's 8 tokens
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-#pragma unroll
-                for (int y = 0; y < J / 2; ++y) odd |= not_finite(vw[e][y]);
-        }
-        // first operands of d = J p + 2 y (z = 0) and J p + 2 y + 1 (z = 1)
-        auto transposed = [&](int y, int z) {
+        for (int j = 0; j < J; ++j) {
             u32x4_t w;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                w[e] = __builtin_amdgcn_perm(vw[2 * e + 1][y], vw[2 * e][y], z ? 0x07060302 : 0x05040100);
-            return w;
-        };
-        auto product = [&](u32x4_t w, int j) {
+                w[e] = __builtin_amdgcn_perm(vw[2 * e + 1][j / 2], vw[2 * e][j / 2], j % 2 ? 0x07060302 : 0x05040100);
             const bf16x8_t val = __builtin_bit_cast(bf16x8_t, w);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                o[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, hi[rt], o[rt][j], 0, 0, 0);
-                o[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, lo[rt], o[rt][j], 0, 0, 0);
-            }
-        };
-        if (__ballot(odd) == 0) {
-#pragma unroll
-            for (int j = 0; j < J; ++j) product(transposed(j / 2, j % 2), j);
-        } else {
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const u32x4_t w = transposed(j / 2, j % 2);
-#pragma unroll 1
-                for (int kind = 0; kind < 3; ++kind) {
-                    u32x4_t hit;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) hit[e] = indicator(w[e], kind);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        const f32x4_t count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8_t, hit), ones_of(x[rt]), f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) o[rt][j][v] += count[v] > 0.f ? special(kind) : 0.f;
-                    }
-                }
-                u32x4_t clean;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) clean[e] = finite_only(w[e]);
-                product(clean, j);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, hi, o[j], 0, 0, 0);
+            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, lo, o[j], 0, 0, 0);
         }
         if (next < t1) load_v();
         t = next;
     }
 
+    if (__ballot(odd)) {
+        for (int tok = ctx > t0 ? ctx : t0; tok < t1; ++tok) {
+            if ((tok - t0) / 32 / per % 4 != wave) continue;        // another wave's
+            const char* const from = value_row(a, bs, s, kvh, tok, item);
+            if (from && ((seen >> ((tok - ctx) & 63)) & 1)) {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) m[rt] = fmaxf(m[rt] * scale, kLowest);     // log2 units from here on
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) o[j][v] += not_finite_part<FP8>(from, J * (4 * c + v) + j);
+            }
+        }
+    }
+    m = fmaxf(m * scale, kLowest);      // log2 units from here on
+    l = sum_over_c(l);
 
     // the waves' sums: 2 and 3 into 0 and 1, then 1 into 0
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) l[rt] = sum_over_c(l[rt]);
 #pragma unroll
     for (int round = 2; round >= 1; round >>= 1) {
         if (wave >= round && wave < 2 * round) {
             float* const to = exchange[wave - round];
+            to[4 * J * 64 + lane] = m;
+            to[(4 * J + 1) * 64 + lane] = l;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                to[(RT * J * 4 + 2 * rt) * 64 + lane] = m[rt];
-                to[(RT * J * 4 + 2 * rt + 1) * 64 + lane] = l[rt];
+            for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) to[((rt * J + j) * 4 + v) * 64 + lane] = o[rt][j][v];
-            }
+                for (int v = 0; v < 4; ++v) to[(4 * j + v) * 64 + lane] = o[j][v];
         }
         __syncthreads();
         if (wave < round) {
             const float* const from = exchange[wave];
+            const float m_other = from[4 * J * 64 + lane], m_new = fmaxf(m, m_other);
+            const float f = exp2_of(m - m_new), f_other = exp2_of(m_other - m_new);
+            l = l * f + from[(4 * J + 1) * 64 + lane] * f_other;
+            m = m_new;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const float m_other = from[(RT * J * 4 + 2 * rt) * 64 + lane];
-                const float m_new = fmaxf(m[rt], m_other);
-                const float f = exp2_of(m[rt] - m_new), f_other = exp2_of(m_other - m_new);
-                l[rt] = l[rt] * f + from[(RT * J * 4 + 2 * rt + 1) * 64 + lane] * f_other;
-                m[rt] = m_new;
+            for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int j = 0; j < J; ++j)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        o[rt][j][v] = o[rt][j][v] * f + from[((rt * J + j) * 4 + v) * 64 + lane] * f_other;
-            }
+                for (int v = 0; v < 4; ++v) o[j][v] = o[j][v] * f + from[(4 * j + v) * 64 + lane] * f_other;
         }
         __syncthreads();
     }
-    if (wave != 0) return;
-    const bool whole = run >= len;      // no other run: the result
+    if (wave != 0 || r >= R) return;
+    const bool none = !live || l == 0.f;
+    if (run >= len) {       // no other run: the result
+        const float f = none ? 0.f : a.cache.v_scale / l;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int r = rt * 16 + n;
-        if (r >= R) continue;
-        const int64_t row = ((int64_t)s * a.M + r / g) * a.Hq + kvh * g + r % g;
-        const bool none = !live[rt] || l[rt] == 0.f;
-        if (whole) {
-            const float f = none ? 0.f : a.cache.v_scale / l[rt];
+        for (int v = 0; v < 4; ++v) {
+            uint32_t w[J / 2];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                uint32_t w[J / 2];
+            for (int y = 0; y < J / 2; ++y) w[y] = none ? 0u : bf16_pair(o[2 * y][v] * f, o[2 * y + 1][v] * f);
+            uint32_t* const to = reinterpret_cast<uint32_t*>(a.out + row * D + J * (4 * c + v));
 #pragma unroll
-                for (int y = 0; y < J / 2; ++y)
-                    w[y] = none ? 0u : bf16_pair(o[rt][2 * y][v] * f, o[rt][2 * y + 1][v] * f);
-                uint32_t* const to = reinterpret_cast<uint32_t*>(a.out + row * D + J * (4 * c + v));
-#pragma unroll
-                for (int y = 0; y < J / 2; ++y) to[y] = w[y];
-            }
-            if (a.lse && c == 0) a.lse[row] = none ? -INFINITY : (m[rt] + log2_of(l[rt])) * kLn2;
-        } else {
-            const int64_t which = ((int64_t)s * a.Hk + kvh) * sp.runs + split;
-            float* const to = part_sums(a, sp, which, R) + (int64_t)r * D;
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-#pragma unroll
-                for (int y = 0; y < J / 4; ++y)
-                    *reinterpret_cast<float4*>(to + J * (4 * c + v) + 4 * y) =
-                        make_float4(none ? 0.f : o[rt][4 * y][v], none ? 0.f : o[rt][4 * y + 1][v],
-                                    none ? 0.f : o[rt][4 * y + 2][v], none ? 0.f : o[rt][4 * y + 3][v]);
-            if (c == 0) part_stats(a, sp, which, R)[r] = make_float2(none ? kLowest : m[rt], none ? 0.f : l[rt]);
+            for (int y = 0; y < J / 2; ++y) to[y] = w[y];
         }
+        if (a.lse && c == 0) a.lse[row] = none ? -INFINITY : (m + log2_of(l)) * kLn2;
+    } else if (live) {
+        const int64_t which = ((int64_t)s * a.Hk + kvh) * sp.runs + split;
+        float* const to = part_sums(a, sp, which, R) + (int64_t)r * D;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int y = 0; y < J / 4; ++y)
+                *reinterpret_cast<float4*>(to + J * (4 * c + v) + 4 * y) =
+                    make_float4(o[4 * y][v], o[4 * y + 1][v], o[4 * y + 2][v], o[4 * y + 3][v]);
+        if (c == 0) part_stats(a, sp, which, R)[r] = make_float2(m, l);
     }
 }
 
@@ -895,6 +841,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
     constexpr int KS = D / 16, DT = D / 32;
     constexpr int kRowWaves = 4 / WK;
     __shared__ __attribute__((aligned(16))) char lds[4 * T::kTile];     // keys 0, keys 1, values 0, values 1
+    __shared__ int any_odd;         // a drafted token's value is not finite
 
     const TreePlace at = tree_place(a, sp, groups);
     if (at.s >= a.S) return;
@@ -936,7 +883,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
         q[k] = bf16x8_t{};
-        if (live) q[k] = load8(a.q + row * D + 16 * k + 8 * f);
+        if (live) q[k] = signed_by(a.scale, load8(a.q + row * D + 16 * k + 8 * f));
     }
 
     const int64_t item = FP8 ? 1 : 2;
@@ -971,12 +918,22 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
             }
         }
     };
-    auto store_tile = [&](int buf) {
+    auto store_tile = [&](int buf, int t) {
         char* const kt = lds + buf * T::kTile;
         char* const vt = lds + (2 + buf) * T::kTile;
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             const int id = threadIdx.x + 256 * x, tok = id / CR, piece = id % CR;
+            if (t + 64 > ctx && t + tok >= ctx) {       // drafted: only what is finite enters the products
+                bool odd = false;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const uint32_t finite = FP8 ? finite_only_fp8(vs[x][y]) : finite_only(vs[x][y]);
+                    odd |= finite != vs[x][y];
+                    vs[x][y] = finite;
+                }
+                if (odd) any_odd = 1;
+            }
             if constexpr (FP8) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
@@ -1002,15 +959,17 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
     float m = kLowest, l = 0.f, wide_m = kLowest, wide_l = 0.f;
-    const float scale = a.scale * a.cache.k_scale * kLog2e;
+    const float scale = fabsf(a.scale) * a.cache.k_scale * kLog2e, slack = 8.f / scale;     // as in the stream kernel
     const int l16 = lane & 15;
 
+    if (threadIdx.x == 0) any_odd = 0;
+    __syncthreads();
     int slot = entry_of(t0);
     int64_t off = offset_of(t0, slot);
     uint64_t nowhere = __ballot(off < 0), nowhere_next = 0;
     load_tile(off);
     slot = entry_of(t0 + 64);
-    store_tile(0);
+    store_tile(0, t0);
     __syncthreads();
     for (int t = t0, buf = 0; t < t1; t += 64, buf ^= 1) {
         const bool more = t + 64 < t1;
@@ -1033,176 +992,150 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
                 const uint32_t past = t1 - th < 32 ? ~0u << (t1 - th) : 0u;
                 if (dead & ~past) atomicOr(a.err, DEVERR_TABLE);
             }
+            if (!wave_live) {       // empty rows in a workgroup that has others
+                if (a.block_lse && r < R && (th == t0 || bs.block(th) != bs.block(th - 1) || bs.B < 32))
+                    for (int b = bs.block(th) + f; b <= bs.block(th + 31 < t1 ? th + 31 : t1 - 1); b += 2)
+                        block_row[b * block_step] = -INFINITY;
+                continue;
+            }
             float x[16];
-            if (wave_live) {
-                f32x16_t acc = f32x16_t{};
+            {
+                // two chains of products
+                f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     const bf16x8_t key = __builtin_bit_cast(
                         bf16x8_t, *reinterpret_cast<const u32x4_t*>(kt + T::key(32 * half + n, 2 * k + f)));
-                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc, 0, 0, 0);
+                    acc[k % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc[k % 2], 0, 0, 0);
                 }
 #pragma unroll
-                for (int v = 0; v < 16; ++v) x[v] = acc[v] * scale;
-                if (masked) {
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        const int in = v % 4 + 8 * (v / 4) + 4 * f, place = th + in - ctx;
-                        const bool sees = !((dead >> in) & 1) && (place < 0 || ((seen >> (place & 63)) & 1));
-                        x[v] = sees ? x[v] : -INFINITY;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < 16; ++v) x[v] = -INFINITY;
+                for (int v = 0; v < 16; ++v) x[v] = acc[0][v] + acc[1][v];
             }
-
-            if (a.block_lse) {
-                // 8-token blocks are quads of v, 16-token ones pairs of quads; one of 32 or more fills the half
-                const int parts = bs.B >= 32 ? 1 : 32 / bs.B;
-                float bm[4], bl[4];
+            if (masked) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    bm[y] = fmaxf(fmaxf(x[4 * y], x[4 * y + 1]), fmaxf(x[4 * y + 2], x[4 * y + 3]));
-                if (parts <= 2) {
-                    bm[0] = bm[1] = fmaxf(bm[0], bm[1]);
-                    bm[2] = bm[3] = fmaxf(bm[2], bm[3]);
-                }
-                if (parts == 1) bm[0] = bm[1] = bm[2] = bm[3] = fmaxf(bm[0], bm[2]);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    bm[y] = fmaxf(max_over_f(bm[y]), kLowest);
-                    bl[y] = 0.f;
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) bl[y] += exp2_of(x[4 * y + v] - bm[y]);
-                }
-                if (parts <= 2) {
-                    bl[0] = bl[0] + bl[1];
-                    bl[2] = bl[2] + bl[3];
-                }
-                if (parts == 1) bl[0] += bl[2];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) bl[y] = sum_over_f(bl[y]);
-                if (parts > 1) {
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int tok = th + 8 * y;
-                        const bool mine = parts == 4 ? f == y % 2 : (y % 2 == 0 && f == y / 2);
-                        if (mine && r < R && tok < t1)
-                            block_row[bs.block(tok) * block_step] =
-                                live && !(bl[y] <= 0.f) ? (bm[y] + log2_of(bl[y])) * kLn2 : -INFINITY;
-                    }
-                } else {
-                    const float top = fmaxf(wide_m, bm[0]);
-                    wide_l = wide_l * exp2_of(wide_m - top) + bl[0] * exp2_of(bm[0] - top);
-                    wide_m = top;
-                    if (th + 32 >= t1 || (th + 32) % bs.B == 0) {
-                        if (f == 0 && r < R)
-                            block_row[bs.block(th) * block_step] =
-                                live && !(wide_l <= 0.f) ? (wide_m + log2_of(wide_l)) * kLn2 : -INFINITY;
-                        wide_m = kLowest;
-                        wide_l = 0.f;
-                    }
+                for (int v = 0; v < 16; ++v) {
+                    const int in = v % 4 + 8 * (v / 4) + 4 * f, place = th + in - ctx;
+                    const bool sees = !((dead >> in) & 1) && (place < 0 || ((seen >> (place & 63)) & 1));
+                    x[v] = sees ? x[v] : -INFINITY;
                 }
             }
-            if (!wave_live) continue;
 
             float top = x[0];
 #pragma unroll
             for (int v = 1; v < 16; ++v) top = fmaxf(top, x[v]);
-            if (__ballot(top > m + 8.f)) {
+            if (__ballot(top > m + slack)) {
                 const float m_new = fmaxf(m, max_over_f(top));
-                const float alpha = exp2_of(m - m_new);
+                const float alpha = exp2_of((m - m_new) * scale);
                 m = m_new;
                 l *= alpha;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[d] *= alpha;
             }
-            bf16x8_t hi[2], lo[2];
+
+            // weights, as in the stream kernel: 8-token blocks are quads of v, 16-token ones pairs of quads
+            if (a.block_lse) {
+                auto blocks = [&](auto parts_) {
+                    constexpr int parts = decltype(parts_)::value, each = 16 / parts;
+                    float mine[parts >= 2 ? parts / 2 : 1];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                u32x4_t wh, wl;
+                    for (int y = 0; y < parts; ++y) {
+                        float* const xb = x + y * each;
+                        float bm = xb[0];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[8 * y + e] = exp2_of(x[8 * y + e] - m);
-                    l += x[8 * y + e];
-                }
+                        for (int e = 1; e < each; ++e) bm = fmaxf(bm, xb[e]);
+                        bm = fmaxf(max_over_f(bm), kLowest);
+                        float bl = 0.f;
+                        const float to_running = exp2_of((bm - m) * scale);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    wh[e] = bf16_pair(x[8 * y + 2 * e], x[8 * y + 2 * e + 1]);
-                    wl[e] = bf16_pair(x[8 * y + 2 * e] - bf16_lo(wh[e]), x[8 * y + 2 * e + 1] - bf16_hi(wh[e]));
-                }
-                hi[y] = __builtin_bit_cast(bf16x8_t, wh);
-                lo[y] = __builtin_bit_cast(bf16x8_t, wl);
+                        for (int e = 0; e < each; ++e) {
+                            xb[e] = exp2_of((xb[e] - bm) * scale);
+                            bl += xb[e];
+                            xb[e] *= to_running;
+                        }
+                        bl = sum_over_f(bl);
+                        if constexpr (parts == 1) {
+                            const float both = fmaxf(wide_m, bm);
+                            wide_l = wide_l * exp2_of((wide_m - both) * scale) + bl * exp2_of((bm - both) * scale);
+                            wide_m = both;
+                            bl = wide_l;
+                            bm = both;
+                        }
+                        const float log = live && !(bl <= 0.f) ? (bm * scale + log2_of(bl)) * kLn2 : -INFINITY;
+                        mine[y / 2] = y % 2 == f || parts == 1 ? log : mine[y / 2];
+                    }
+                    const bool done = parts > 1 || th + 32 >= t1 || bs.block(th + 32) != bs.block(th);
+#pragma unroll
+                    for (int y = 0; y < (parts >= 2 ? parts / 2 : 1); ++y) {
+                        const int tok = th + (parts == 1 ? 0 : 32 / parts * (2 * y + f));
+                        if (done && r < R && tok < t1 && (parts > 1 || f == 0))
+                            block_row[bs.block(tok) * block_step] = mine[y];
+                    }
+                    if (parts == 1 && done) {
+                        wide_m = kLowest;
+                        wide_l = 0.f;
+                    }
+                };
+                if (bs.B == 16) blocks(std::integral_constant<int, 2>());
+                else if (bs.B == 8) blocks(std::integral_constant<int, 4>());
+                else blocks(std::integral_constant<int, 1>());
+            } else {
+#pragma unroll
+                for (int v = 0; v < 16; ++v) x[v] = exp2_of((x[v] - m) * scale);
             }
+#pragma unroll
+            for (int v = 0; v < 16; ++v) l += x[v];
+
             // 8 tokens' values of one d: two transpose reads
             auto value_of = [&](int d, int y) {
-                bf16x8_t out;
-                i16x4_t part[2];
+                struct { i16x4_t p[2]; } both;
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const int tok = 32 * half + 16 * y + 8 * z + 4 * f + l16 / 4;
                     const int col = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (l16 % 4);
-                    part[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    both.p[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                         (lds_i16x4_t*)(vt + T::value(tok, col / 8) + 2 * (col % 8)));
                 }
-                struct { i16x4_t p[2]; } both = {{part[0], part[1]}};
-                out = __builtin_bit_cast(bf16x8_t, both);
-                return out;
+                return __builtin_bit_cast(bf16x8_t, both);
             };
-            bool odd = false;       // as in the stream kernel: a drafted token's value that is not finite
-            if (masked && th + 32 > ctx) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                u32x4_t wh, wl;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float u = x[8 * y + 2 * e], w = x[8 * y + 2 * e + 1];
+                    wh[e] = bf16_pair(u, w);
+                    wl[e] = bf16_pair(u - bf16_lo(wh[e]), w - bf16_hi(wh[e]));
+                }
+                bf16x8_t val[DT];
+#pragma unroll
+                for (int d = 0; d < DT; ++d) val[d] = value_of(d, y);
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val[d], __builtin_bit_cast(bf16x8_t, wh), o[d], 0, 0, 0);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const u32x4_t w = __builtin_bit_cast(u32x4_t, value_of(d, y));
-                        odd |= not_finite(w[0]) || not_finite(w[1]) || not_finite(w[2]) || not_finite(w[3]);
-                    }
-            }
-            auto product = [&](bool clean) {
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        bf16x8_t val = value_of(d, y);
-                        if (clean) {
-                            u32x4_t w = __builtin_bit_cast(u32x4_t, val);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] = finite_only(w[e]);
-                            val = __builtin_bit_cast(bf16x8_t, w);
-                        }
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val, hi[y], o[d], 0, 0, 0);
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val, lo[y], o[d], 0, 0, 0);
-                    }
-            };
-            if (__ballot(odd) == 0) {
-                product(false);
-            } else {
-#pragma unroll 1
-                for (int kind = 0; kind < 3; ++kind)
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        f32x16_t count = f32x16_t{};
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            u32x4_t w = __builtin_bit_cast(u32x4_t, value_of(d, y));
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] = indicator(w[e], kind);
-                            count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, w),
-                                                                            ones_of(x + 8 * y), count, 0, 0, 0);
-                        }
-#pragma unroll
-                        for (int v = 0; v < 16; ++v) o[d][v] += count[v] > 0.f ? special(kind) : 0.f;
-                    }
-                product(true);
+                for (int d = 0; d < DT; ++d)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val[d], __builtin_bit_cast(bf16x8_t, wl), o[d], 0, 0, 0);
             }
         }
-        if (more) store_tile(buf ^ 1);
+        if (more) store_tile(buf ^ 1, t + 64);
         nowhere = nowhere_next;
         __syncthreads();
     }
 
+    if (any_odd) {
+        for (int tok = ctx > t0 ? ctx : t0; tok < t1; ++tok) {
+            if (WK == 2 && (tok - t0) / 32 % 2 != wave % 2) continue;       // the other wave's half
+            const char* const from = value_row(a, bs, s, kvh, tok, item);
+            if (from && ((seen >> ((tok - ctx) & 63)) & 1)) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        o[d][v] += not_finite_part<FP8>(from, 32 * d + v % 4 + 8 * (v / 4) + 4 * f);
+            }
+        }
+    }
+    m = fmaxf(m * scale, kLowest);      // log2 units from here on
     l = sum_over_f(l);
     if constexpr (WK == 2) {
         // the pair's sums, through the (now unused) stage
@@ -1308,9 +1241,10 @@ hipError_t launch_fast(const AttendArgs& a, Kind kind, const Split& sp, hipStrea
     const BlockSize bs = block_size(a.B);
     int64_t grid = (int64_t)a.S * a.Hk * sp.runs;
     if (kind == Kind::Stream) {
+        const int groups = (queries_of(a) + 15) / 16;
+        grid = ((int64_t)a.S * sp.runs + 7) / 8 * 8 * a.Hk * groups;
         if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
-        if (queries_of(a) <= 16) attend_stream_kernel<D, FP8, 1><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs);
-        else attend_stream_kernel<D, FP8, 2><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs);
+        attend_stream_kernel<D, FP8><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs, groups);
         return hipGetLastError();
     }
     const int groups = tree_groups(a);
@@ -1319,6 +1253,14 @@ hipError_t launch_fast(const AttendArgs& a, Kind kind, const Split& sp, hipStrea
     if (tree_pairs(a)) attend_tree_kernel<D, FP8, 2><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs, groups);
     else attend_tree_kernel<D, FP8, 1><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs, groups);
     return hipGetLastError();
+}
+
+// Four waves a row where there are runs enough for them, else one (131072 tokens
+// of one sequence in 64 runs are 32 rows; a batch's 65536 rows have few runs).
+template <int D>
+void launch_join(const AttendArgs& a, const Split& sp, uint32_t rows, hipStream_t stream) {
+    if (sp.runs > 8) attend_join_kernel<D, 4><<<rows, 256, 0, stream>>>(a, sp);
+    else attend_join_kernel<D, 1><<<(rows + 3) / 4, 256, 0, stream>>>(a, sp);
 }
 
 }  // namespace
@@ -1355,10 +1297,8 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     if (a.D == 64) e = a.cache.fp8 ? launch_fast<64, true>(a, kind, sp, stream) : launch_fast<64, false>(a, kind, sp, stream);
     else e = a.cache.fp8 ? launch_fast<128, true>(a, kind, sp, stream) : launch_fast<128, false>(a, kind, sp, stream);
     if (e != hipSuccess || sp.runs <= 1) return e;
-    // four waves a row where there are runs enough for them (131072 tokens of one sequence in 64 runs: 15.6 us with one
-    // thread after another reading the maxima; 65536 rows of 4 runs want one wave each)
-    if (sp.runs > 8) attend_join_kernel<4><<<row_grid, 256, 0, stream>>>(a, sp);
-    else attend_join_kernel<1><<<(row_grid + 3) / 4, 256, 0, stream>>>(a, sp);
+    if (a.D == 64) launch_join<64>(a, sp, row_grid, stream);
+    else launch_join<128>(a, sp, row_grid, stream);
     return hipGetLastError();
 }
 
