@@ -892,49 +892,59 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
     const char* const vp = static_cast<const char*>(a.cache.v) + head_off;
     const int32_t* const table = a.tables ? a.tables + (int64_t)s * a.n : nullptr;
 
-    // lane x of every wave keeps where token x of a tile lies (bytes from the cache's start), -1 if nowhere
+    // Staging.  Lane x of every wave finds where token x of a tile lies (bytes from the head's start; 0 and a bit in
+    // `nowhere` for a token past the run's end or in a block with an invalid entry), and the threads take the offsets
+    // of the tokens whose pieces they stage from there.
     auto entry_of = [&](int t) {
         const int tok = t + lane;
         if (tok >= t1) return -1;
         const int b = bs.block(tok);
         return table ? table[b] : b;
     };
-    auto offset_of = [&](int t, int slot) -> int64_t {
+    auto offset_of = [&](int t, int slot, uint64_t& nowhere) -> int64_t {
         const int tok = t + lane;
-        if (tok >= t1 || slot < 0 || slot >= a.N) return -1;
-        return (slot * a.cache.block_stride + (int64_t)(tok - bs.block(tok) * bs.B) * a.cache.token_stride) * item;
+        const bool none = tok >= t1 || slot < 0 || slot >= a.N;
+        nowhere = __ballot(none);
+        return none ? 0 : (slot * a.cache.block_stride + (int64_t)(tok - bs.block(tok) * bs.B) * a.cache.token_stride) * item;
     };
+    const int my_tok = threadIdx.x / CR, my_piece = threadIdx.x % CR;     // and tokens 256 / CR further on
     u32x4_t ks[NR], vs[NR];
     auto load_tile = [&](int64_t off) {
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
-            const int id = threadIdx.x + 256 * x;
-            const int64_t o = __shfl(off, id / CR);
-            ks[x] = u32x4_t{0, 0, 0, 0};
-            vs[x] = u32x4_t{0, 0, 0, 0};
-            if (o >= 0) {
-                ks[x] = *reinterpret_cast<const u32x4_t*>(kp + o + 16 * (id % CR));
-                vs[x] = *reinterpret_cast<const u32x4_t*>(vp + o + 16 * (id % CR));
-            }
+            const int from = my_tok + 256 / CR * x;
+            const int64_t o = ((int64_t)__shfl((int)(off >> 32), from) << 32 | (uint32_t)__shfl((int)off, from)) +
+                              16 * my_piece;
+            ks[x] = *reinterpret_cast<const u32x4_t*>(kp + o);
+            vs[x] = *reinterpret_cast<const u32x4_t*>(vp + o);
         }
     };
-    auto store_tile = [&](int buf, int t) {
-        char* const kt = lds + buf * T::kTile;
-        char* const vt = lds + (2 + buf) * T::kTile;
+    // 256 / CR is a multiple of 16, so a thread's rows share their permutation and lie a fixed step apart
+    const int k_to = T::key(my_tok, FP8 ? 2 * my_piece : my_piece), v_to = T::value(my_tok, FP8 ? 2 * my_piece : my_piece);
+    auto store_tile = [&](int buf, int t, uint64_t nowhere) {
+        if (t + 64 > ctx || nowhere != 0) {
+            bool odd = false;
 #pragma unroll
-        for (int x = 0; x < NR; ++x) {
-            const int id = threadIdx.x + 256 * x, tok = id / CR, piece = id % CR;
-            if (t + 64 > ctx && t + tok >= ctx) {       // drafted: only what is finite enters the products
-                bool odd = false;
+            for (int x = 0; x < NR; ++x) {
+                const int tok = my_tok + 256 / CR * x;
+                const bool none = (nowhere >> tok) & 1, tail = t + tok >= ctx;
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const uint32_t finite = FP8 ? finite_only_fp8(vs[x][y]) : finite_only(vs[x][y]);
-                    odd |= finite != vs[x][y];
-                    vs[x][y] = finite;
+                    const uint32_t w = none ? 0u : vs[x][y];
+                    const uint32_t finite = FP8 ? finite_only_fp8(w) : finite_only(w);
+                    odd |= tail && finite != w;
+                    vs[x][y] = tail ? finite : w;
                 }
-                if (odd) any_odd = 1;
             }
+            if (odd) any_odd = 1;
+        }
+        char* const kt = lds + buf * T::kTile + k_to;
+        char* const vt = lds + (2 + buf) * T::kTile + v_to;
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            constexpr int kStep = 256 / CR * T::kRow;
             if constexpr (FP8) {
+                // the piece's two halves are pieces 2 p and 2 p + 1: the permutation flips at most their last bit
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     u32x4_t wk, wv;
@@ -945,42 +955,42 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
                         wv[2 * z] = fp8x2_to_bf16<false>(vs[x][2 * y + z]);
                         wv[2 * z + 1] = fp8x2_to_bf16<true>(vs[x][2 * y + z]);
                     }
-                    *reinterpret_cast<u32x4_t*>(kt + T::key(tok, 2 * piece + y)) = wk;
-                    *reinterpret_cast<u32x4_t*>(vt + T::value(tok, 2 * piece + y)) = wv;
+                    *reinterpret_cast<u32x4_t*>(lds + buf * T::kTile + (k_to ^ (16 * y)) + x * kStep) = wk;
+                    *reinterpret_cast<u32x4_t*>(lds + (2 + buf) * T::kTile + (v_to ^ (16 * y)) + x * kStep) = wv;
                 }
             } else {
-                *reinterpret_cast<u32x4_t*>(kt + T::key(tok, piece)) = ks[x];
-                *reinterpret_cast<u32x4_t*>(vt + T::value(tok, piece)) = vs[x];
+                *reinterpret_cast<u32x4_t*>(kt + x * kStep) = ks[x];
+                *reinterpret_cast<u32x4_t*>(vt + x * kStep) = vs[x];
             }
         }
     };
+    // A lane's reads: key row n, piece 2 k + f; value row 4 f + l16 / 4, column 32 d + 16 * (lane / 16 % 2) + 4 * (l16 %
+    // 4).  Rows a multiple of 16 (keys) or 4 (values) further on have the same permutation, and it is an exclusive or,
+    // so k and d enter as one.
+    const int l16 = lane & 15;
+    const int k_from = T::key(n, f);
+    const int v_from = T::value(4 * f + l16 / 4, 2 * ((lane >> 4) & 1) + l16 % 4 / 2) + 8 * (l16 % 2);
 
     f32x16_t o[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
     float m = kLowest, l = 0.f, wide_m = kLowest, wide_l = 0.f;
     const float scale = fabsf(a.scale) * a.cache.k_scale * kLog2e, slack = 8.f / scale;     // as in the stream kernel
-    const int l16 = lane & 15;
 
     if (threadIdx.x == 0) any_odd = 0;
     __syncthreads();
+    uint64_t nowhere, nowhere_next = 0;
     int slot = entry_of(t0);
-    int64_t off = offset_of(t0, slot);
-    uint64_t nowhere = __ballot(off < 0), nowhere_next = 0;
-    load_tile(off);
+    load_tile(offset_of(t0, slot, nowhere));
     slot = entry_of(t0 + 64);
-    store_tile(0, t0);
+    store_tile(0, t0, nowhere);
     __syncthreads();
     for (int t = t0, buf = 0; t < t1; t += 64, buf ^= 1) {
         const bool more = t + 64 < t1;
         if (more) {
-            off = offset_of(t + 64, slot);
-            nowhere_next = __ballot(off < 0);
-            load_tile(off);
+            load_tile(offset_of(t + 64, slot, nowhere_next));
             slot = entry_of(t + 128);
         }
-        const char* const kt = lds + buf * T::kTile;
-        const char* const vt = lds + (2 + buf) * T::kTile;
 #pragma unroll 1
         for (int half = WK == 2 ? wave % 2 : 0; half < (WK == 2 ? wave % 2 + 1 : 2); ++half) {
             const int th = t + 32 * half;
@@ -1001,11 +1011,12 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
             float x[16];
             {
                 // two chains of products
+                const char* const kt0 = lds + buf * T::kTile + 32 * half * T::kRow;
                 f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     const bf16x8_t key = __builtin_bit_cast(
-                        bf16x8_t, *reinterpret_cast<const u32x4_t*>(kt + T::key(32 * half + n, 2 * k + f)));
+                        bf16x8_t, *reinterpret_cast<const u32x4_t*>(kt0 + (k_from ^ (32 * k))));
                     acc[k % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc[k % 2], 0, 0, 0);
                 }
 #pragma unroll
@@ -1086,15 +1097,13 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
             for (int v = 0; v < 16; ++v) l += x[v];
 
             // 8 tokens' values of one d: two transpose reads
+            const char* const vt0 = lds + (2 + buf) * T::kTile + 32 * half * T::kRow;
             auto value_of = [&](int d, int y) {
                 struct { i16x4_t p[2]; } both;
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const int tok = 32 * half + 16 * y + 8 * z + 4 * f + l16 / 4;
-                    const int col = 32 * d + 16 * ((lane >> 4) & 1) + 4 * (l16 % 4);
+                for (int z = 0; z < 2; ++z)
                     both.p[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (lds_i16x4_t*)(vt + T::value(tok, col / 8) + 2 * (col % 8)));
-                }
+                        (lds_i16x4_t*)(vt0 + (v_from ^ (64 * d)) + (16 * y + 8 * z) * T::kRow));
                 return __builtin_bit_cast(bf16x8_t, both);
             };
 #pragma unroll
@@ -1117,7 +1126,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
                     o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val[d], __builtin_bit_cast(bf16x8_t, wl), o[d], 0, 0, 0);
             }
         }
-        if (more) store_tile(buf ^ 1, t + 64);
+        if (more) store_tile(buf ^ 1, t + 64, nowhere_next);
         nowhere = nowhere_next;
         __syncthreads();
     }
