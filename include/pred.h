@@ -458,7 +458,8 @@ int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int6
  * does not reach a row that cannot see it.  Lengths outside their range are
  * clamped, and a block whose table entry is outside [0, max_blocks) is left out
  * of every sum; both raise the device error word.  head_dim <= 256
- * (PRED_ERR_UNSUPPORTED above); n_blocks * block_size <= 2^31 - 64. */
+ * (PRED_ERR_UNSUPPORTED above); n_blocks * block_size <= 2^29 (here and in the
+ * two calls below). */
 int pred_attend(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32_t n_rows, const uint64_t* tree,
                 const int32_t* block_tables, int64_t n_blocks, int32_t n_seqs, const int32_t* kv_len,
                 const int32_t* draft_len, float scale, pred_bf16* out, float* lse, float* block_lse, void* workspace,

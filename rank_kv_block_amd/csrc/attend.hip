@@ -131,31 +131,141 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
         a.lse[((int64_t)s * a.M + i) * a.Hq + h] = none ? -INFINITY : (top + log2_of(total)) * kLn2;
 }
 
-// ---------------------------------------------------------------- splitting a context
+// ---------------------------------------------------------------- splitting the work
 //
-// A sequence's tokens are cut into up to `splits` runs, a workgroup for each
-// (sequence, kv head, run); with more than one run in use the workgroups write
-// their unnormalised sums, maximum and total, and a second launch joins them.
-// The number of runs comes from the shape alone (the lengths are on the
-// device); the run's length from the sequence's own length, so that a short
-// sequence in a wide table is spread as well as a long one.
-struct Split {
-    int runs;       // most runs a sequence is cut into
+// A workgroup takes an item: one group of `rows` queries of one kv head over
+// one run of a sequence's tokens.  The lengths are on the device, so every
+// workgroup works the split out for itself from all of them: with w_s = tokens
+// of sequence s times its groups that have a live row, a run is about the sum
+// of w_s over the items wanted, so the items are alike however uneven the
+// sequences are.  A sequence of one run gets its result written by its items;
+// of one with more the items write unnormalised sums, maximum and total, and
+// a second launch joins them.
+struct Plan {
+    int slots;      // workgroups the chip holds at once
+    int rounds;     // at most this many times as many items; the runs' rounding adds at most one per sequence, head and
+                    // group
+    int run;        // shorter runs than this are not worth a round more: an item's start and its partial results
     int unit;       // a run is a multiple of this many tokens
+    int rows;       // queries of a group
+    int groups;     // groups of a kv head's queries
 };
 
-// Tokens of a run of a sequence of `len` tokens.
-__device__ inline int run_of(const Split& sp, int len) {
-    const int even = (len + sp.runs - 1) / sp.runs;
-    return (even + sp.unit - 1) / sp.unit * sp.unit;
+// One sequence's share: `first` items (counting one kv head) before its own.
+struct Share {
+    int len, groups, run, runs, first;
+};
+
+struct Item {
+    int s, kvh, group, split;
+    Share share;
+    int slot;       // index of its partial results; -1: no item
+    bool last;      // the last group: it also writes what the rows of dead groups get
+};
+
+__device__ inline int runs_of(int len, int run) { return len > run ? (len + run - 1) / run : 1; }
+
+// Workgroup b of the grid, worked out by every wave alike.  Item f = ((first_s +
+// split * groups) * Hk ..): an XCD (b % 8) takes consecutive items, so the
+// groups that read the same bytes, and the heads whose bytes lie side by side,
+// meet in one L2.
+__device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b) {
+    const int lane = threadIdx.x & 63, g = a.Hq / a.Hk;
+    const int64_t most = (int64_t)a.n * a.B;
+    auto read = [&](int s, int& len, int& groups) {
+        len = 0;
+        groups = 0;
+        if (s < a.S) {
+            len = kv_len_of(a.kv_len, s, most);
+            groups = (draft_len_of(a, s, len) * g + pl.rows - 1) / pl.rows;
+            groups = groups < 1 ? 1 : groups;
+        }
+    };
+    int len0, groups0;      // the first 64 sequences' stay in registers
+    read(lane, len0, groups0);
+    auto sequence = [&](int s0, int& len, int& groups) {
+        if (s0 == 0) {
+            len = len0;
+            groups = groups0;
+        } else {
+            read(s0 + lane, len, groups);
+        }
+    };
+    int64_t total = 0;
+    for (int s0 = 0; s0 < a.S; s0 += 64) {
+        int len, groups;
+        sequence(s0, len, groups);
+        total += (int64_t)len * groups;
+    }
+    if (a.S > 1)
+        for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o);
+    // (lane 0 has a single sequence's) the same in every lane from here on, in scalar registers
+    total = ((int64_t)__builtin_amdgcn_readfirstlane((int)(total >> 32)) << 32 |
+             (uint32_t)__builtin_amdgcn_readfirstlane((int)total)) * a.Hk;
+    const int64_t per_slot = total / pl.slots, rounds = per_slot / pl.run;
+    const int64_t items = (int64_t)pl.slots * (rounds < 1 ? 1 : (rounds < pl.rounds ? rounds : pl.rounds));
+    const int64_t wanted = ((total + items - 1) / items + pl.unit - 1) / pl.unit * pl.unit;
+    const int run = (int)(wanted < pl.unit ? pl.unit : (wanted < 0x7FFFFFFF ? wanted : 0x7FFFFFFF));
+    int count = 0;      // items of one kv head
+    for (int s0 = 0; s0 < a.S; s0 += 64) {
+        int len, groups;
+        sequence(s0, len, groups);
+        count += groups * runs_of(len, run);
+    }
+    if (a.S > 1)
+        for (int o = 32; o >= 1; o >>= 1) count += __shfl_xor(count, o);
+    count = __builtin_amdgcn_readfirstlane(count);
+    const uint32_t all = (uint32_t)count * a.Hk, each = (all + 7) / 8, f = b % 8 * each + b / 8;
+    Item it{};
+    it.slot = -1;
+    if (b / 8 >= each || f >= all) return it;
+    int before = 0;
+    for (int s0 = 0; s0 < a.S; s0 += 64) {
+        int len, groups;
+        sequence(s0, len, groups);
+        const int own = groups * runs_of(len, run);
+        int upto = own;
+        for (int o = 1; o < 64; o <<= 1) {
+            const int x = __shfl_up(upto, o);
+            if (lane >= o) upto += x;
+        }
+        const uint64_t past = __ballot((uint32_t)(before + upto) * a.Hk > f);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            it.s = s0 + at;
+            it.share.first = __builtin_amdgcn_readlane(before + upto - own, at);
+            it.share.len = __builtin_amdgcn_readlane(len, at);
+            it.share.groups = __builtin_amdgcn_readlane(groups, at);
+            break;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    it.share.runs = runs_of(it.share.len, run);
+    // the sequence's runs, evened out
+    const int even_run = (it.share.len + it.share.runs - 1) / it.share.runs;
+    it.share.run = it.share.runs == 1 ? run : (even_run + pl.unit - 1) / pl.unit * pl.unit;
+    uint32_t in = f - (uint32_t)it.share.first * a.Hk;
+    it.slot = (int)f;
+    it.group = (int)(in % it.share.groups);
+    in /= it.share.groups;
+    it.kvh = (int)(in % a.Hk);
+    it.split = (int)(in / a.Hk);
+    it.last = it.group == it.share.groups - 1;
+    return it;
 }
 
-// Partial results: sums [S, Hk, runs, R, D], then (maximum, total) [S, Hk, runs, R].
-__device__ inline float* part_sums(const AttendArgs& a, const Split& sp, int64_t which, int R) {
-    return static_cast<float*>(a.ws) + which * R * a.D;
+// Workspace: each sequence's share, then [items, rows, D] sums, then [items,
+// rows] (maximum, total).
+__device__ inline Share* shares_of(const AttendArgs& a) { return static_cast<Share*>(a.ws); }
+__host__ __device__ inline int64_t share_bytes(int64_t S) { return (S * (int64_t)sizeof(Share) + 15) / 16 * 16; }
+__device__ inline float* part_sums(const AttendArgs& a, const Plan& pl, int64_t slot) {
+    return reinterpret_cast<float*>(static_cast<char*>(a.ws) + share_bytes(a.S)) + slot * pl.rows * a.D;
 }
-__device__ inline float2* part_stats(const AttendArgs& a, const Split& sp, int64_t which, int R) {
-    return reinterpret_cast<float2*>(static_cast<float*>(a.ws) + (int64_t)a.S * a.Hk * sp.runs * R * a.D) + which * R;
+__host__ __device__ inline int64_t most_items(const AttendArgs& a, const Plan& pl) {
+    return (int64_t)pl.slots * pl.rounds + (int64_t)a.S * a.Hk * pl.groups;
+}
+__device__ inline float2* part_stats(const AttendArgs& a, const Plan& pl, int64_t slot) {
+    return reinterpret_cast<float2*>(part_sums(a, pl, most_items(a, pl))) + slot * pl.rows;
 }
 
 // Joins a row's runs: out = sum_r 2^(m_r - m) o_r / sum_r 2^(m_r - m) l_r.
@@ -164,38 +274,40 @@ __device__ inline float2* part_stats(const AttendArgs& a, const Split& sp, int64
 // wave adds the runs' sums, 4 values a lane and 64 / (D / 4) runs at a time.
 // Latency bound, so a row with many runs gets four waves.
 template <int D, int WAVES>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Split sp) {
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl) {
     __shared__ float4 sums[4][64];
     __shared__ float2 stats[4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = (int64_t)blockIdx.x * (4 / WAVES) + wave / WAVES;      // [S, M, Hq]
     if (row >= (int64_t)a.S * a.M * a.Hq) return;       // WAVES = 1 only: no barrier follows
     const int h = (int)(row % a.Hq), i = (int)(row / a.Hq % a.M), s = (int)(row / a.Hq / a.M);
-    const int len = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B);
-    const int run = run_of(sp, len);
-    if (len <= run) return;     // one run: it wrote the result itself
+    const Share share = shares_of(a)[s];
+    if (share.runs == 1) return;        // its items wrote the result
+    const int g = a.Hq / a.Hk, r = i * g + h % g, group = r / pl.rows;
     // a row past the draft has no partial sums: its result is that of no run
-    const int runs = i < draft_len_of(a, s, len) ? (len + run - 1) / run : 0;
-    const int g = a.Hq / a.Hk, R = a.M * g, r = i * g + h % g;
-    const int64_t first = ((int64_t)s * a.Hk + h / g) * sp.runs;
+    const int runs = i < draft_len_of(a, s, share.len) ? share.runs : 0;
+    auto slot_of = [&](int split) {
+        return (int64_t)share.first * a.Hk + ((int64_t)split * a.Hk + h / g) * share.groups + group;
+    };
+    const int in_group = r % pl.rows;
     constexpr int lanes = D / 4, groups = 64 / lanes, kAhead = 8;       // kAhead loads in flight a lane
-    const int group = lane / lanes, d4 = lane % lanes;
+    const int part = lane / lanes, d4 = lane % lanes;
     float m = kLowest, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     // this wave's runs: w, w + WAVES, ..; 64 at a time for the statistics, groups * kAhead for the sums
     const int mine = (runs - wave % WAVES + WAVES - 1) / WAVES;
     for (int x0 = 0; x0 < mine; x0 += 64) {
-        auto run_at = [&](int x) { return first + wave % WAVES + (int64_t)x * WAVES; };
+        auto slot_at = [&](int x) { return slot_of(wave % WAVES + x * WAVES); };
         const int count = mine - x0 < 64 ? mine - x0 : 64;
-        const float2 st = lane < count ? part_stats(a, sp, run_at(x0 + lane), R)[r] : make_float2(kLowest, 0.f);
+        const float2 st = lane < count ? part_stats(a, pl, slot_at(x0 + lane))[in_group] : make_float2(kLowest, 0.f);
         float top = m, weight = 0.f;
         for (int y0 = 0; y0 < count; y0 += groups * kAhead) {
             float4 o[kAhead];
 #pragma unroll
             for (int e = 0; e < kAhead; ++e) {
-                const int x = y0 + e * groups + group;
-                o[e] = reinterpret_cast<const float4*>(part_sums(a, sp, run_at(x0 + (x < count ? x : 0)), R) +
-                                                       (int64_t)r * D)[d4];
+                const int x = y0 + e * groups + part;
+                o[e] = reinterpret_cast<const float4*>(part_sums(a, pl, slot_at(x0 + (x < count ? x : 0))) +
+                                                       in_group * D)[d4];
             }
             if (y0 == 0) {
                 top = fmaxf(m, st.x);
@@ -208,7 +320,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Split sp
             }
 #pragma unroll
             for (int e = 0; e < kAhead; ++e) {
-                const int x = y0 + e * groups + group;
+                const int x = y0 + e * groups + part;
                 const float f = __shfl(weight, x & 63);
                 if (x < count) v = make_float4(v.x + f * o[e].x, v.y + f * o[e].y, v.z + f * o[e].z, v.w + f * o[e].w);
             }
@@ -244,7 +356,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Split sp
             v.w += fw * o.w;
         }
     }
-    if (group != 0) return;
+    if (part != 0) return;
     const bool none = l == 0.f;
     const float f = none ? 0.f : a.cache.v_scale / l;
     uint16_t w[4] = {to_bf16(none ? 0.f : v.x * f), to_bf16(none ? 0.f : v.y * f), to_bf16(none ? 0.f : v.z * f),
@@ -407,6 +519,28 @@ struct TableWindow {
     }
 };
 
+// What the rows of groups without a live row get (rows `from` on of a kv head):
+// block_lse -inf for this run's blocks and, where no join follows, output 0
+// and lse -inf.
+__device__ inline void write_dead_rows(const AttendArgs& a, const Item& it, const BlockSize& bs, int from, int t0, int t1) {
+    const int g = a.Hq / a.Hk, dead = a.M * g - from;
+    if (dead <= 0) return;
+    if (a.block_lse && t1 > t0) {
+        const int b0 = bs.block(t0), blocks = bs.block(t1 - 1) + 1 - b0;
+        for (int64_t x = threadIdx.x; x < (int64_t)blocks * dead; x += 256) {
+            const int r = from + (int)(x % dead), b = b0 + (int)(x / dead);
+            a.block_lse[(((int64_t)it.s * a.n + b) * a.M + r / g) * a.Hq + it.kvh * g + r % g] = -INFINITY;
+        }
+    }
+    if (it.share.runs > 1) return;
+    for (int x = threadIdx.x; x < dead * (a.D / 8); x += 256) {
+        const int r = from + x / (a.D / 8), d = x % (a.D / 8) * 8;
+        const int64_t row = ((int64_t)it.s * a.M + r / g) * a.Hq + it.kvh * g + r % g;
+        *reinterpret_cast<u32x4_t*>(a.out + row * a.D + d) = u32x4_t{0, 0, 0, 0};
+        if (a.lse && d == 0) a.lse[row] = -INFINITY;
+    }
+}
+
 // BYTES from a uniform address and a lane's offset, nontemporal (each byte is
 // read once).
 template <int BYTES>
@@ -428,32 +562,28 @@ __device__ inline void stream_load(uint32_t* dst, const char* base, uint32_t off
 }
 
 template <int D, bool FP8>
-__global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Split sp, BlockSize bs, int groups) {
+__global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Plan pl, BlockSize bs) {
     using L = StreamLayout<D, FP8>;
     constexpr int NK = L::NK, W = L::W, H = L::H, KP = L::KP, J = L::J, TPL = L::TPL, VW = L::VW;
     __shared__ float exchange[2][(J * 4 + 2) * 64];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, c = lane >> 4;
-    // the kv heads of a run are 8 workgroups apart: one XCD reads the heads of a token, which lie side by side in
-    // HBM, at about the same time (64 sequences, FP8: 457 us, against 499 with the heads on XCDs of their own)
-    // (and so are the row groups of a head, which read the same bytes)
-    const uint32_t each = 8u * a.Hk * groups, chunk = blockIdx.x / each, in = blockIdx.x % each;
-    const int kvh = in / 8 / groups, group = in / 8 % groups;
-    const int64_t item_run = (int64_t)chunk * 8 + in % 8;
-    const int split = (int)(item_run % sp.runs), s = (int)(item_run / sp.runs);
-    if (s >= a.S) return;
-    const int len = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B), drafted = draft_len_of(a, s, len);
-    if (kvh == 0 && group == 0 && split == 0 && threadIdx.x == 0) check_lengths(a, s, len, drafted);
-    const int ctx = len - drafted;
-    const int run = run_of(sp, len);
-    const int t0 = split * run;
-    if (t0 >= len && split > 0) return;
-    const int t1 = t0 + run < len ? t0 + run : len;
+    const Item it = item_of(a, pl, blockIdx.x);
+    if (it.slot < 0) return;
+    const int s = it.s, kvh = it.kvh, len = it.share.len, drafted = draft_len_of(a, s, len);
+    if (kvh == 0 && it.group == 0 && it.split == 0 && threadIdx.x == 0) {
+        check_lengths(a, s, len, drafted);
+        if (a.ws) shares_of(a)[s] = it.share;
+    }
+    const int ctx = len - drafted, t0 = it.split * it.share.run;
+    const int t1 = t0 + it.share.run < len ? t0 + it.share.run : len;
     const int g = a.Hq / a.Hk, R = a.M * g;
 
+    if (it.last) write_dead_rows(a, it, bs, 16 * (it.group + 1), t0, t1);
+
     // the lane's row, and the queries as second operands
-    const int r = 16 * group + n, i = r / g;
+    const int r = 16 * it.group + n, i = r / g;
     const bool live = r < R && i < drafted;
     const uint64_t seen = live ? tree_word(a, s, i) : 0;
     const int64_t row = ((int64_t)s * a.M + i) * a.Hq + kvh * g + r % g;
@@ -482,7 +612,7 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Spl
     table.used = t1 > 0 ? bs.block(t1 - 1) + 1 : 0;
 
     // this wave's tiles: groups of `per` consecutive ones, every fourth group
-    const int per = sp.unit / 128;
+    const int per = pl.unit / 128;
     auto tile_of = [&](int k) { return per == 1 ? t0 + 32 * (4 * k + wave) : t0 + 32 * ((k / per * 4 + wave) * per + k % per); };
 
     // Where a tile's wave-loads begin (each inside one block), moving the window if the tile is past it.
@@ -740,7 +870,7 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Spl
     }
     if (wave != 0 || r >= R) return;
     const bool none = !live || l == 0.f;
-    if (run >= len) {       // no other run: the result
+    if (it.share.runs == 1) {       // the result
         const float f = none ? 0.f : a.cache.v_scale / l;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -753,15 +883,14 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Spl
         }
         if (a.lse && c == 0) a.lse[row] = none ? -INFINITY : (m + log2_of(l)) * kLn2;
     } else if (live) {
-        const int64_t which = ((int64_t)s * a.Hk + kvh) * sp.runs + split;
-        float* const to = part_sums(a, sp, which, R) + (int64_t)r * D;
+        float* const to = part_sums(a, pl, it.slot) + n * D;
 #pragma unroll
         for (int v = 0; v < 4; ++v)
 #pragma unroll
             for (int y = 0; y < J / 4; ++y)
                 *reinterpret_cast<float4*>(to + J * (4 * c + v) + 4 * y) =
                     make_float4(o[4 * y][v], o[4 * y + 1][v], o[4 * y + 2][v], o[4 * y + 3][v]);
-        if (c == 0) part_stats(a, sp, which, R)[r] = make_float2(m, l);
+        if (c == 0) part_stats(a, pl, it.slot)[n] = make_float2(m, l);
     }
 }
 
@@ -816,24 +945,8 @@ __device__ inline float sum_over_f(float x) {
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 
-// Which (sequence, kv head, run, row group) a workgroup takes: a cache region's
-// row groups are 8 workgroups apart, so they share an XCD's L2.
-struct TreePlace {
-    int s, kvh, split, group;
-};
-__device__ inline TreePlace tree_place(const AttendArgs& a, const Split& sp, int groups) {
-    const uint32_t chunk = blockIdx.x / (8u * groups), in = blockIdx.x % (8u * groups);
-    const int64_t which = (int64_t)chunk * 8 + in % 8;
-    TreePlace r;
-    r.group = in / 8;
-    r.kvh = (int)(which % a.Hk);
-    r.split = (int)(which / a.Hk % sp.runs);
-    r.s = (int)(which / a.Hk / sp.runs);
-    return r;
-}
-
 template <int D, bool FP8, int WK>
-__global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split sp, BlockSize bs, int groups) {
+__global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan pl, BlockSize bs) {
     using T = TreeLds<D>;
     constexpr int RB = D * (FP8 ? 1 : 2);       // bytes of a cache row
     constexpr int CR = RB / 16;                 // 16-byte pieces of it
@@ -843,41 +956,28 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
     __shared__ __attribute__((aligned(16))) char lds[4 * T::kTile];     // keys 0, keys 1, values 0, values 1
     __shared__ int any_odd;         // a drafted token's value is not finite
 
-    const TreePlace at = tree_place(a, sp, groups);
-    if (at.s >= a.S) return;
-    const int s = at.s, kvh = at.kvh;
+    const Item it = item_of(a, pl, blockIdx.x);
+    if (it.slot < 0) return;
+    const int s = it.s, kvh = it.kvh, len = it.share.len, drafted = draft_len_of(a, s, len);
+    if (kvh == 0 && it.group == 0 && it.split == 0 && threadIdx.x == 0) {
+        check_lengths(a, s, len, drafted);
+        if (a.ws) shares_of(a)[s] = it.share;
+    }
+    const int ctx = len - drafted, t0 = it.split * it.share.run;
+    const int t1 = t0 + it.share.run < len ? t0 + it.share.run : len;
+
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, f = lane >> 5;
-    const int len = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B), drafted = draft_len_of(a, s, len);
-    if (kvh == 0 && at.split == 0 && at.group == 0 && threadIdx.x == 0) check_lengths(a, s, len, drafted);
-    const int ctx = len - drafted;
-    const int run = run_of(sp, len);
-    const int t0 = at.split * run;
-    if (t0 >= len && at.split > 0) return;
-    const int t1 = t0 + run < len ? t0 + run : len;
     const int g = a.Hq / a.Hk, R = a.M * g;
-    const int r0 = (at.group * kRowWaves + wave / WK) * 32, r = r0 + n, i = r / g;
+    if (it.last) write_dead_rows(a, it, bs, kRowWaves * 32 * (it.group + 1), t0, t1);
+    const int in_group = wave / WK * 32, r0 = it.group * kRowWaves * 32 + in_group, r = r0 + n, i = r / g;
     const bool live = r < R && i < drafted;
     const bool wave_live = r0 < R && r0 / g < drafted;          // rows of a wave die from the end
-    const bool group_live = at.group * kRowWaves * 32 / g < drafted;
     const uint64_t seen = live ? tree_word(a, s, i) : 0;
     float* const block_row =
         a.block_lse ? a.block_lse + ((int64_t)s * a.n * a.M + i) * a.Hq + kvh * g + r % g : nullptr;
     const int64_t block_step = (int64_t)a.M * a.Hq;
-    const bool whole = run >= len;
     const int64_t row = ((int64_t)s * a.M + i) * a.Hq + kvh * g + r % g;
-
-    if (!group_live) {      // nothing but the empty rows' results
-        if (r >= R || (WK == 2 && wave % 2)) return;
-        if (a.block_lse)
-            for (int b = bs.block(t0) + f; b <= (t1 > t0 ? bs.block(t1 - 1) : -1); b += 2)
-                block_row[b * block_step] = -INFINITY;
-        if (whole) {
-            for (int d = 8 * f; d < D; d += 16) *reinterpret_cast<u32x4_t*>(a.out + row * D + d) = u32x4_t{0, 0, 0, 0};
-            if (a.lse && f == 0) a.lse[row] = -INFINITY;
-        }
-        return;
-    }
 
     bf16x8_t q[KS];
 #pragma unroll
@@ -1170,7 +1270,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
     }
     if (r >= R) return;
     const bool none = !live || l == 0.f;
-    if (whole) {
+    if (it.share.runs == 1) {
         const float inv = none ? 0.f : a.cache.v_scale / l;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
@@ -1183,15 +1283,14 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Split
             }
         if (a.lse && f == 0) a.lse[row] = none ? -INFINITY : (m + log2_of(l)) * kLn2;
     } else if (live) {
-        const int64_t which = ((int64_t)s * a.Hk + kvh) * sp.runs + at.split;
-        float* const to = part_sums(a, sp, which, R) + (int64_t)r * D;
+        float* const to = part_sums(a, pl, it.slot) + (in_group + n) * D;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int y = 0; y < 4; ++y)
                 *reinterpret_cast<float4*>(to + 32 * d + 8 * y + 4 * f) =
                     make_float4(o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]);
-        if (f == 0) part_stats(a, sp, which, R)[r] = make_float2(m, l);
+        if (f == 0) part_stats(a, pl, it.slot)[in_group + n] = make_float2(m, l);
     }
 }
 
@@ -1201,13 +1300,14 @@ enum class Kind { Stream, Tree, Plain };
 
 int queries_of(const AttendArgs& a) { return a.M * (a.Hq / a.Hk); }
 
+constexpr int kRounds = 8;              // most workgroups a CU's places get one after another
 constexpr int kStreamQueries = 32;      // queries per kv head of the stream kernel
 
 Kind kind_of(const AttendArgs& a) {
     const int item = a.cache.fp8 ? 1 : 2;
     if (a.D != 64 && a.D != 128) return Kind::Plain;
     // a block's sum is taken inside a tile, or over whole tiles
-    if (a.block_lse && !(a.B % 32 == 0 || a.B == 16 || a.B == 8)) return Kind::Plain;
+    if (a.block_lse && (!(a.B % 32 == 0 || a.B == 16 || a.B == 8) || a.B > 65536)) return Kind::Plain;
     // 16-byte loads
     if (!aligned_to(a.cache.k, 16) || !aligned_to(a.cache.v, 16) ||
         ((a.cache.block_stride | a.cache.token_stride | a.cache.head_stride) * item) % 16 != 0)
@@ -1223,66 +1323,60 @@ Kind kind_of(const AttendArgs& a) {
 // idle; not where a block's sum spans the halves of a tile that they take.
 bool tree_pairs(const AttendArgs& a) { return queries_of(a) <= 64 && !(a.block_lse && a.B > 32); }
 
-int tree_groups(const AttendArgs& a) {
-    const int rows = tree_pairs(a) ? 64 : 128;
-    return (queries_of(a) + rows - 1) / rows;
+Plan plan_of(const AttendArgs& a, bool tree, bool pairs) {
+    const int queries = queries_of(a);
+    Plan pl;
+    pl.rows = tree ? (pairs ? 64 : 128) : 16;
+    pl.groups = (queries + pl.rows - 1) / pl.rows;
+    if (pl.rows > queries) pl.rows = queries;       // of one group
+    // whole tiles (four waves take one each in the stream kernel), or whole blocks where a block's sum spans tiles
+    pl.unit = tree ? 64 : 128;
+    if (a.block_lse && a.B > 32) pl.unit = tree ? (a.B % 64 == 0 ? a.B : 2 * a.B) : 4 * a.B;
+    // Two workgroups fit a CU.  Items of a batch are of uneven length where a run ends early, so more rounds than one
+    // even them out (64 sequences, FP8: 503 us with 2, 463 with 4, 449 with 6), but a run has to be worth its start
+    // and its partial results (8 sequences of 5k tokens, 13 rows: 75 us with 1, 91 with 2, 109 with 4).
+    pl.slots = 2 * a.n_cu;
+    pl.run = tree ? 2048 : 2560;
+    const int64_t most = (int64_t)a.S * a.n * a.B * pl.groups * a.Hk / pl.slots / pl.run;
+    pl.rounds = most < 1 ? 1 : (most < kRounds ? (int)most : kRounds);
+    return pl;
 }
 
-Split split_of(const AttendArgs& a, bool with_block_lse) {
-    const bool tree = queries_of(a) > kStreamQueries;
-    const int64_t base = (int64_t)a.S * a.Hk * (tree ? tree_groups(a) : 1), most = (int64_t)a.n * a.B;
-    Split sp;
-    // whole tiles (four waves take one each in the stream kernel), or whole blocks where a block's sum spans tiles
-    sp.unit = tree ? 64 : 128;
-    if (with_block_lse && a.B > 32) sp.unit = tree ? (a.B % 64 == 0 ? a.B : 2 * a.B) : 4 * a.B;
-    // two workgroups on every CU, and runs short enough to even out sequences of different lengths
-    int64_t runs = (2 * (int64_t)a.n_cu + base - 1) / base;
-    const int64_t even = most / 4096;
-    if (runs < even) runs = even;
-    const int64_t limit = (most + sp.unit - 1) / sp.unit;
-    if (runs > limit) runs = limit;
-    sp.runs = runs < 1 ? 1 : (int)runs;
-    return sp;
+// Whether a sequence can have more than one run, so that there are partial results.
+bool may_split(const AttendArgs& a, const Plan& pl) { return (int64_t)a.n * a.B > pl.unit; }
+
+size_t plan_bytes(const AttendArgs& a, const Plan& pl) {
+    return may_split(a, pl) ? (size_t)(share_bytes(a.S) + most_items(a, pl) * pl.rows * (a.D + 2) * (int64_t)sizeof(float)) : 0;
 }
 
 template <int D, bool FP8>
-hipError_t launch_fast(const AttendArgs& a, Kind kind, const Split& sp, hipStream_t stream) {
+void launch_fast(const AttendArgs& a, Kind kind, const Plan& pl, uint32_t grid, hipStream_t stream) {
     const BlockSize bs = block_size(a.B);
-    int64_t grid = (int64_t)a.S * a.Hk * sp.runs;
-    if (kind == Kind::Stream) {
-        const int groups = (queries_of(a) + 15) / 16;
-        grid = ((int64_t)a.S * sp.runs + 7) / 8 * 8 * a.Hk * groups;
-        if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
-        attend_stream_kernel<D, FP8><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs, groups);
-        return hipGetLastError();
-    }
-    const int groups = tree_groups(a);
-    grid = (grid + 7) / 8 * 8 * groups;
-    if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
-    if (tree_pairs(a)) attend_tree_kernel<D, FP8, 2><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs, groups);
-    else attend_tree_kernel<D, FP8, 1><<<(uint32_t)grid, 256, 0, stream>>>(a, sp, bs, groups);
-    return hipGetLastError();
+    if (kind == Kind::Stream) attend_stream_kernel<D, FP8><<<grid, 256, 0, stream>>>(a, pl, bs);
+    else if (tree_pairs(a)) attend_tree_kernel<D, FP8, 2><<<grid, 256, 0, stream>>>(a, pl, bs);
+    else attend_tree_kernel<D, FP8, 1><<<grid, 256, 0, stream>>>(a, pl, bs);
 }
 
-// Four waves a row where there are runs enough for them, else one (131072 tokens
-// of one sequence in 64 runs are 32 rows; a batch's 65536 rows have few runs).
+// Four waves a row where a sequence has runs enough for them, else one (131072
+// tokens of one sequence in 64 runs are 32 rows; a batch's 65536 rows have few
+// runs).
 template <int D>
-void launch_join(const AttendArgs& a, const Split& sp, uint32_t rows, hipStream_t stream) {
-    if (sp.runs > 8) attend_join_kernel<D, 4><<<rows, 256, 0, stream>>>(a, sp);
-    else attend_join_kernel<D, 1><<<(rows + 3) / 4, 256, 0, stream>>>(a, sp);
+void launch_join(const AttendArgs& a, const Plan& pl, uint32_t rows, hipStream_t stream) {
+    if ((int64_t)pl.slots * pl.rounds > 8ll * a.S * a.Hk * pl.groups) attend_join_kernel<D, 4><<<rows, 256, 0, stream>>>(a, pl);
+    else attend_join_kernel<D, 1><<<(rows + 3) / 4, 256, 0, stream>>>(a, pl);
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(const AttendArgs& a) {
     if (a.D != 64 && a.D != 128) return 0;
-    // with block_lse the runs are as many or fewer, but up to 64 queries take more workgroups (tree_pairs)
-    AttendArgs b = a;
-    float any;
-    b.block_lse = &any;
-    const int64_t runs[2] = {split_of(a, false).runs, split_of(b, true).runs};
-    const int64_t most = runs[0] > runs[1] ? runs[0] : runs[1];
-    return most <= 1 ? 0 : (size_t)a.S * a.Hk * most * queries_of(a) * (a.D + 2) * sizeof(float);
+    // the most that a call of this shape may need, whatever its cache and whether it asks for block_lse
+    size_t most = 0;
+    for (int pairs = 0; pairs < 2; ++pairs) {
+        const size_t bytes = plan_bytes(a, plan_of(a, queries_of(a) > kStreamQueries, pairs));
+        most = bytes > most ? bytes : most;
+    }
+    return most;
 }
 
 const char* attend_kernel_name(const AttendArgs& a) {
@@ -1301,13 +1395,21 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
         else attend_plain_kernel<false><<<row_grid, 256, 0, stream>>>(a);
         return hipGetLastError();
     }
-    const Split sp = split_of(a, a.block_lse != nullptr);
-    hipError_t e;
-    if (a.D == 64) e = a.cache.fp8 ? launch_fast<64, true>(a, kind, sp, stream) : launch_fast<64, false>(a, kind, sp, stream);
-    else e = a.cache.fp8 ? launch_fast<128, true>(a, kind, sp, stream) : launch_fast<128, false>(a, kind, sp, stream);
-    if (e != hipSuccess || sp.runs <= 1) return e;
-    if (a.D == 64) launch_join<64>(a, sp, row_grid, stream);
-    else launch_join<128>(a, sp, row_grid, stream);
+    const Plan pl = plan_of(a, kind == Kind::Tree, tree_pairs(a));
+    const bool split = may_split(a, pl);
+    AttendArgs b = a;
+    if (!split) b.ws = nullptr;
+    // an XCD's items are numbered from the whole's eighth, rounded up
+    const int64_t grid = (most_items(a, pl) + 7) / 8 * 8;
+    if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
+    if (a.D == 64 && a.cache.fp8) launch_fast<64, true>(b, kind, pl, (uint32_t)grid, stream);
+    else if (a.D == 64) launch_fast<64, false>(b, kind, pl, (uint32_t)grid, stream);
+    else if (a.cache.fp8) launch_fast<128, true>(b, kind, pl, (uint32_t)grid, stream);
+    else launch_fast<128, false>(b, kind, pl, (uint32_t)grid, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !split) return e;
+    if (a.D == 64) launch_join<64>(b, pl, row_grid, stream);
+    else launch_join<128>(b, pl, row_grid, stream);
     return hipGetLastError();
 }
 

@@ -95,14 +95,17 @@ pred::RopeArgs rope_args(pred_t* p, const pred_rope* r, const int32_t* positions
     return a;
 }
 
+// Tokens of a sequence: with 2^29 no sum of lengths, runs and tiles passes 32 bits.
+constexpr int64_t kMostTokens = 1ll << 29;
+
 // The table's extent and the counts shared by the calls over sequences.
 int check_counts(pred_t* p, int64_t n_blocks, int32_t n_seqs, const char* what) {
     if (n_blocks < 0 || n_seqs < 0)
         return fail(PRED_ERR_OUT_OF_RANGE, "%s: negative count (n_blocks %lld, n_seqs %d)", what, (long long)n_blocks,
                     n_seqs);
     int64_t tokens;
-    if (!mul_ok(n_blocks, p->d.block_size, &tokens) || tokens > 2147483647LL - 63)
-        return fail(PRED_ERR_OUT_OF_RANGE, "%s: %lld blocks of %d tokens are above 2^31 - 64 tokens", what,
+    if (!mul_ok(n_blocks, p->d.block_size, &tokens) || tokens > kMostTokens)
+        return fail(PRED_ERR_OUT_OF_RANGE, "%s: %lld blocks of %d tokens are above 2^29 tokens", what,
                     (long long)n_blocks, p->d.block_size);
     return PRED_OK;
 }
@@ -130,7 +133,7 @@ pred::AttendArgs attend_shape(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t
 
 bool attend_counts_ok(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_blocks) {
     return n_seqs >= 1 && n_rows >= 1 && n_rows <= 64 && n_blocks >= 1 &&
-           n_blocks <= (2147483647LL - 63) / p->d.block_size;
+           n_blocks <= kMostTokens / p->d.block_size;
 }
 
 }  // namespace
