@@ -425,6 +425,12 @@ __device__ inline float sum_over_c(float x) {
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
+// Turns a product q k into units of log2: above 0, so that a masked -inf stays
+// one (the queries carry a negative scale's sign).
+__device__ inline float log2_scale(const AttendArgs& a) {
+    return fmaxf(fabsf(a.scale) * a.cache.k_scale * kLog2e, 0x1p-120f);
+}
+
 // x, or -x where scale is negative
 __device__ inline bf16x8_t signed_by(float scale, bf16x8_t x) {
     const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
@@ -587,6 +593,10 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
     const bool live = r < R && i < drafted;
     const uint64_t seen = live ? tree_word(a, s, i) : 0;
     const int64_t row = ((int64_t)s * a.M + i) * a.Hq + kvh * g + r % g;
+    const int64_t block_step = (int64_t)a.M * a.Hq;
+    // where lane group c writes the c-th block of a tile that starts with block 0
+    float* const block_row =
+        a.block_lse ? a.block_lse + (((int64_t)s * a.n + (bs.B < 32 ? c : 0)) * a.M + i) * a.Hq + kvh * g + r % g : nullptr;
     bf16x8_t q[H][KP];
 #pragma unroll
     for (int j = 0; j < H; ++j)
@@ -647,8 +657,7 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
     for (int j = 0; j < J; ++j) o[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     float m = kLowest, l = 0.f;
     float wide_m = kLowest, wide_l = 0.f;       // block_lse of a block wider than a tile: its maximum and sum so far
-    // scores stay in units of q k; `scale` (not negative, the queries carry the sign) turns them into log2 units
-    const float scale = fabsf(a.scale) * a.cache.k_scale * kLog2e, slack = 8.f / scale;
+    const float scale = log2_scale(a);      // the queries carry its sign
 
     bool odd = false;       // a drafted token's value is not finite
     int t = tile_of(0);
@@ -722,58 +731,75 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
             }
         }
 
-        // the running maximum
-        float top = x[0];
+        // the running maximum, in log2 units; weights 2^(score - maximum)
+        float top[4];       // of each pair of places
 #pragma unroll
-        for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-        if (__ballot(top > m + slack)) {
-            const float m_new = fmaxf(m, max_over_c(top));
-            const float alpha = exp2_of((m - m_new) * scale);
+        for (int y = 0; y < 4; ++y) top[y] = fmaxf(x[2 * y], x[2 * y + 1]);
+        const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+        if (__ballot(tile_top > m + 8.f)) {
+            const float m_new = fmaxf(m, max_over_c(tile_top));
+            const float alpha = exp2_of(m - m_new);
             m = m_new;
             l *= alpha;
 #pragma unroll
             for (int j = 0; j < J; ++j) o[j] *= alpha;
         }
-
-        // weights: x becomes 2^(score - running maximum)
         if (a.block_lse) {
             // Blocks of 8 or 16 tokens lie side by side in a tile, in 2 or 4 of a lane's 8 places; one of 32 or more
-            // fills it.  Weights are taken against their block's own maximum, summed, and then brought to the running
-            // one, so a block far below the rest still has its sum.
+            // fills it.  Their sums are those of the weights, brought back by the maximum, unless one lies so far
+            // below it that its weights are lost: then the sums are taken against each block's own maximum.
             auto blocks = [&](auto parts_) {
                 constexpr int parts = decltype(parts_)::value, each = 8 / parts;
-                float* const to = a.block_lse + ((int64_t)s * a.n * a.M + i) * a.Hq + kvh * g + r % g;
-                float mine = -INFINITY;
+                float part_top[parts], sum[parts], ref[parts];
+                bool far = false;
 #pragma unroll
                 for (int y = 0; y < parts; ++y) {
-                    float* const xb = x + y * each;
-                    float bm = xb[0];
+                    part_top[y] = top[y * each / 2];
 #pragma unroll
-                    for (int e = 1; e < each; ++e) bm = fmaxf(bm, xb[e]);
-                    bm = fmaxf(max_over_c(bm), kLowest);
-                    float bl = 0.f;
-                    const float to_running = exp2_of((bm - m) * scale);
+                    for (int e = 1; e < each / 2; ++e) part_top[y] = fmaxf(part_top[y], top[y * each / 2 + e]);
+                    far |= part_top[y] * scale < m - 60.f && part_top[y] > kLowest;
+                    sum[y] = 0.f;
+                    ref[y] = m;
+                }
+                const bool own = __ballot(far) != 0;
+                if (own) {
+#pragma unroll
+                    for (int y = 0; y < parts; ++y) {
+                        ref[y] = fmaxf(max_over_c(part_top[y]) * scale, kLowest);
+#pragma unroll
+                        for (int e = 0; e < each; ++e) sum[y] += exp2_of(__builtin_fmaf(x[y * each + e], scale, -ref[y]));
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < parts; ++y) {
+                    float part_l = 0.f;
 #pragma unroll
                     for (int e = 0; e < each; ++e) {
-                        xb[e] = exp2_of((xb[e] - bm) * scale);
-                        bl += xb[e];
-                        xb[e] *= to_running;
+                        x[y * each + e] = exp2_of(__builtin_fmaf(x[y * each + e], scale, -m));
+                        part_l += x[y * each + e];
                     }
-                    bl = sum_over_c(bl);
-                    if constexpr (parts == 1) {
-                        const float both = fmaxf(wide_m, bm);
-                        wide_l = wide_l * exp2_of((wide_m - both) * scale) + bl * exp2_of((bm - both) * scale);
-                        wide_m = both;
-                        bl = wide_l;
-                        bm = both;
-                    }
-                    const float log = live && !(bl <= 0.f) ? (bm * scale + log2_of(bl)) * kLn2 : -INFINITY;
-                    mine = y == c ? log : mine;
+                    l += part_l;
+                    sum[y] = sum_over_c(own ? sum[y] : part_l);
                 }
-                const int tok = t + 32 / parts * c;
+                float mine_sum = sum[0], mine_ref = ref[0];
+#pragma unroll
+                for (int y = 1; y < parts; ++y) {
+                    mine_sum = y == c ? sum[y] : mine_sum;
+                    mine_ref = y == c ? ref[y] : mine_ref;
+                }
+                if constexpr (parts == 1) {
+                    const float both = fmaxf(wide_m, mine_ref);
+                    wide_l = wide_l * exp2_of(wide_m - both) + mine_sum * exp2_of(mine_ref - both);
+                    wide_m = both;
+                    mine_sum = wide_l;
+                    mine_ref = both;
+                }
+                const int b = bs.block(t);
                 // of a block wider than a tile: with its last tile, or the sequence's
-                const bool done = parts > 1 || t + 32 >= t1 || bs.block(t + 32) != bs.block(t);
-                if (done && c < parts && r < R && tok < t1) to[bs.block(tok) * (int64_t)a.M * a.Hq] = mine;
+                const bool done = parts > 1 || t + 32 >= t1 || bs.block(t + 32) != b;
+                if (done && c < parts && r < R && t + 32 / parts * c < t1)
+                    block_row[(int64_t)b * block_step] =
+                        live && !(mine_sum <= 0.f) ? (mine_ref + log2_of(mine_sum)) * kLn2 : -INFINITY;
                 if (parts == 1 && done) {
                     wide_m = kLowest;
                     wide_l = 0.f;
@@ -784,12 +810,13 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
             else blocks(std::integral_constant<int, 1>());
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = exp2_of((x[e] - m) * scale);
+            for (int e = 0; e < 8; ++e) {
+                x[e] = exp2_of(__builtin_fmaf(x[e], scale, -m));
+                l += x[e];
+            }
         }
 
         u32x4_t wh, wl;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) l += x[e];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             wh[e] = bf16_pair(x[2 * e], x[2 * e + 1]);
@@ -839,7 +866,6 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
             }
         }
     }
-    m = fmaxf(m * scale, kLowest);      // log2 units from here on
     l = sum_over_c(l);
 
     // the waves' sums: 2 and 3 into 0 and 1, then 1 into 0
@@ -974,8 +1000,9 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
     const bool live = r < R && i < drafted;
     const bool wave_live = r0 < R && r0 / g < drafted;          // rows of a wave die from the end
     const uint64_t seen = live ? tree_word(a, s, i) : 0;
+    // where lane f writes the f-th block of a half tile that starts with block 0
     float* const block_row =
-        a.block_lse ? a.block_lse + ((int64_t)s * a.n * a.M + i) * a.Hq + kvh * g + r % g : nullptr;
+        a.block_lse ? a.block_lse + (((int64_t)s * a.n + (bs.B < 32 ? f : 0)) * a.M + i) * a.Hq + kvh * g + r % g : nullptr;
     const int64_t block_step = (int64_t)a.M * a.Hq;
     const int64_t row = ((int64_t)s * a.M + i) * a.Hq + kvh * g + r % g;
 
@@ -1075,7 +1102,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
     float m = kLowest, l = 0.f, wide_m = kLowest, wide_l = 0.f;
-    const float scale = fabsf(a.scale) * a.cache.k_scale * kLog2e, slack = 8.f / scale;     // as in the stream kernel
+    const float scale = log2_scale(a);
 
     if (threadIdx.x == 0) any_odd = 0;
     __syncthreads();
@@ -1103,24 +1130,25 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
                 if (dead & ~past) atomicOr(a.err, DEVERR_TABLE);
             }
             if (!wave_live) {       // empty rows in a workgroup that has others
-                if (a.block_lse && r < R && (th == t0 || bs.block(th) != bs.block(th - 1) || bs.B < 32))
-                    for (int b = bs.block(th) + f; b <= bs.block(th + 31 < t1 ? th + 31 : t1 - 1); b += 2)
+                if (a.block_lse && r < R) {
+                    const int last = bs.block(th + 31 < t1 ? th + 31 : t1 - 1);
+                    for (int b = bs.block(th); b + (bs.B < 32 ? f : 0) <= last; b += bs.B < 32 ? 2 : 1)
                         block_row[b * block_step] = -INFINITY;
+                }
                 continue;
             }
             float x[16];
             {
-                // two chains of products
                 const char* const kt0 = lds + buf * T::kTile + 32 * half * T::kRow;
-                f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
+                f32x16_t acc = f32x16_t{};
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     const bf16x8_t key = __builtin_bit_cast(
                         bf16x8_t, *reinterpret_cast<const u32x4_t*>(kt0 + (k_from ^ (32 * k))));
-                    acc[k % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc[k % 2], 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc, 0, 0, 0);
                 }
 #pragma unroll
-                for (int v = 0; v < 16; ++v) x[v] = acc[0][v] + acc[1][v];
+                for (int v = 0; v < 16; ++v) x[v] = acc[v];
             }
             if (masked) {
 #pragma unroll
@@ -1131,55 +1159,74 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
                 }
             }
 
-            float top = x[0];
+            // as in the stream kernel; 8-token blocks are quads of v, 16-token ones pairs of quads
+            float top[4];
 #pragma unroll
-            for (int v = 1; v < 16; ++v) top = fmaxf(top, x[v]);
-            if (__ballot(top > m + slack)) {
-                const float m_new = fmaxf(m, max_over_f(top));
-                const float alpha = exp2_of((m - m_new) * scale);
+            for (int y = 0; y < 4; ++y)
+                top[y] = fmaxf(fmaxf(x[4 * y], x[4 * y + 1]), fmaxf(x[4 * y + 2], x[4 * y + 3]));
+            const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+            if (__ballot(tile_top > m + 8.f)) {
+                const float m_new = fmaxf(m, max_over_f(tile_top));
+                const float alpha = exp2_of(m - m_new);
                 m = m_new;
                 l *= alpha;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[d] *= alpha;
             }
-
-            // weights, as in the stream kernel: 8-token blocks are quads of v, 16-token ones pairs of quads
             if (a.block_lse) {
                 auto blocks = [&](auto parts_) {
                     constexpr int parts = decltype(parts_)::value, each = 16 / parts;
-                    float mine[parts >= 2 ? parts / 2 : 1];
+                    float part_top[parts], sum[parts], ref[parts];
+                    bool far = false;
 #pragma unroll
                     for (int y = 0; y < parts; ++y) {
-                        float* const xb = x + y * each;
-                        float bm = xb[0];
+                        part_top[y] = top[y * each / 4];
 #pragma unroll
-                        for (int e = 1; e < each; ++e) bm = fmaxf(bm, xb[e]);
-                        bm = fmaxf(max_over_f(bm), kLowest);
-                        float bl = 0.f;
-                        const float to_running = exp2_of((bm - m) * scale);
+                        for (int e = 1; e < each / 4; ++e) part_top[y] = fmaxf(part_top[y], top[y * each / 4 + e]);
+                        far |= part_top[y] * scale < m - 60.f && part_top[y] > kLowest;
+                        sum[y] = 0.f;
+                        ref[y] = m;
+                    }
+                    const bool own = __ballot(far) != 0;
+                    if (own) {
+#pragma unroll
+                        for (int y = 0; y < parts; ++y) {
+                            ref[y] = fmaxf(max_over_f(part_top[y]) * scale, kLowest);
+#pragma unroll
+                            for (int e = 0; e < each; ++e)
+                                sum[y] += exp2_of(__builtin_fmaf(x[y * each + e], scale, -ref[y]));
+                        }
+                    }
+#pragma unroll
+                    for (int y = 0; y < parts; ++y) {
+                        float part_l = 0.f;
 #pragma unroll
                         for (int e = 0; e < each; ++e) {
-                            xb[e] = exp2_of((xb[e] - bm) * scale);
-                            bl += xb[e];
-                            xb[e] *= to_running;
+                            x[y * each + e] = exp2_of(__builtin_fmaf(x[y * each + e], scale, -m));
+                            part_l += x[y * each + e];
                         }
-                        bl = sum_over_f(bl);
-                        if constexpr (parts == 1) {
-                            const float both = fmaxf(wide_m, bm);
-                            wide_l = wide_l * exp2_of((wide_m - both) * scale) + bl * exp2_of((bm - both) * scale);
-                            wide_m = both;
-                            bl = wide_l;
-                            bm = both;
-                        }
-                        const float log = live && !(bl <= 0.f) ? (bm * scale + log2_of(bl)) * kLn2 : -INFINITY;
-                        mine[y / 2] = y % 2 == f || parts == 1 ? log : mine[y / 2];
+                        l += part_l;
+                        sum[y] = sum_over_f(own ? sum[y] : part_l);
                     }
-                    const bool done = parts > 1 || th + 32 >= t1 || bs.block(th + 32) != bs.block(th);
+                    const int b = bs.block(th);
+                    const bool done = parts > 1 || th + 32 >= t1 || bs.block(th + 32) != b;
+                    // lane f writes blocks f, f + 2 of the half; a single one lane 0
 #pragma unroll
-                    for (int y = 0; y < (parts >= 2 ? parts / 2 : 1); ++y) {
-                        const int tok = th + (parts == 1 ? 0 : 32 / parts * (2 * y + f));
-                        if (done && r < R && tok < t1 && (parts > 1 || f == 0))
-                            block_row[bs.block(tok) * block_step] = mine[y];
+                    for (int y = 0; y < (parts + 1) / 2; ++y) {
+                        float mine_sum = sum[2 * y], mine_ref = ref[2 * y];
+                        if constexpr (parts > 1) {
+                            mine_sum = f ? sum[2 * y + 1] : mine_sum;
+                            mine_ref = f ? ref[2 * y + 1] : mine_ref;
+                        } else {
+                            const float both = fmaxf(wide_m, mine_ref);
+                            wide_l = wide_l * exp2_of(wide_m - both) + mine_sum * exp2_of(mine_ref - both);
+                            wide_m = both;
+                            mine_sum = wide_l;
+                            mine_ref = both;
+                        }
+                        if (done && f < parts && r < R && th + 32 / parts * (2 * y + f) < t1)
+                            block_row[(int64_t)(b + 2 * y) * block_step] =
+                                live && !(mine_sum <= 0.f) ? (mine_ref + log2_of(mine_sum)) * kLn2 : -INFINITY;
                     }
                     if (parts == 1 && done) {
                         wide_m = kLowest;
@@ -1191,10 +1238,11 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
                 else blocks(std::integral_constant<int, 1>());
             } else {
 #pragma unroll
-                for (int v = 0; v < 16; ++v) x[v] = exp2_of((x[v] - m) * scale);
+                for (int v = 0; v < 16; ++v) {
+                    x[v] = exp2_of(__builtin_fmaf(x[v], scale, -m));
+                    l += x[v];
+                }
             }
-#pragma unroll
-            for (int v = 0; v < 16; ++v) l += x[v];
 
             // 8 tokens' values of one d: two transpose reads
             const char* const vt0 = lds + (2 + buf) * T::kTile + 32 * half * T::kRow;
@@ -1244,7 +1292,6 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
             }
         }
     }
-    m = fmaxf(m * scale, kLowest);      // log2 units from here on
     l = sum_over_f(l);
     if constexpr (WK == 2) {
         // the pair's sums, through the (now unused) stage
