@@ -463,6 +463,20 @@ inline BlockSize block_size(int B) {
     return BlockSize{B, 31 + s, (uint32_t)((one + B - 1) / B)};
 }
 
+// The larger of three, one instruction where `a` is known to be a number.
+__device__ inline float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// x less its bf16 value, half HI of `pair`: exact, as one dot product.  The
+// factor -1 is kept in a register: as an operand (-1, 0) the compiler writes
+// the inline constant -1.0, which the instruction takes for (0, -1).
+template <bool HI>
+__device__ inline float rest_of(float x, uint32_t pair) {
+    uint32_t minus_one = HI ? 0xBF800000u : 0x0000BF80u;
+    asm("" : "+s"(minus_one));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, pair), __builtin_bit_cast(bf16x2_t, minus_one), x,
+                                           false);
+}
+
 // w with its halves that are not finite set to 0
 __device__ inline uint32_t finite_only(uint32_t w) {
     return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
@@ -525,11 +539,13 @@ struct TableWindow {
     }
 };
 
-// What the rows of groups without a live row get (rows `from` on of a kv head):
+// What rows `from` (to `end`, by default the last) of a kv head get that have no
+// live row in their group:
 // block_lse -inf for this run's blocks and, where no join follows, output 0
 // and lse -inf.
-__device__ inline void write_dead_rows(const AttendArgs& a, const Item& it, const BlockSize& bs, int from, int t0, int t1) {
-    const int g = a.Hq / a.Hk, dead = a.M * g - from;
+__device__ inline void write_dead_rows(const AttendArgs& a, const Item& it, const BlockSize& bs, int from, int t0, int t1,
+                                       int end = 0x7FFFFFFF) {
+    const int g = a.Hq / a.Hk, dead = (a.M * g < end ? a.M * g : end) - from;
     if (dead <= 0) return;
     if (a.block_lse && t1 > t0) {
         const int b0 = bs.block(t0), blocks = bs.block(t1 - 1) + 1 - b0;
@@ -734,8 +750,8 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
         // the running maximum, in log2 units; weights 2^(score - maximum)
         float top[4];       // of each pair of places
 #pragma unroll
-        for (int y = 0; y < 4; ++y) top[y] = fmaxf(x[2 * y], x[2 * y + 1]);
-        const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+        for (int y = 0; y < 4; ++y) top[y] = max3(kLowest, x[2 * y], x[2 * y + 1]);
+        const float tile_top = max3(max3(top[0], top[1], top[2]), top[3], kLowest) * scale;
         if (__ballot(tile_top > m + 8.f)) {
             const float m_new = fmaxf(m, max_over_c(tile_top));
             const float alpha = exp2_of(m - m_new);
@@ -820,7 +836,7 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             wh[e] = bf16_pair(x[2 * e], x[2 * e + 1]);
-            wl[e] = bf16_pair(x[2 * e] - bf16_lo(wh[e]), x[2 * e + 1] - bf16_hi(wh[e]));
+            wl[e] = bf16_pair(rest_of<false>(x[2 * e], wh[e]), rest_of<true>(x[2 * e + 1], wh[e]));
         }
         const bf16x8_t hi = __builtin_bit_cast(bf16x8_t, wh), lo = __builtin_bit_cast(bf16x8_t, wl);
 
@@ -971,14 +987,15 @@ __device__ inline float sum_over_f(float x) {
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 
-template <int D, bool FP8, int WK>
+// BLOCKS: block sums a half tile has: 0 without block_lse, 1 for blocks of 32
+// tokens or more, 2 for 16, 4 for 8.
+template <int D, bool FP8, int BLOCKS>
 __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan pl, BlockSize bs) {
     using T = TreeLds<D>;
     constexpr int RB = D * (FP8 ? 1 : 2);       // bytes of a cache row
     constexpr int CR = RB / 16;                 // 16-byte pieces of it
     constexpr int NR = 64 * CR / 256;           // pieces a thread stages, of keys and of values
     constexpr int KS = D / 16, DT = D / 32;
-    constexpr int kRowWaves = 4 / WK;
     __shared__ __attribute__((aligned(16))) char lds[4 * T::kTile];     // keys 0, keys 1, values 0, values 1
     __shared__ int any_odd;         // a drafted token's value is not finite
 
@@ -995,8 +1012,11 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, f = lane >> 5;
     const int g = a.Hq / a.Hk, R = a.M * g;
-    if (it.last) write_dead_rows(a, it, bs, kRowWaves * 32 * (it.group + 1), t0, t1);
-    const int in_group = wave / WK * 32, r0 = it.group * kRowWaves * 32 + in_group, r = r0 + n, i = r / g;
+    if (it.last) write_dead_rows(a, it, bs, 128 * (it.group + 1), t0, t1);
+    // up to 64 live queries: two waves each, a half of every tile (not where a block's sum spans the halves)
+    const bool pairs = drafted * g - 128 * it.group <= 64 && !(BLOCKS == 1 && bs.B > 32);
+    if (pairs && it.last) write_dead_rows(a, it, bs, 128 * it.group + 64, t0, t1, 128 * (it.group + 1));
+    const int in_group = (pairs ? wave / 2 : wave) * 32, r0 = 128 * it.group + in_group, r = r0 + n, i = r / g;
     const bool live = r < R && i < drafted;
     const bool wave_live = r0 < R && r0 / g < drafted;          // rows of a wave die from the end
     const uint64_t seen = live ? tree_word(a, s, i) : 0;
@@ -1112,176 +1132,189 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
     slot = entry_of(t0 + 64);
     store_tile(0, t0, nowhere);
     __syncthreads();
-    for (int t = t0, buf = 0; t < t1; t += 64, buf ^= 1) {
-        const bool more = t + 64 < t1;
-        if (more) {
-            load_tile(offset_of(t + 64, slot, nowhere_next));
-            slot = entry_of(t + 128);
-        }
-#pragma unroll 1
-        for (int half = WK == 2 ? wave % 2 : 0; half < (WK == 2 ? wave % 2 + 1 : 2); ++half) {
-            const int th = t + 32 * half;
-            if (th >= t1) break;
-            const uint32_t dead = (uint32_t)(nowhere >> (32 * half));
-            const bool masked = th + 32 > ctx || dead != 0;
-            if (dead && th < t1 && wave == 0 && lane == 0) {
-                // past the run's end is no error
-                const uint32_t past = t1 - th < 32 ? ~0u << (t1 - th) : 0u;
-                if (dead & ~past) atomicOr(a.err, DEVERR_TABLE);
+    // HALVES = 2: the whole of every tile; 1: half `mine` of it
+    auto walk = [&](auto halves_, const int mine) {
+        constexpr int HALVES = decltype(halves_)::value;
+        for (int t = t0, buf = 0; t < t1; t += 64, buf ^= 1) {
+            const bool more = t + 64 < t1;
+            if (more) {
+                load_tile(offset_of(t + 64, slot, nowhere_next));
+                slot = entry_of(t + 128);
             }
-            if (!wave_live) {       // empty rows in a workgroup that has others
-                if (a.block_lse && r < R) {
-                    const int last = bs.block(th + 31 < t1 ? th + 31 : t1 - 1);
-                    for (int b = bs.block(th); b + (bs.B < 32 ? f : 0) <= last; b += bs.B < 32 ? 2 : 1)
-                        block_row[b * block_step] = -INFINITY;
-                }
-                continue;
-            }
-            float x[16];
-            {
-                const char* const kt0 = lds + buf * T::kTile + 32 * half * T::kRow;
-                f32x16_t acc = f32x16_t{};
+            uint64_t wrong = nowhere;       // invalid entries: tokens past the run's end are none
+            if (t + 64 > t1) wrong &= (1ull << (t1 - t)) - 1;
+            if (wrong && wave == 0 && lane == 0) atomicOr(a.err, DEVERR_TABLE);
+            if (wave_live) {
+                float x[HALVES][16];
+                const char* const kt = lds + buf * T::kTile + (HALVES == 1 ? 32 * mine * T::kRow : 0);
+                const char* const vt = kt + 2 * T::kTile;
+                const int th = t + 32 * mine;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const bf16x8_t key = __builtin_bit_cast(
-                        bf16x8_t, *reinterpret_cast<const u32x4_t*>(kt0 + (k_from ^ (32 * k))));
-                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc, 0, 0, 0);
-                }
+                for (int h = 0; h < HALVES; ++h) {
+                    f32x16_t acc = f32x16_t{};
 #pragma unroll
-                for (int v = 0; v < 16; ++v) x[v] = acc[v];
-            }
-            if (masked) {
+                    for (int k = 0; k < KS; ++k) {
+                        const bf16x8_t key = __builtin_bit_cast(
+                            bf16x8_t, *reinterpret_cast<const u32x4_t*>(kt + (k_from ^ (32 * k)) + 32 * h * T::kRow));
+                        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc, 0, 0, 0);
+                    }
 #pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const int in = v % 4 + 8 * (v / 4) + 4 * f, place = th + in - ctx;
-                    const bool sees = !((dead >> in) & 1) && (place < 0 || ((seen >> (place & 63)) & 1));
-                    x[v] = sees ? x[v] : -INFINITY;
+                    for (int v = 0; v < 16; ++v) x[h][v] = acc[v];
                 }
-            }
+                if (t + 64 > ctx || nowhere != 0) {
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) {
+                        const uint32_t dead = (uint32_t)(nowhere >> (32 * (h + mine)));
+#pragma unroll
+                        for (int v = 0; v < 16; ++v) {
+                            const int in = v % 4 + 8 * (v / 4) + 4 * f, place = th + 32 * h + in - ctx;
+                            const bool sees = ((dead >> in) & 1) == 0 && (place < 0 || ((seen >> (place & 63)) & 1));
+                            x[h][v] = sees ? x[h][v] : -INFINITY;
+                        }
+                    }
+                }
 
-            // as in the stream kernel; 8-token blocks are quads of v, 16-token ones pairs of quads
-            float top[4];
+                // the running maximum and the blocks' sums as in the stream kernel; 8-token blocks are quads of v,
+                // 16-token ones pairs of quads
+                float top[HALVES][4], tile_top = kLowest;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-                top[y] = fmaxf(fmaxf(x[4 * y], x[4 * y + 1]), fmaxf(x[4 * y + 2], x[4 * y + 3]));
-            const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-            if (__ballot(tile_top > m + 8.f)) {
-                const float m_new = fmaxf(m, max_over_f(tile_top));
-                const float alpha = exp2_of(m - m_new);
-                m = m_new;
-                l *= alpha;
+                for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-                for (int d = 0; d < DT; ++d) o[d] *= alpha;
-            }
-            if (a.block_lse) {
-                auto blocks = [&](auto parts_) {
-                    constexpr int parts = decltype(parts_)::value, each = 16 / parts;
-                    float part_top[parts], sum[parts], ref[parts];
+                    for (int y = 0; y < 4; ++y) {
+                        top[h][y] = max3(max3(kLowest, x[h][4 * y], x[h][4 * y + 1]), x[h][4 * y + 2], x[h][4 * y + 3]);
+                        if (y % 2) tile_top = max3(tile_top, top[h][y - 1], top[h][y]);
+                    }
+                tile_top *= scale;
+                if (__ballot(tile_top > m + 8.f)) {
+                    const float m_new = fmaxf(m, max_over_f(tile_top));
+                    const float alpha = exp2_of(m - m_new);
+                    m = m_new;
+                    l *= alpha;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) o[d] *= alpha;
+                }
+                constexpr int kSums = BLOCKS ? BLOCKS : 1, each = 16 / kSums;
+                float sum[HALVES][kSums], ref[HALVES][kSums];
+                bool own = false;
+                if constexpr (BLOCKS > 0) {
                     bool far = false;
 #pragma unroll
-                    for (int y = 0; y < parts; ++y) {
-                        part_top[y] = top[y * each / 4];
+                    for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-                        for (int e = 1; e < each / 4; ++e) part_top[y] = fmaxf(part_top[y], top[y * each / 4 + e]);
-                        far |= part_top[y] * scale < m - 60.f && part_top[y] > kLowest;
-                        sum[y] = 0.f;
-                        ref[y] = m;
-                    }
-                    const bool own = __ballot(far) != 0;
-                    if (own) {
+                        for (int b = 0; b < BLOCKS; ++b) {
+                            float& part_top = ref[h][b];
+                            part_top = top[h][b * each / 4];
 #pragma unroll
-                        for (int y = 0; y < parts; ++y) {
-                            ref[y] = fmaxf(max_over_f(part_top[y]) * scale, kLowest);
-#pragma unroll
-                            for (int e = 0; e < each; ++e)
-                                sum[y] += exp2_of(__builtin_fmaf(x[y * each + e], scale, -ref[y]));
+                            for (int e = 1; e < each / 4; ++e) part_top = fmaxf(part_top, top[h][b * each / 4 + e]);
+                            far |= part_top * scale < m - 60.f && part_top > kLowest;
                         }
-                    }
+                    own = __ballot(far) != 0;
 #pragma unroll
-                    for (int y = 0; y < parts; ++y) {
-                        float part_l = 0.f;
+                    for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-                        for (int e = 0; e < each; ++e) {
-                            x[y * each + e] = exp2_of(__builtin_fmaf(x[y * each + e], scale, -m));
-                            part_l += x[y * each + e];
+                        for (int b = 0; b < BLOCKS; ++b) {
+                            sum[h][b] = 0.f;
+                            if (own) {
+                                ref[h][b] = fmaxf(max_over_f(ref[h][b]) * scale, kLowest);
+#pragma unroll
+                                for (int e = 0; e < each; ++e)
+                                    sum[h][b] += exp2_of(__builtin_fmaf(x[h][b * each + e], scale, -ref[h][b]));
+                            } else {
+                                ref[h][b] = m;
+                            }
                         }
-                        l += part_l;
-                        sum[y] = sum_over_f(own ? sum[y] : part_l);
-                    }
-                    const int b = bs.block(th);
-                    const bool done = parts > 1 || th + 32 >= t1 || bs.block(th + 32) != b;
-                    // lane f writes blocks f, f + 2 of the half; a single one lane 0
-#pragma unroll
-                    for (int y = 0; y < (parts + 1) / 2; ++y) {
-                        float mine_sum = sum[2 * y], mine_ref = ref[2 * y];
-                        if constexpr (parts > 1) {
-                            mine_sum = f ? sum[2 * y + 1] : mine_sum;
-                            mine_ref = f ? ref[2 * y + 1] : mine_ref;
-                        } else {
-                            const float both = fmaxf(wide_m, mine_ref);
-                            wide_l = wide_l * exp2_of(wide_m - both) + mine_sum * exp2_of(mine_ref - both);
-                            wide_m = both;
-                            mine_sum = wide_l;
-                            mine_ref = both;
-                        }
-                        if (done && f < parts && r < R && th + 32 / parts * (2 * y + f) < t1)
-                            block_row[(int64_t)(b + 2 * y) * block_step] =
-                                live && !(mine_sum <= 0.f) ? (mine_ref + log2_of(mine_sum)) * kLn2 : -INFINITY;
-                    }
-                    if (parts == 1 && done) {
-                        wide_m = kLowest;
-                        wide_l = 0.f;
-                    }
-                };
-                if (bs.B == 16) blocks(std::integral_constant<int, 2>());
-                else if (bs.B == 8) blocks(std::integral_constant<int, 4>());
-                else blocks(std::integral_constant<int, 1>());
-            } else {
-#pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    x[v] = exp2_of(__builtin_fmaf(x[v], scale, -m));
-                    l += x[v];
                 }
-            }
 
-            // 8 tokens' values of one d: two transpose reads
-            const char* const vt0 = lds + (2 + buf) * T::kTile + 32 * half * T::kRow;
-            auto value_of = [&](int d, int y) {
-                struct { i16x4_t p[2]; } both;
 #pragma unroll
-                for (int z = 0; z < 2; ++z)
-                    both.p[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (lds_i16x4_t*)(vt0 + (v_from ^ (64 * d)) + (16 * y + 8 * z) * T::kRow));
-                return __builtin_bit_cast(bf16x8_t, both);
-            };
+                for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                u32x4_t wh, wl;
+                    for (int y = 0; y < 2; ++y) {
+                        float* const w = x[h] + 8 * y;
+                        float part_l[2] = {0.f, 0.f};       // of each quad
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float u = x[8 * y + 2 * e], w = x[8 * y + 2 * e + 1];
-                    wh[e] = bf16_pair(u, w);
-                    wl[e] = bf16_pair(u - bf16_lo(wh[e]), w - bf16_hi(wh[e]));
+                        for (int e = 0; e < 8; ++e) {
+                            w[e] = exp2_of(__builtin_fmaf(w[e], scale, -m));
+                            part_l[e / 4] += w[e];
+                        }
+                        l += part_l[0] + part_l[1];
+                        if constexpr (BLOCKS > 0) {
+                            if (!own) {
+                                sum[h][8 * y / each] += part_l[0];
+                                sum[h][(8 * y + 4) / each] += part_l[1];
+                            }
+                        }
+                        u32x4_t wh, wl;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            wh[e] = bf16_pair(w[2 * e], w[2 * e + 1]);
+                            wl[e] = bf16_pair(rest_of<false>(w[2 * e], wh[e]), rest_of<true>(w[2 * e + 1], wh[e]));
+                        }
+                        // 8 tokens' values of one d: two transpose reads
+                        bf16x8_t val[DT];
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) {
+                            struct { i16x4_t p[2]; } both;
+#pragma unroll
+                            for (int z = 0; z < 2; ++z)
+                                both.p[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                    (lds_i16x4_t*)(vt + (v_from ^ (64 * d)) + (32 * h + 16 * y + 8 * z) * T::kRow));
+                            val[d] = __builtin_bit_cast(bf16x8_t, both);
+                        }
+#pragma unroll
+                        for (int d = 0; d < DT; ++d)
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val[d], __builtin_bit_cast(bf16x8_t, wh), o[d], 0, 0, 0);
+#pragma unroll
+                        for (int d = 0; d < DT; ++d)
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val[d], __builtin_bit_cast(bf16x8_t, wl), o[d], 0, 0, 0);
+                    }
+
+                if constexpr (BLOCKS > 0) {
+                    // lane f writes blocks f, f + 2 of a half; a single one lane 0
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) {
+                        const int half = th + 32 * h, b = bs.block(half);
+                        const bool done = BLOCKS > 1 || half + 32 >= t1 || bs.block(half + 32) != b;
+                        if (half >= t1) break;
+#pragma unroll
+                        for (int y = 0; y < (BLOCKS + 1) / 2; ++y) {
+                            float mine_sum = sum_over_f(sum[h][2 * y]), mine_ref = ref[h][2 * y];
+                            if constexpr (BLOCKS > 1) {
+                                const float other = sum_over_f(sum[h][2 * y + 1]);
+                                mine_sum = f ? other : mine_sum;
+                                mine_ref = f ? ref[h][2 * y + 1] : mine_ref;
+                            } else {
+                                const float both = fmaxf(wide_m, mine_ref);
+                                wide_l = wide_l * exp2_of(wide_m - both) + mine_sum * exp2_of(mine_ref - both);
+                                wide_m = both;
+                                mine_sum = wide_l;
+                                mine_ref = both;
+                            }
+                            if (done && f < BLOCKS && r < R && half + 32 / BLOCKS * (2 * y + f) < t1)
+                                block_row[(int64_t)(b + 2 * y) * block_step] =
+                                    live && !(mine_sum <= 0.f) ? (mine_ref + log2_of(mine_sum)) * kLn2 : -INFINITY;
+                        }
+                        if (BLOCKS == 1 && done) {
+                            wide_m = kLowest;
+                            wide_l = 0.f;
+                        }
+                    }
                 }
-                bf16x8_t val[DT];
-#pragma unroll
-                for (int d = 0; d < DT; ++d) val[d] = value_of(d, y);
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val[d], __builtin_bit_cast(bf16x8_t, wh), o[d], 0, 0, 0);
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val[d], __builtin_bit_cast(bf16x8_t, wl), o[d], 0, 0, 0);
+            } else if (BLOCKS > 0 && r < R && !(pairs && wave % 2)) {     // empty rows in a workgroup that has others
+                const int last = bs.block(t + 63 < t1 ? t + 63 : t1 - 1);
+                for (int b = bs.block(t); b + (bs.B < 32 ? f : 0) <= last; b += bs.B < 32 ? 2 : 1)
+                    block_row[b * block_step] = -INFINITY;
             }
+            if (more) store_tile(buf ^ 1, t + 64, nowhere_next);
+            nowhere = nowhere_next;
+            __syncthreads();
         }
-        if (more) store_tile(buf ^ 1, t + 64, nowhere_next);
-        nowhere = nowhere_next;
-        __syncthreads();
-    }
+    };
+    if (pairs) walk(std::integral_constant<int, 1>(), wave % 2);
+    else walk(std::integral_constant<int, 2>(), 0);
 
     if (any_odd) {
         for (int tok = ctx > t0 ? ctx : t0; tok < t1; ++tok) {
-            if (WK == 2 && (tok - t0) / 32 % 2 != wave % 2) continue;       // the other wave's half
+            if (pairs && (tok - t0) / 32 % 2 != wave % 2) continue;         // the other wave's half
             const char* const from = value_row(a, bs, s, kvh, tok, item);
             if (from && ((seen >> ((tok - ctx) & 63)) & 1)) {
 #pragma unroll
@@ -1293,7 +1326,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
         }
     }
     l = sum_over_f(l);
-    if constexpr (WK == 2) {
+    if (pairs) {
         // the pair's sums, through the (now unused) stage
         float* const x = reinterpret_cast<float*>(lds) + (wave / 2) * (16 * DT + 2) * 64;
         if (wave % 2) {
@@ -1366,14 +1399,10 @@ Kind kind_of(const AttendArgs& a) {
     return Kind::Stream;
 }
 
-// Two waves to 32 queries where the queries would leave half of the workgroup
-// idle; not where a block's sum spans the halves of a tile that they take.
-bool tree_pairs(const AttendArgs& a) { return queries_of(a) <= 64 && !(a.block_lse && a.B > 32); }
-
-Plan plan_of(const AttendArgs& a, bool tree, bool pairs) {
+Plan plan_of(const AttendArgs& a, bool tree) {
     const int queries = queries_of(a);
     Plan pl;
-    pl.rows = tree ? (pairs ? 64 : 128) : 16;
+    pl.rows = tree ? 128 : 16;
     pl.groups = (queries + pl.rows - 1) / pl.rows;
     if (pl.rows > queries) pl.rows = queries;       // of one group
     // whole tiles (four waves take one each in the stream kernel), or whole blocks where a block's sum spans tiles
@@ -1400,7 +1429,9 @@ template <int D, bool FP8>
 void launch_fast(const AttendArgs& a, Kind kind, const Plan& pl, uint32_t grid, hipStream_t stream) {
     const BlockSize bs = block_size(a.B);
     if (kind == Kind::Stream) attend_stream_kernel<D, FP8><<<grid, 256, 0, stream>>>(a, pl, bs);
-    else if (tree_pairs(a)) attend_tree_kernel<D, FP8, 2><<<grid, 256, 0, stream>>>(a, pl, bs);
+    else if (!a.block_lse) attend_tree_kernel<D, FP8, 0><<<grid, 256, 0, stream>>>(a, pl, bs);
+    else if (a.B == 8) attend_tree_kernel<D, FP8, 4><<<grid, 256, 0, stream>>>(a, pl, bs);
+    else if (a.B == 16) attend_tree_kernel<D, FP8, 2><<<grid, 256, 0, stream>>>(a, pl, bs);
     else attend_tree_kernel<D, FP8, 1><<<grid, 256, 0, stream>>>(a, pl, bs);
 }
 
@@ -1417,13 +1448,8 @@ void launch_join(const AttendArgs& a, const Plan& pl, uint32_t rows, hipStream_t
 
 size_t attend_workspace_bytes(const AttendArgs& a) {
     if (a.D != 64 && a.D != 128) return 0;
-    // the most that a call of this shape may need, whatever its cache and whether it asks for block_lse
-    size_t most = 0;
-    for (int pairs = 0; pairs < 2; ++pairs) {
-        const size_t bytes = plan_bytes(a, plan_of(a, queries_of(a) > kStreamQueries, pairs));
-        most = bytes > most ? bytes : most;
-    }
-    return most;
+    // of a call without block_lse, whose runs can be the shorter
+    return plan_bytes(a, plan_of(a, queries_of(a) > kStreamQueries));
 }
 
 const char* attend_kernel_name(const AttendArgs& a) {
@@ -1442,7 +1468,7 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
         else attend_plain_kernel<false><<<row_grid, 256, 0, stream>>>(a);
         return hipGetLastError();
     }
-    const Plan pl = plan_of(a, kind == Kind::Tree, tree_pairs(a));
+    const Plan pl = plan_of(a, kind == Kind::Tree);
     const bool split = may_split(a, pl);
     AttendArgs b = a;
     if (!split) b.ws = nullptr;
