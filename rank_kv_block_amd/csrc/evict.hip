@@ -59,63 +59,101 @@ __global__ __launch_bounds__(256) void weight_kernel(WeightArgs a, int lanes, ui
 // ---------------------------------------------------------------- evict
 //
 // One workgroup of 16 waves per sequence.  Wave w owns a contiguous range of
-// the row and reads it 64 entries at a time, so an entry's place among those of
+// the row and takes it 64 entries at a time, so an entry's place among those of
 // its kind is the count of the waves before, plus the wave's running count,
-// plus a ballot's prefix.  With E > 0 a lane keeps its E entries in registers
-// (rows up to 1024 E) and every pass runs from them; E = 0 reads them again
-// from a copy in the workspace.  Reading everything before the first write is
-// what lets an output be its input.
+// plus its rank in a ballot.  Everything is read before the first write, which
+// is what lets an output be its input.
 //
-// The e-th lowest key is found bit by bit: 32 counts of the keys below a
-// candidate.  Bound: latency (the row is 8 bytes an entry; 32 dependent
-// counts).
+// The key below which everything goes is found 8 bits a step, from a histogram
+// in LDS of the digits of the keys that still match.  Rows up to 1024 E keep
+// their keys in registers (a protected entry's above every key); longer ones (E
+// = 0) are copied to the workspace and read from there.  Bound: latency, of a
+// row of 8 bytes an entry on one CU.  (Fixing the key bit by bit from counts
+// took 0.5 us a step: 12.8 us for rows of 2048, 44 us for one of 32768.)
 constexpr int kWaves = 16;
+constexpr uint32_t kNoKey = 0xFFFFFFFFu;    // above every order key
 
-struct Shared {
-    int count[2][kWaves];
-    int less[kWaves], equal[kWaves];
-};
-
-__device__ inline int sum_of(const int* c) {
-    int t = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) t += c[w];
-    return t;
+// Sum over a wave, in every lane.
+__device__ inline int wave_sum(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0xB1, 0xF, 0xF, true);       // neighbours
+    x += __builtin_amdgcn_update_dpp(0, x, 0x4E, 0xF, 0xF, true);       // pairs
+    x += __builtin_amdgcn_update_dpp(0, x, 0x141, 0xF, 0xF, true);      // mirrored in 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x140, 0xF, 0xF, true);      // mirrored in 16
+    auto a = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+    x = (int)(a[0] + a[1]);
+    auto b = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)x, false, false);
+    return (int)(b[0] + b[1]);
 }
+
+// Sum over a wave up to and with each lane.
+__device__ inline int wave_scan(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);     // one to the right, in rows of 16
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);     // a row's last to the next row
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);     // the half's last to the other half
+    return x;
+}
+
+// Where the entries of a wave go, 64 after 64.
+struct Places {
+    uint32_t key;       // keys below it go, and the first `ties` equal to it
+    int ties, kept, used;
+    int gone, equal;    // of the entries so far
+
+    // the place of entry b of this lane, ~place if it goes
+    __device__ inline int next(int b, uint32_t k) {
+        uint64_t eq = __ballot(k == key);
+        const int room = ties - equal, here = __popcll(eq);
+        equal += here;
+        if (here > room) {      // the tie that is cut, once a row, and those after it
+            if (room <= 0) eq = 0;
+            else
+                while (__popcll(eq) > room) eq &= ~(1ull << (63 - __builtin_clzll(eq)));
+        }
+        const uint64_t out = eq | __ballot(k < key);
+        const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(out >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)out, gone));
+        gone += __popcll(out);
+        const bool mine = (out >> (threadIdx.x & 63)) & 1;
+        return mine ? ~(kept + before) : (b >= used ? b : b - before);
+    }
+};
 
 template <int E>
 __global__ __launch_bounds__(1024) void evict_kernel(EvictArgs a) {
-    __shared__ Shared sh;
+    // a step's each; copies for lanes that would queue on one digit's address (masses share their leading bits), on
+    // banks of their own
+    constexpr int kCopies = E == 2 ? 2 : 8, kHist = 256 + 8;
+    __shared__ __attribute__((aligned(16))) int hist[4][kCopies][kHist];
+    __shared__ int ranks[2][kWaves];
     const int s = blockIdx.x;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = (int64_t)s * a.n;
     const int n_row = (int)a.n;
-    const int given = a.kv_len[s];
     const int len = kv_len_of(a.kv_len, s, a.n * a.B);
-    if (threadIdx.x == 0 && given != len) atomicOr(a.err, DEVERR_LEN);
+    if (threadIdx.x == 0 && a.kv_len[s] != len) atomicOr(a.err, DEVERR_LEN);
     const int used = (int)(((int64_t)len + a.B - 1) / a.B);
     const int lo = a.first < used ? a.first : used;
     const int hi = used - a.last > lo ? used - a.last : lo;    // candidates [lo, hi)
     const int64_t over = used > a.budget ? used - a.budget : 0;
     const int gone = over < hi - lo ? (int)over : hi - lo;
 
-    const int per_wave = E > 0 ? 64 * E : (n_row + 64 * kWaves - 1) / (64 * kWaves) * 64;
-    const int w0 = wave * per_wave;
     constexpr int kHeld = E > 0 ? E : 1;
-    int32_t held_t[kHeld];
-    float held_m[kHeld];
-    const int steps = E > 0 ? E : per_wave / 64;
+    const int steps = E > 0 ? E : (n_row + 64 * kWaves - 1) / (64 * kWaves);
+    const int w0 = wave * 64 * steps;
+    uint32_t keys[kHeld];
     int32_t* const copy_t = static_cast<int32_t*>(a.ws) + (E > 0 ? 0 : row);
     float* const copy_m = static_cast<float*>(a.ws) + (E > 0 ? 0 : (int64_t)a.S * a.n + row);
+    auto key_of = [&](int b, float m) { return b >= lo && b < hi ? order_key(m) : kNoKey; };
+    auto copied_key = [&](int b) { return b < n_row ? key_of(b, copy_m[b]) : kNoKey; };
 
+    for (int x = threadIdx.x; x < 4 * kCopies * kHist; x += 1024) (&hist[0][0][0])[x] = 0;
     if constexpr (E > 0) {
 #pragma unroll
         for (int e = 0; e < kHeld; ++e) {
             const int b = w0 + 64 * e + lane;
-            if (b < n_row) {
-                held_t[e] = a.tables[row + b];
-                held_m[e] = a.mass[row + b];
-            }
+            keys[e] = key_of(b, b < n_row ? a.mass[row + b] : 0.f);
         }
     } else {
         for (int e = 0; e < steps; ++e) {
@@ -126,70 +164,113 @@ __global__ __launch_bounds__(1024) void evict_kernel(EvictArgs a) {
             }
         }
     }
-    auto mass_of = [&](int e, int b) { return E > 0 ? held_m[E > 0 ? e : 0] : copy_m[b]; };
-    auto table_of = [&](int e, int b) { return E > 0 ? held_t[E > 0 ? e : 0] : copy_t[b]; };
+    __syncthreads();
 
-    // the key below which everything goes, and how many equal to it go too
+    // the largest key with fewer than `gone` candidates below it
     uint32_t key = 0;
-    int ties = 0;
+    int below = 0;      // candidates below the bits fixed so far
     if (gone > 0) {
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t cand = key | (1u << bit);
-            int c = 0;
+        for (int step = 0; step < 4; ++step) {
+            const int shift = 24 - 8 * step;
+            // protected entries are above every key in each digit or an earlier one: counted, they change no digit below
+            auto count = [&](uint32_t k) {
+                if (step == 0 || (k ^ key) >> (shift + 8) == 0) atomicAdd(&hist[step][lane % kCopies][k >> shift & 255], 1);
+            };
+            if constexpr (E > 0) {
 #pragma unroll
-            for (int e = 0; e < (E > 0 ? E : steps); ++e) {
-                const int b = w0 + 64 * e + lane;
-                c += __popcll(__ballot(b >= lo && b < hi && order_key(mass_of(e, b)) < cand));
+                for (int e = 0; e < kHeld; ++e) count(keys[e]);
+            } else {
+                for (int e = 0; e < steps; ++e) count(copied_key(w0 + 64 * e + lane));
             }
-            int* const slot = sh.count[bit & 1];
-            if (lane == 0) slot[wave] = c;
             __syncthreads();
-            if (sum_of(slot) < gone) key = cand;
+            // every wave finds the digit for itself, four a lane
+            int4 c = make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int4 x = *reinterpret_cast<const int4*>(&hist[step][i][4 * lane]);
+                c = make_int4(c.x + x.x, c.y + x.y, c.z + x.z, c.w + x.w);
+            }
+            const int own = c.x + c.y + c.z + c.w, upto = below + wave_scan(own);
+            const int at = __builtin_ctzll(__ballot(upto >= gone));     // some lane: no more go than there are candidates
+            int sum = upto - own, digit = 4 * lane;
+            const int three[3] = {c.x, c.y, c.z};
+            bool on = true;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                on = on && sum + three[i] < gone;
+                sum += on ? three[i] : 0;
+                digit += on;
+            }
+            key |= (uint32_t)__builtin_amdgcn_readlane(digit, at) << shift;
+            below = __builtin_amdgcn_readlane(sum, at);
         }
     }
+
     // places: kept entries in order, then the evicted ones
-    int below = 0, equal = 0;
-    if (gone > 0) {
+    int wave_below = 0, wave_equal = 0;
+    if constexpr (E > 0) {
 #pragma unroll
-        for (int e = 0; e < (E > 0 ? E : steps); ++e) {
-            const int b = w0 + 64 * e + lane;
-            const bool in = b >= lo && b < hi;
-            const uint32_t k = in ? order_key(mass_of(e, b)) : 0u;
-            below += __popcll(__ballot(in && k < key));
-            equal += __popcll(__ballot(in && k == key));
+        for (int e = 0; e < kHeld; ++e) {
+            wave_below += keys[e] < key;
+            wave_equal += keys[e] == key;
+        }
+    } else {
+        for (int e = 0; e < steps; ++e) {
+            const uint32_t k = copied_key(w0 + 64 * e + lane);
+            wave_below += k < key;
+            wave_equal += k == key;
         }
     }
+    wave_below = wave_sum(wave_below);
+    wave_equal = wave_sum(wave_equal);
     if (lane == 0) {
-        sh.less[wave] = below;
-        sh.equal[wave] = equal;
+        ranks[0][wave] = wave_below;
+        ranks[1][wave] = wave_equal;
     }
-    __syncthreads();        // also: every read of the inputs is done before the first write below
-    ties = gone - sum_of(sh.less);
-    int below_before = 0, equal_before = 0;
+    __syncthreads();
+    Places p{key, gone - below, used - gone, used, 0, 0};
     for (int w = 0; w < wave; ++w) {
-        below_before += sh.less[w];
-        equal_before += sh.equal[w];
+        p.gone += ranks[0][w];
+        p.equal += ranks[1][w];
     }
-    const uint64_t before = (1ull << lane) - 1;
-    const int kept = used - gone;
+    p.gone += p.equal < p.ties ? p.equal : p.ties;
+    if constexpr (E > 0) {
+        // in place of the keys; then the tables and the masses, each read whole before its first write
 #pragma unroll
-    for (int e = 0; e < (E > 0 ? E : steps); ++e) {
-        const int b = w0 + 64 * e + lane;
-        const bool in = gone > 0 && b >= lo && b < hi;
-        const float m = b < n_row ? mass_of(e, b) : 0.f;
-        const uint32_t k = order_key(m);
-        const uint64_t lt = __ballot(in && k < key), eq = __ballot(in && k == key);
-        const int eq_at = equal_before + __popcll(eq & before);
-        // evicted entries before this one: those below the key, and of those equal to it the first `ties`
-        const int out_before = below_before + __popcll(lt & before) + (eq_at < ties ? eq_at : ties);
-        const bool out = in && (k < key || (k == key && eq_at < ties));
-        if (b < n_row) {
-            const int to = b >= used ? b : (out ? kept + out_before : b - out_before);
-            a.tables_out[row + to] = table_of(e, b);
-            a.mass_out[row + to] = out ? 0.f : m;
+        for (int e = 0; e < kHeld; ++e) keys[e] = (uint32_t)p.next(w0 + 64 * e + lane, keys[e]);
+        int32_t table[kHeld];
+#pragma unroll
+        for (int e = 0; e < kHeld; ++e) {
+            const int b = w0 + 64 * e + lane;
+            table[e] = b < n_row ? a.tables[row + b] : 0;
         }
-        below_before += __popcll(lt);
-        equal_before += __popcll(eq);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kHeld; ++e) {
+            const int to = (int)keys[e] < 0 ? ~(int)keys[e] : (int)keys[e];
+            if (w0 + 64 * e + lane < n_row) a.tables_out[row + to] = table[e];
+        }
+        float mass[kHeld];
+#pragma unroll
+        for (int e = 0; e < kHeld; ++e) {
+            const int b = w0 + 64 * e + lane;
+            mass[e] = b < n_row ? a.mass[row + b] : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kHeld; ++e) {
+            const int to = (int)keys[e] < 0 ? ~(int)keys[e] : (int)keys[e];
+            if (w0 + 64 * e + lane < n_row) a.mass_out[row + to] = (int)keys[e] < 0 ? 0.f : mass[e];
+        }
+    } else {
+        for (int e = 0; e < steps; ++e) {
+            const int b = w0 + 64 * e + lane;
+            const int place = p.next(b, copied_key(b)), to = place < 0 ? ~place : place;
+            if (b < n_row) {
+                a.tables_out[row + to] = copy_t[b];
+                a.mass_out[row + to] = place < 0 ? 0.f : copy_m[b];
+            }
+        }
     }
     if (threadIdx.x == 0) {
         a.kv_len_out[s] = len - gone * a.B;
