@@ -16,16 +16,17 @@ _KINDS = {"none": _lib.PRED_ROPE_NONE, "linear": _lib.PRED_ROPE_LINEAR, "ntk": _
           "llama3": _lib.PRED_ROPE_LLAMA3, "yarn": _lib.PRED_ROPE_YARN}
 
 # torch and the dtypes a tensor may have, from the first call that takes tensors on (the package itself needs none)
-torch = _BF16 = _FP8 = _WORD = _I32 = _F32 = None
+torch = _BF16 = _FP8 = _WORD = _I32 = _F32 = _current_raw = None
 
 
 def _load_torch():
-    global torch, _BF16, _FP8, _WORD, _I32, _F32
+    global torch, _BF16, _FP8, _WORD, _I32, _F32, _current_raw
     import torch as t
     _BF16 = (t.bfloat16, t.int16, t.uint16)
     _FP8 = (t.float8_e4m3fn, t.uint8)
     _WORD = (t.int64, t.uint64)
     _I32, _F32 = (t.int32,), (t.float32,)
+    _current_raw = getattr(t._C, "_cuda_getCurrentRawStream", None)
     torch = t
 
 
@@ -46,9 +47,10 @@ def _dims(h):
     return _pkg().pred_get_dims(h) if d is None else d
 
 
-def _raw_stream(stream):
+def _raw_stream(stream, device):
+    """The stream's handle (the current one's without making a Stream object of it, 2.5 us of a 10 us call)."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_raw(device) if _current_raw else torch.cuda.current_stream(device).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -187,7 +189,7 @@ def pred_rotate(h, rope, x, positions, out, stream=None):
     xp, xs = a.rows(x, "x", n, heads, d.head_dim)
     op, os_ = a.rows(out, "out", n, heads, d.head_dim)
     _check(_lib.load().pred_rotate(h, rope._on(a), xp, xs, n, heads, a.ptr(positions, "positions", _I32, (n,)),
-                                   op, os_, _raw_stream(stream)))
+                                   op, os_, _raw_stream(stream, a.device)))
 
 
 def pred_rotate_store(h, rope, q, k, v, positions, slots, cache, q_out, stream=None):
@@ -203,7 +205,7 @@ def pred_rotate_store(h, rope, q, k, v, positions, slots, cache, q_out, stream=N
     _check(_lib.load().pred_rotate_store(
         h, rope._on(a), qp, qs, kp, ks, vp, vs, n, a.ptr(positions, "positions", _I32, (n,)),
         a.ptr(slots, "slots", _WORD[:1], (n,)), cache._of(d, a),
-        a.ptr(q_out, "q_out", _BF16, (n, d.num_q_heads, d.head_dim)), _raw_stream(stream)))
+        a.ptr(q_out, "q_out", _BF16, (n, d.num_q_heads, d.head_dim)), _raw_stream(stream, a.device)))
 
 
 def pred_attend_workspace_bytes(h, n_seqs, n_rows, n_blocks):
@@ -242,7 +244,7 @@ def pred_attend(h, cache, q, tree, block_tables, kv_len, draft_len, scale, out, 
         a.ptr(block_tables, "block_tables", _I32, (S, n_blocks)), n_blocks, S, a.ptr(kv_len, "kv_len", _I32, (S,)),
         a.ptr(draft_len, "draft_len", _I32, (S,)), scale, a.ptr(out, "out", _BF16, shape),
         a.ptr(lse, "lse", _F32, shape[:3]), a.ptr(block_lse, "block_lse", _F32, (S, n_blocks, M, d.num_q_heads)),
-        ws, ws_bytes, _raw_stream(stream)))
+        ws, ws_bytes, _raw_stream(stream, a.device)))
 
 
 def pred_accumulate_weight(h, lse, block_lse, accepted, kv_len, decay, mass, mass_out=None, stream=None):
@@ -257,7 +259,7 @@ def pred_accumulate_weight(h, lse, block_lse, accepted, kv_len, decay, mass, mas
     _check(_lib.load().pred_accumulate_weight(
         h, a.ptr(lse, "lse", _F32, (S, M, d.num_q_heads)), a.ptr(block_lse, "block_lse", _F32, (S, n, M, d.num_q_heads)),
         M, a.ptr(accepted, "accepted", _WORD, (S,)), a.ptr(kv_len, "kv_len", _I32, (S,)), n, S, decay,
-        mass_ptr, mass_ptr if mass_out is None else a.ptr(mass_out, "mass_out", _F32, (S, n)), _raw_stream(stream)))
+        mass_ptr, mass_ptr if mass_out is None else a.ptr(mass_out, "mass_out", _F32, (S, n)), _raw_stream(stream, a.device)))
 
 
 def pred_evict_workspace_bytes(n_blocks, n_seqs):
@@ -280,4 +282,4 @@ def pred_evict_blocks(h, block_tables, mass, kv_len, budget, protect_first, prot
         a.ptr(kv_len, "kv_len", _I32, (S,)), n, S, budget, protect_first, protect_last,
         a.ptr(tables_out, "tables_out", _I32, shape), a.ptr(mass_out, "mass_out", _F32, shape),
         a.ptr(kv_len_out, "kv_len_out", _I32, (S,)), a.ptr(evicted, "evicted", _I32, (S,)), ws, ws_bytes,
-        _raw_stream(stream)))
+        _raw_stream(stream, a.device)))
