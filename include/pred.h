@@ -471,10 +471,12 @@ int pred_attend(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32
 size_t pred_attend_workspace_bytes(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_blocks);
 
 /* Name of the kernel pred_attend runs for this handle, cache and shape (host
- * only, static string): "attend_stream_kernel" (up to 32 queries per kv head),
- * "attend_tree_kernel" (more) or "attend_plain_kernel" (head sizes other than
- * 64 and 128, cache rows off 16-byte alignment, or block sizes the two do not
- * take).  NULL for a NULL argument or n_rows outside [1, 64]. */
+ * only, static string), for head sizes 64 and 128: "attend_stream_kernel" (up to
+ * 32 queries per kv head, block sizes a multiple of 1024 / (head_dim * element
+ * bytes)) or "attend_tree_kernel" (more queries, or other block sizes).
+ * "attend_plain_kernel" for other head sizes, cache rows off 16-byte alignment,
+ * and block_lse with a block size other than 8, 16 or a multiple of 32 up to
+ * 65536.  NULL for a NULL argument or n_rows outside [1, 64]. */
 const char* pred_attend_kernel_name(pred_t* p, const pred_kv_cache* cache, int32_t n_rows, int32_t with_block_lse);
 
 /* Accumulated attention weight of each block, from pred_attend's lse and

@@ -1392,11 +1392,11 @@ Kind kind_of(const AttendArgs& a) {
     if (!aligned_to(a.cache.k, 16) || !aligned_to(a.cache.v, 16) ||
         ((a.cache.block_stride | a.cache.token_stride | a.cache.head_stride) * item) % 16 != 0)
         return Kind::Plain;
-    if (queries_of(a) > kStreamQueries) return Kind::Tree;
-    // a wave-load's tokens lie in one block, within 32-bit offsets of its first
+    // the stream kernel's wave-loads take tokens of one block, within 32-bit offsets of the first (the tree kernel
+    // finds every token's place for itself: 32 queries over blocks of 8 FP8 rows of 64 take it as well)
     const int tpl = 1024 / (a.D * item);
-    if (a.B % tpl != 0 || a.cache.token_stride > (1 << 24)) return Kind::Plain;
-    return Kind::Stream;
+    const bool fits = a.B % tpl == 0 && a.cache.token_stride <= (1 << 24);
+    return fits && queries_of(a) <= kStreamQueries ? Kind::Stream : Kind::Tree;
 }
 
 Plan plan_of(const AttendArgs& a, bool tree) {
@@ -1449,7 +1449,9 @@ void launch_join(const AttendArgs& a, const Plan& pl, uint32_t rows, hipStream_t
 size_t attend_workspace_bytes(const AttendArgs& a) {
     if (a.D != 64 && a.D != 128) return 0;
     // of a call without block_lse, whose runs can be the shorter
-    return plan_bytes(a, plan_of(a, queries_of(a) > kStreamQueries));
+    const size_t tree = plan_bytes(a, plan_of(a, true));
+    const size_t stream = queries_of(a) > kStreamQueries ? 0 : plan_bytes(a, plan_of(a, false));
+    return tree > stream ? tree : stream;
 }
 
 const char* attend_kernel_name(const AttendArgs& a) {

@@ -603,6 +603,89 @@ def test_attend_long_context_split(M):
             assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("S,M,Hq,Hk,D,B,n,dtype", [
+    (65, 1, 4, 1, 64, 16, 40, torch.bfloat16), (150, 3, 4, 2, 128, 16, 40, FP8), (700, 1, 8, 1, 64, 8, 30, torch.bfloat16),
+    (129, 20, 4, 2, 64, 16, 40, FP8), (300, 64, 2, 1, 128, 32, 12, torch.bfloat16)])
+def test_attend_many_sequences(S, M, Hq, Hk, D, B, n, dtype):
+    """More sequences than a wave has lanes, of very different lengths (one of every block, others of nothing): sampled
+    sequences against the oracle, the ends of each 64 among them; the same bits again."""
+    _say("attend many", S, M, Hq, Hk, D, B, n, dtype)
+    g = torch.Generator().manual_seed(S + M)
+    lens = torch.randint(0, 3 * B, (S,), generator=g)
+    lens[S // 2] = lens[1] = n * B
+    lens[[0, 2, 63, S - 1]] = torch.tensor([0, 1, n * B - 1, 5])
+    drafts = torch.minimum(torch.randint(0, M + 1, (S,), generator=g), lens)
+    c = Case(S, M, Hq, Hk, D, B, n, dtype, tree="tree", lens=lens, drafts=drafts)
+    with _handle(Hq, Hk, D, B, c.N) as p:
+        c.run(p)
+        rk.pred_device_error(p.handle)
+        c.check(seqs=sorted({0, 1, 2, 3, 62, 63, 64, S // 2, S // 2 + 1, S - 2, S - 1}))
+        again = [t.clone() for t in (c.out, c.lse, c.block_lse)]
+        c.run(p)
+        for got, want in zip((c.out, c.lse, c.block_lse), again):
+            assert torch.equal(got, want)
+
+
+KERNELS = [     # Hq, Hk, D, B, M, dtype, with block_lse, the kernel
+    (32, 8, 128, 16, 1, torch.bfloat16, True, "attend_stream_kernel"),
+    (32, 8, 128, 16, 8, FP8, True, "attend_stream_kernel"),        # 32 queries for each kv head
+    (32, 8, 128, 16, 9, FP8, True, "attend_tree_kernel"),
+    (8, 2, 64, 8, 1, torch.bfloat16, True, "attend_stream_kernel"),
+    (8, 2, 64, 8, 1, FP8, True, "attend_tree_kernel"),             # a wave-load is 16 tokens
+    (8, 2, 64, 8, 64, FP8, False, "attend_tree_kernel"),
+    (4, 2, 128, 7, 2, torch.bfloat16, False, "attend_tree_kernel"),
+    (4, 2, 128, 7, 2, torch.bfloat16, True, "attend_plain_kernel"),
+    (4, 2, 64, 1, 1, FP8, False, "attend_tree_kernel"),
+    (4, 2, 80, 16, 1, torch.bfloat16, False, "attend_plain_kernel"),
+]
+
+
+@pytest.mark.parametrize("Hq,Hk,D,B,M,dtype,weights,name", KERNELS)
+def test_attend_kernel_of_a_shape(Hq, Hk, D, B, M, dtype, weights, name):
+    """The kernel that runs for a shape, over a context of many runs and a short one, against the oracle."""
+    _say("attend kernel", Hq, Hk, D, B, M, dtype, weights, name)
+    n = 1500 // B
+    c = Case(2, M, Hq, Hk, D, B, n, dtype, tree="tree", lens=[n * B, M], drafts=[M, M])
+    with _handle(Hq, Hk, D, B, c.N) as p:
+        assert rk.pred_attend_kernel_name(p.handle, c.kv, M, weights) == name
+        c.run(p, weights)
+        rk.pred_device_error(p.handle)
+        c.check(weights)
+
+
+@pytest.mark.parametrize("Hq,Hk,D,B,M", SHAPES)
+def test_attend_scales(Hq, Hk, D, B, M):
+    """A scale of zero weighs every seen token alike; a negative one turns the order round."""
+    n = 4
+    for scale in (0.0, -0.3):
+        c = Case(2, M, Hq, Hk, D, B, n, lens=[n * B, n * B // 2 + 1], drafts=[1, min(M, n * B // 2 + 1)])
+        c.scale = scale
+        with _handle(Hq, Hk, D, B, c.N) as p:
+            c.run(p)
+            rk.pred_device_error(p.handle)
+            c.scale = scale
+            _check_scaled(c)
+
+
+def _check_scaled(c):
+    """Case.check, whose tolerance takes the scale's magnitude."""
+    q, k, v, out, lse = _f64(c.q), _f64(c.k), _f64(c.v), _f64(c.out), _f64(c.lse)
+    g = c.Hq // c.Hk
+    for s in range(c.S):
+        length, drafted = int(c.lens[s]), int(c.drafts[s])
+        pages = c.tables[s, :-(-length // c.B)].cpu().numpy()
+        seen = np.repeat(cache.seen_by(c.M, length, drafted, None), g, axis=0)
+        for h in range(c.Hk):
+            kk, vv = (t[pages, :, h].reshape(-1, c.D)[:length] for t in (k, v))
+            qq = q[s, :, h * g:h * g + g].reshape(-1, c.D)
+            want, want_lse, _, absolute = cache.attend_one(qq, kk, vv, seen, c.scale)
+            delta = (c.D + 4) * 2.0 ** -24 * abs(c.scale) * (np.abs(qq) @ np.abs(kk).T).max()
+            rel = 2 * delta + 2.0 ** -20 + 2.0 ** -16 + (length + 64) * 2.0 ** -24
+            got = out[s, :, h * g:h * g + g].reshape(-1, c.D)
+            assert np.all(np.abs(got - want) <= HALF_BF16 * np.abs(want) + rel * absolute), ("out", s, h)
+            Case._close_log(lse[s, :, h * g:h * g + g].reshape(-1), want_lse, rel, ("lse", s, h))
+
+
 # ---------------------------------------------------------------- weight and eviction
 
 @pytest.mark.parametrize("S,M,Hq,B,n", [(1, 1, 4, 16, 7), (3, 1, 32, 16, 300), (2, 5, 5, 8, 33), (2, 64, 8, 16, 50),
