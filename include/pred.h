@@ -473,7 +473,7 @@ size_t pred_attend_workspace_bytes(pred_t* p, int32_t n_seqs, int32_t n_rows, in
 /* Name of the kernel pred_attend runs for this handle, cache and shape (host
  * only, static string), for head sizes 64 and 128: "attend_stream_kernel" (up to
  * 32 queries per kv head, block sizes a multiple of 1024 / (head_dim * element
- * bytes)) or "attend_tree_kernel" (more queries, or other block sizes).
+ * bytes), a block's tokens within 2 GiB) or "attend_tree_kernel" (the others).
  * "attend_plain_kernel" for other head sizes, cache rows off 16-byte alignment,
  * and block_lse with a block size other than 8, 16 or a multiple of 32 up to
  * 65536.  NULL for a NULL argument or n_rows outside [1, 64]. */

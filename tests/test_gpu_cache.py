@@ -653,6 +653,24 @@ def test_attend_kernel_of_a_shape(Hq, Hk, D, B, M, dtype, weights, name):
         c.check(weights)
 
 
+@pytest.mark.parametrize("M", [1, 40])
+def test_attend_block_beyond_two_gib(M):
+    """A block whose tokens lie 4 MiB apart, 2.5 GiB in all: offsets inside it pass 31 bits."""
+    Hq, Hk, D, B, apart = 4, 2, 64, 640, 1 << 21
+    c = Case(1, M, Hq, Hk, D, B, 1, identity=True, tree="tree")
+    for name in ("k", "v"):
+        far = torch.empty((B * apart,), dtype=torch.bfloat16, device="cuda")
+        far = far.as_strided((1, B, Hk, D), (B * apart, apart, D, 1))
+        far.copy_(getattr(c, name))
+        setattr(c, name, far)
+    c.kv = rk.KVCache(c.k, c.v)
+    with _handle(Hq, Hk, D, B, 1) as p:
+        assert rk.pred_attend_kernel_name(p.handle, c.kv, M) == "attend_tree_kernel"
+        c.run(p, weights=False)
+        rk.pred_device_error(p.handle)
+        c.check(weights=False)
+
+
 @pytest.mark.parametrize("Hq,Hk,D,B,M", SHAPES)
 def test_attend_scales(Hq, Hk, D, B, M):
     """A scale of zero weighs every seen token alike; a negative one turns the order round."""
