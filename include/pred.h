@@ -429,7 +429,8 @@ int pred_rotate(pred_t* p, const pred_rope* rope, const pred_bf16* x, int64_t x_
  *   q_out      device, [n_tokens, num_q_heads, head_dim] bf16; may be q itself if q_stride is num_q_heads * head_dim
  * A bf16 cache takes keys and values rounded once; an FP8 cache takes value /
  * scale clamped to +-448 and rounded once (nearest, ties to even), NaN kept.
- * rope->backward must be 0. */
+ * rope->backward must be 0, and the cache's k and v must not overlap (one
+ * address for both is PRED_ERR_OUT_OF_RANGE). */
 int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int64_t q_stride, const pred_bf16* k,
                       int64_t k_stride, const pred_bf16* v, int64_t v_stride, int64_t n_tokens,
                       const int32_t* positions, const int64_t* slots, const pred_kv_cache* cache, pred_bf16* q_out,
@@ -446,7 +447,8 @@ int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int6
  *   block_tables  device, [n_seqs, n_blocks] int32 physical ids, or NULL for the identity
  *   kv_len        device, [n_seqs] int32 in [0, n_blocks * block_size], or NULL for that upper limit
  *   draft_len     device, [n_seqs] int32 in [0, min(n_rows, kv_len)], or NULL for that upper limit
- *   out           device, [n_seqs, n_rows, num_q_heads, head_dim] bf16: softmax(scale * q k) v over the row's tokens
+ *   out           device, [n_seqs, n_rows, num_q_heads, head_dim] bf16: softmax(scale * q k) v over the row's tokens;
+ *                 must not overlap q (PRED_ERR_OUT_OF_RANGE)
  *   lse           device, [n_seqs, n_rows, num_q_heads] float32 or NULL: the log of the softmax's sum
  *   block_lse     device, [n_seqs, n_blocks, n_rows, num_q_heads] float32 or NULL: the same sum over each block's
  *                 tokens alone, for pred_accumulate_weight; blocks at or past kv_len / block_size rounded up are left

@@ -232,6 +232,8 @@ def pred_attend(h, cache, q, tree, block_tables, kv_len, draft_len, scale, out, 
         raise TypeError("q: expected a tensor [n_seqs, n_rows, num_q_heads, head_dim]")
     S, M = q.shape[0], q.shape[1]
     if block_tables is not None:
+        if not isinstance(block_tables, torch.Tensor):
+            raise TypeError("block_tables: expected a torch.Tensor")
         if block_tables.dim() != 2:
             raise ValueError("block_tables must be [n_seqs, n_blocks]")
         n_blocks = block_tables.shape[1]

@@ -1415,7 +1415,7 @@ Plan plan_of(const AttendArgs& a, bool tree) {
     // and its partial results (8 sequences of 5k tokens, 13 rows: 75 us with 1, 91 with 2, 109 with 4).
     pl.slots = 2 * a.n_cu;
     pl.run = tree ? 2048 : 2560;
-    const int64_t most = (int64_t)a.S * a.n * a.B * pl.groups * a.Hk / pl.slots / pl.run;
+    const double most = (double)a.S * a.n * a.B * pl.groups * a.Hk / pl.slots / pl.run;
     pl.rounds = most < 1 ? 1 : (most < kRounds ? (int)most : kRounds);
     return pl;
 }

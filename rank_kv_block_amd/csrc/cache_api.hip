@@ -228,6 +228,7 @@ int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int6
     if (rope->backward) return fail(PRED_ERR_UNSUPPORTED, "rotate_store: rope->backward must be 0");
     pred::CacheView view;
     if ((rc = check_cache(p, cache, &view, "rotate_store"))) return rc;
+    if (cache->k == cache->v) return fail(PRED_ERR_OUT_OF_RANGE, "rotate_store: the cache's k and v are one");
     if (n_tokens < 0) return fail(PRED_ERR_OUT_OF_RANGE, "rotate_store: n_tokens (%lld) < 0", (long long)n_tokens);
     if (n_tokens == 0) return ok();
     if (!positions || !slots) return fail(PRED_ERR_NULL_ARG, "rotate_store: positions or slots is NULL");
@@ -300,6 +301,10 @@ int pred_attend(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32
     if (!q || !out) return fail(PRED_ERR_NULL_ARG, "attend: q or out is NULL");
     if (!pred::aligned16(q) || !pred::aligned16(out))
         return fail(PRED_ERR_UNSUPPORTED, "attend: q and out must be 16-byte aligned");
+    // a row's queries are read by several workgroups, and its output may be written before the last of them starts
+    const uint64_t bytes = (uint64_t)n_seqs * n_rows * p->d.num_q_heads * p->d.head_dim * 2;
+    const uint64_t from = (uint64_t)(uintptr_t)q, to = (uint64_t)(uintptr_t)out;
+    if (from < to + bytes && to < from + bytes) return fail(PRED_ERR_OUT_OF_RANGE, "attend: out overlaps q");
     pred::AttendArgs a = attend_shape(p, n_seqs, n_rows, n_blocks);
     const size_t need = n_blocks > 0 ? pred::attend_workspace_bytes(a) : 0;
     if (need > 0 && (!workspace || ws_bytes < need))

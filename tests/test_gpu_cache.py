@@ -950,6 +950,36 @@ def test_refusals():
         assert e.value.code == rk.PRED_ERR_UNSUPPORTED
 
 
+def test_overlaps_are_refused():
+    """An attention whose output lies on its queries, a store into a cache whose k and v are one."""
+    D, B, Hk, N = 64, 16, 2, 8
+    z = dict(device="cuda")
+    with _handle(4, Hk, D, B, N) as p:
+        k, v = _cache_tensors(N, B, Hk, D, torch.bfloat16, "tokens", fill=0.0)
+        kv, lens = rk.KVCache(k, v), torch.ones((2,), dtype=torch.int32, **z)
+        both = torch.zeros((3, 1, 4, D), dtype=torch.bfloat16, **z)
+        ws = torch.empty((rk.pred_attend_workspace_bytes(p.handle, 2, 1, N) + 16,), dtype=torch.uint8, **z)
+
+        def attend(q, out, table=None):
+            rk.pred_attend(p.handle, kv, q, None, table, lens[:q.shape[0]], None, 1.0, out, workspace=ws)
+
+        attend(both[:1], both[1:2])         # side by side
+        for q, out in ((both[:2], both[:2]), (both[:2], both[1:]), (both[1:], both[:2])):
+            with pytest.raises(rk.PredError) as e:
+                attend(q, out)
+            assert e.value.code == rk.PRED_ERR_OUT_OF_RANGE and "overlaps" in str(e.value)
+        with pytest.raises(TypeError):
+            attend(both[:1], both[1:2], np.zeros((1, N), np.int32))
+        rope, _, _ = _rope(64)
+        x = torch.zeros((3, 4, D), dtype=torch.bfloat16, **z)
+        kk = torch.zeros((3, Hk, D), dtype=torch.bfloat16, **z)
+        slots, pos = torch.full((3,), -1, dtype=torch.int64, **z), torch.zeros((3,), dtype=torch.int32, **z)
+        with pytest.raises(rk.PredError) as e:
+            rk.pred_rotate_store(p.handle, rope, x, kk, kk, pos, slots, rk.KVCache(k, k), torch.empty_like(x))
+        assert e.value.code == rk.PRED_ERR_OUT_OF_RANGE
+        rk.pred_device_error(p.handle)
+
+
 def test_nothing_to_do():
     with _handle(4, 1, 64, 16, 4) as p:
         h = p.handle
