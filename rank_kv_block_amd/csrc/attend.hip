@@ -27,6 +27,12 @@ __device__ inline void check_lengths(const AttendArgs& a, int s, int len, int dr
     if ((a.kv_len && a.kv_len[s] != len) || (a.draft && a.draft[s] != drafted)) atomicOr(a.err, DEVERR_LEN);
 }
 
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t bf16_pair(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){lo, hi}, bf16x2_t));
+}
+
 __device__ inline uint16_t to_bf16(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
 
 __device__ inline float fp8_value(uint32_t byte) { return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0); }
@@ -268,38 +274,97 @@ __device__ inline float2* part_stats(const AttendArgs& a, const Plan& pl, int64_
     return reinterpret_cast<float2*>(part_sums(a, pl, most_items(a, pl))) + slot * pl.rows;
 }
 
-// Joins a row's runs: out = sum_r 2^(m_r - m) o_r / sum_r 2^(m_r - m) l_r.
-// WAVES waves share a row (sequence, drafted row, query head), wave w taking
-// runs w, w + WAVES, ..: a lane reads one run's (maximum, total), then the
-// wave adds the runs' sums, 4 values a lane and 64 / (D / 4) runs at a time.
-// Latency bound, so a row with many runs gets four waves.
-template <int D, int WAVES>
+// Joins a row's runs: out = sum_r 2^(m_r - m) o_r / sum_r 2^(m_r - m) l_r, for a
+// row (sequence, drafted row, query head) that has more than one.
+struct JoinRow {
+    int h, s, runs, in_group;       // runs: 0 for a row past the draft, which has no partial sums
+    bool wanted;                    // else its items wrote the result
+    int64_t slot, step;             // of its first run, and from one to the next
+};
+__device__ inline JoinRow join_row(const AttendArgs& a, const Plan& pl, uint32_t row) {
+    JoinRow j;
+    j.h = (int)(row % (uint32_t)a.Hq);
+    const int i = (int)(row / (uint32_t)a.Hq % (uint32_t)a.M);
+    j.s = (int)(row / (uint32_t)a.Hq / (uint32_t)a.M);
+    const Share share = shares_of(a)[j.s];
+    j.wanted = share.runs > 1;
+    const int g = a.Hq / a.Hk, r = i * g + j.h % g;
+    j.runs = j.wanted && i < draft_len_of(a, j.s, share.len) ? share.runs : 0;
+    j.in_group = r % pl.rows;
+    j.step = (int64_t)a.Hk * share.groups;
+    j.slot = (int64_t)share.first * a.Hk + (int64_t)(j.h / g) * share.groups + r / pl.rows;
+    return j;
+}
+// 4 values of a row from its sums (v, l, m), the lse by the first lane
+__device__ inline void join_store(const AttendArgs& a, int D, uint32_t row, int d4, float4 v, float l, float m) {
+    const bool none = l == 0.f;
+    const float f = none ? 0.f : a.cache.v_scale / l;
+    const uint2 w = make_uint2(bf16_pair(v.x * f, v.y * f), bf16_pair(v.z * f, v.w * f));
+    *reinterpret_cast<uint2*>(a.out + (int64_t)row * D + 4 * d4) = none ? make_uint2(0, 0) : w;
+    if (a.lse && d4 == 0) a.lse[row] = none ? -INFINITY : (m + log2_of(l)) * kLn2;
+}
+
+// Rows of few runs: D / 4 lanes a row, 4 values each, that read the row's
+// (maximum, total) for themselves, kAhead runs in flight.
+template <int D>
+__global__ __launch_bounds__(256) void attend_join_rows_kernel(AttendArgs a, Plan pl, uint32_t rows) {
+    constexpr int lanes = D / 4, kAhead = 4;
+    const uint32_t row = blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
+    const int d4 = threadIdx.x % lanes;
+    if (row >= rows) return;
+    const JoinRow j = join_row(a, pl, row);
+    float m = kLowest, l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = 0; x0 < j.runs; x0 += kAhead) {
+        float4 o[kAhead];
+        float2 st[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+            st[e] = make_float2(kLowest, 0.f);
+            o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x0 + e >= j.runs) continue;
+            const int64_t slot = j.slot + (x0 + e) * j.step;
+            st[e] = part_stats(a, pl, slot)[j.in_group];
+            o[e] = reinterpret_cast<const float4*>(part_sums(a, pl, slot) + j.in_group * D)[d4];
+        }
+        float top = m;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) top = fmaxf(top, st[e].x);
+        const float alpha = exp2_of(m - top);
+        m = top;
+        l *= alpha;
+        v = make_float4(v.x * alpha, v.y * alpha, v.z * alpha, v.w * alpha);
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+            const float f = exp2_of(st[e].x - top);
+            l += f * st[e].y;
+            v = make_float4(v.x + f * o[e].x, v.y + f * o[e].y, v.z + f * o[e].z, v.w + f * o[e].w);
+        }
+    }
+    if (j.wanted) join_store(a, D, row, d4, v, l, m);
+}
+
+// Rows of many runs: a workgroup each, wave w taking runs w, w + 4, ..: a lane
+// reads one run's (maximum, total), then the wave adds the runs' sums, 4 values
+// a lane and 64 / (D / 4) runs at a time.
+template <int D>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl) {
     __shared__ float4 sums[4][64];
     __shared__ float2 stats[4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t row = (int64_t)blockIdx.x * (4 / WAVES) + wave / WAVES;      // [S, M, Hq]
-    if (row >= (int64_t)a.S * a.M * a.Hq) return;       // WAVES = 1 only: no barrier follows
-    const int h = (int)(row % a.Hq), i = (int)(row / a.Hq % a.M), s = (int)(row / a.Hq / a.M);
-    const Share share = shares_of(a)[s];
-    if (share.runs == 1) return;        // its items wrote the result
-    const int g = a.Hq / a.Hk, r = i * g + h % g, group = r / pl.rows;
-    // a row past the draft has no partial sums: its result is that of no run
-    const int runs = i < draft_len_of(a, s, share.len) ? share.runs : 0;
-    auto slot_of = [&](int split) {
-        return (int64_t)share.first * a.Hk + ((int64_t)split * a.Hk + h / g) * share.groups + group;
-    };
-    const int in_group = r % pl.rows;
+    const uint32_t row = blockIdx.x;        // [S, M, Hq]
+    const JoinRow j = join_row(a, pl, row);
+    if (!j.wanted) return;
     constexpr int lanes = D / 4, groups = 64 / lanes, kAhead = 8;       // kAhead loads in flight a lane
     const int part = lane / lanes, d4 = lane % lanes;
     float m = kLowest, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    // this wave's runs: w, w + WAVES, ..; 64 at a time for the statistics, groups * kAhead for the sums
-    const int mine = (runs - wave % WAVES + WAVES - 1) / WAVES;
+    // 64 at a time for the statistics, groups * kAhead for the sums
+    const int mine = (j.runs - wave + 3) / 4;
     for (int x0 = 0; x0 < mine; x0 += 64) {
-        auto slot_at = [&](int x) { return slot_of(wave % WAVES + x * WAVES); };
+        auto slot_at = [&](int x) { return j.slot + (int64_t)(wave + 4 * x) * j.step; };
         const int count = mine - x0 < 64 ? mine - x0 : 64;
-        const float2 st = lane < count ? part_stats(a, pl, slot_at(x0 + lane))[in_group] : make_float2(kLowest, 0.f);
+        const float2 st = lane < count ? part_stats(a, pl, slot_at(x0 + lane))[j.in_group] : make_float2(kLowest, 0.f);
         float top = m, weight = 0.f;
         for (int y0 = 0; y0 < count; y0 += groups * kAhead) {
             float4 o[kAhead];
@@ -307,7 +372,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
             for (int e = 0; e < kAhead; ++e) {
                 const int x = y0 + e * groups + part;
                 o[e] = reinterpret_cast<const float4*>(part_sums(a, pl, slot_at(x0 + (x < count ? x : 0))) +
-                                                       in_group * D)[d4];
+                                                       j.in_group * D)[d4];
             }
             if (y0 == 0) {
                 top = fmaxf(m, st.x);
@@ -333,36 +398,28 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
         v.z += __shfl_xor(v.z, o);
         v.w += __shfl_xor(v.w, o);
     }
-    if constexpr (WAVES > 1) {
-        sums[wave][lane] = v;
-        if (lane == 0) stats[wave] = make_float2(m, l);
-        __syncthreads();
-        if (wave != 0) return;
-        const float own = m;
-        for (int w = 1; w < WAVES; ++w) m = fmaxf(m, stats[w].x);
-        const float f = exp2_of(own - m);
-        l *= f;
-        v.x *= f;
-        v.y *= f;
-        v.z *= f;
-        v.w *= f;
-        for (int w = 1; w < WAVES; ++w) {
-            const float fw = exp2_of(stats[w].x - m);
-            const float4 o = sums[w][lane];
-            l += fw * stats[w].y;
-            v.x += fw * o.x;
-            v.y += fw * o.y;
-            v.z += fw * o.z;
-            v.w += fw * o.w;
-        }
+    sums[wave][lane] = v;
+    if (lane == 0) stats[wave] = make_float2(m, l);
+    __syncthreads();
+    if (wave != 0) return;
+    const float own = m;
+    for (int w = 1; w < 4; ++w) m = fmaxf(m, stats[w].x);
+    const float f = exp2_of(own - m);
+    l *= f;
+    v.x *= f;
+    v.y *= f;
+    v.z *= f;
+    v.w *= f;
+    for (int w = 1; w < 4; ++w) {
+        const float fw = exp2_of(stats[w].x - m);
+        const float4 o = sums[w][lane];
+        l += fw * stats[w].y;
+        v.x += fw * o.x;
+        v.y += fw * o.y;
+        v.z += fw * o.z;
+        v.w += fw * o.w;
     }
-    if (part != 0) return;
-    const bool none = l == 0.f;
-    const float f = none ? 0.f : a.cache.v_scale / l;
-    uint16_t w[4] = {to_bf16(none ? 0.f : v.x * f), to_bf16(none ? 0.f : v.y * f), to_bf16(none ? 0.f : v.z * f),
-                     to_bf16(none ? 0.f : v.w * f)};
-    *reinterpret_cast<uint2*>(a.out + row * a.D + 4 * d4) = *reinterpret_cast<uint2*>(w);
-    if (a.lse && d4 == 0) a.lse[row] = none ? -INFINITY : (m + log2_of(l)) * kLn2;
+    if (part == 0) join_store(a, D, row, d4, v, l, m);
 }
 
 // ---------------------------------------------------------------- stream kernel
@@ -422,9 +479,6 @@ __device__ inline float sum_over_c(float x) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-
 // Turns a product q k into units of log2: above 0, so that a masked -inf stays
 // one (the queries carry a negative scale's sign).
 __device__ inline float log2_scale(const AttendArgs& a) {
@@ -441,10 +495,6 @@ __device__ inline bf16x8_t signed_by(float scale, bf16x8_t x) {
 template <bool HI>
 __device__ inline uint32_t fp8x2_to_bf16(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI));
-}
-
-__device__ inline uint32_t bf16_pair(float lo, float hi) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){lo, hi}, bf16x2_t));
 }
 
 // Division of a token's index by the block size: one 64-bit product.  With
@@ -1437,13 +1487,14 @@ void launch_fast(const AttendArgs& a, Kind kind, const Plan& pl, uint32_t grid, 
     else attend_tree_kernel<D, FP8, 1><<<grid, 256, 0, stream>>>(a, pl, bs);
 }
 
-// Four waves a row where a sequence has runs enough for them, else one (131072
-// tokens of one sequence in 64 runs are 32 rows; a batch's 65536 rows have few
-// runs).
+// A workgroup for a row where a sequence has runs enough for its four waves,
+// else D / 4 lanes (131072 tokens of one sequence in 64 runs are 32 rows; a
+// batch's 65536 rows have few runs).
 template <int D>
 void launch_join(const AttendArgs& a, const Plan& pl, uint32_t rows, hipStream_t stream) {
-    if ((int64_t)pl.slots * pl.rounds > 8ll * a.S * a.Hk * pl.groups) attend_join_kernel<D, 4><<<rows, 256, 0, stream>>>(a, pl);
-    else attend_join_kernel<D, 1><<<(rows + 3) / 4, 256, 0, stream>>>(a, pl);
+    constexpr uint32_t per = 256 / (D / 4);
+    if ((int64_t)pl.slots * pl.rounds > 8ll * a.S * a.Hk * pl.groups) attend_join_kernel<D><<<rows, 256, 0, stream>>>(a, pl);
+    else attend_join_rows_kernel<D><<<(rows + per - 1) / per, 256, 0, stream>>>(a, pl, rows);
 }
 
 }  // namespace
