@@ -227,7 +227,7 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b) 
     uint32_t all = items_of(run);
     // Every sequence's last run is a part of one, so the items are a few more than wanted.  Where they pass one round
     // by up to a quarter, runs a little longer do without the second, nearly empty one (8 sequences of 5k tokens, 13
-    // rows: 78 -> 70 us; with more rounds there is nothing to gain).
+    // rows: 78 us without, 70 with; with more rounds there is nothing to gain).
     const uint32_t one = (uint32_t)pl.slots;
     int longer = run;
     for (uint32_t tries = 0, now = all; tries < 2 && all > one && all - one <= one / 4; ++tries) {
@@ -1019,8 +1019,8 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 // each wave with 32 queries of its own, or, in a group of up to 64 live ones,
 // two waves with the same 32 queries and half of each tile each (`pairs`).  The
 // stage is double buffered: a tile's loads are issued before the previous tile
-// is computed.  A bf16 tile of the context goes straight into LDS (991 us
-// through registers, 925 without, all 64 rows full); e4m3 is converted in
+// is computed.  A bf16 tile of the context goes straight into LDS (64 full rows:
+// 991 us a call through registers, 930 without); e4m3 is converted in
 // registers on the way, and tiles with drafted or missing tokens are cleaned
 // there.
 //
@@ -1039,11 +1039,10 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 //
 // Bound: at 512 queries per kv head the matrix cores and what feeds them (the
 // cache's bytes would take a quarter of the time); the weights' second bf16 term
-// makes the value product twice as long.  Measured, 16 sequences of up to 16384
-// tokens, 64 rows of 8 queries for each of 8 heads of 128: 978 us where all are
-// full, 550 TFLOP/s (a matrix product of the library's reaches 1233), of which
-// staging is 180, the scores 150 and the values 250; 503 us with block sums where
-// the lengths and drafts vary.  13 rows over 8 sequences of 5k tokens: 62 us.
+// makes the value product twice as long.  Measured, 16 sequences of 16384 tokens,
+// 64 rows of 8 queries for each of 8 heads of 128: 909 us, 600 TFLOP/s (a matrix
+// product of the library's reaches 1233); with block sums and lengths and drafts
+// that vary 489 us.  13 rows over 8 sequences of 5k tokens: 58 us.
 template <int D>
 struct TreeLds {
     static constexpr int kRow = 2 * D;              // bytes of a row
