@@ -568,6 +568,53 @@ def test_attend_bad_tables_and_lengths(Hq, Hk, D, B, M):
             c.check(weights=False)
 
 
+@pytest.mark.parametrize("Hq,Hk,D,M,dtype", [(32, 8, 128, 1, torch.bfloat16), (8, 2, 64, 5, FP8), (16, 2, 128, 40, torch.bfloat16),
+                                             (16, 2, 128, 8, torch.bfloat16), (16, 2, 128, 40, FP8), (8, 2, 64, 64, torch.bfloat16)])
+def test_attend_long_context_with_bad_entries(Hq, Hk, D, M, dtype):
+    """Invalid entries here and there in a long table, alone, side by side and at both ends, with NaN in every block that
+    no sequence has (block 0 among them): the other blocks' tokens against the oracle."""
+    _say("attend bad entries", Hq, Hk, D, M, dtype)
+    B, n, S = 16, 130, 2
+    c = Case(S, M, Hq, Hk, D, B, n, dtype, tree="tree", lens=[n * B, n * B - 37], drafts=[M, max(1, M // 2)])
+    c.tables = (1 + torch.randperm(c.N - 1, generator=c.g)[:S * n]).view(S, n).int().cuda()
+    bad = [[0, 17, 18, 61, 62, 63, 64, 100], [3, 4, 5, 6, 7, 8, 9, 90, 126]]
+    for s in range(S):
+        for at, b in enumerate(bad[s]):
+            c.tables[s, b] = (-1, c.N, 2 ** 31 - 1)[at % 3]
+    used = set(c.tables.flatten().tolist())
+    for page in set(range(c.N)) - used:
+        c.k[page], c.v[page] = (torch.full((), float("nan")).to(dtype) for _ in range(2))
+    with _handle(Hq, Hk, D, B, c.N) as p:
+        c.run(p)
+        with pytest.raises(rk.PredError) as e:
+            rk.pred_device_error(p.handle)
+        assert "block-table" in str(e.value)
+    q, out, lse, blk = _f64(c.q), _f64(c.out), _f64(c.lse), _f64(c.block_lse)
+    g = Hq // Hk
+    for s in range(S):
+        length, drafted = int(c.lens[s]), int(c.drafts[s])
+        used_blocks = -(-length // B)
+        pages = c.tables[s, :used_blocks].cpu().numpy().copy()
+        pages[bad[s]] = [i for i in range(1, c.N) if i in used][0]      # any block: its tokens are not seen
+        k = _f64(c.k[torch.from_numpy(pages).long().cuda()]) * c.scales[0]
+        v = _f64(c.v[torch.from_numpy(pages).long().cuda()]) * c.scales[1]
+        seen = cache.seen_by(M, length, drafted, c.tree[s].tolist())
+        for b in bad[s]:
+            seen[:, b * B:b * B + B] = False
+        seen = np.repeat(seen, g, axis=0)
+        for h in range(Hk):
+            kk, vv = k[:, :, h].reshape(-1, D)[:length], v[:, :, h].reshape(-1, D)[:length]
+            qq = q[s, :, h * g:h * g + g].reshape(-1, D)
+            want, want_lse, x, absolute = cache.attend_one(qq, kk, vv, seen, c.scale)
+            delta = (D + 4) * 2.0 ** -24 * c.scale * (np.abs(qq) @ np.abs(kk).T).max()
+            rel = 2 * delta + 2.0 ** -20 + 2.0 ** -16 + (length + 64) * 2.0 ** -24
+            got = out[s, :, h * g:h * g + g].reshape(-1, D)
+            assert np.all(np.abs(got - want) <= HALF_BF16 * np.abs(want) + rel * absolute), ("out", s, h)
+            Case._close_log(lse[s, :, h * g:h * g + g].reshape(-1), want_lse, rel, ("lse", s, h))
+            got = blk[s, :used_blocks, :, h * g:h * g + g].reshape(used_blocks, M * g)
+            Case._close_log(got, cache.block_lse_one(x, B), rel, ("block_lse", s, h))
+
+
 def test_attend_long_sequence_far_slots():
     """A cache whose slots lie beyond 2^32 bytes: 40000 blocks of 128 KiB, a sequence scattered over them."""
     Hq, Hk, D, B, N, n = 16, 8, 128, 32, 40000, 300
