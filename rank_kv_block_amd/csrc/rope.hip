@@ -16,16 +16,19 @@
 // whole heads side by side, and a lane's cosines and sines serve the same
 // pieces of up to kHeads heads, whose loads are all in flight at once.
 //
-// Measured: 8190 tokens of 64 heads of 128 (268 MB) 52 us, 5.2 TB/s, where a
-// copy of 2 GiB reaches 4.9; 2048 tokens of 32 + 8 + 8 heads into an e4m3 cache
-// (46 MB) 14 us; one token of 4 + 1 + 1 heads of 64 3.4 us.
+// Measured: 8190 tokens of 64 heads of 128 (268 MB) 48 us, 5.6 TB/s, where a
+// copy of 2 GiB reaches 4.9 (52 us without the nontemporal loads and stores);
+// 2048 tokens of 32 + 8 + 8 heads into an e4m3 cache (46 MB) 12.3 us; one token
+// of 4 + 1 + 1 heads of 64 3.4 us.
 #include "common.h"
 #include "kernels.h"
 
 namespace pred {
 namespace {
 
-constexpr int kHeads = 4;   // heads a lane turns with one set of cosines and sines
+// heads a lane turns with one set of cosines and sines (the e4m3 chunk: 13.8 us with 2, 12.6 with 3, 13.8 with 4, 13.2
+// with 6)
+constexpr int kHeads = 3;
 
 struct CosSin {
     float c, s;
@@ -80,7 +83,7 @@ __device__ inline void store8(const float* x, void* row, int d0, bool fp8, float
         u32x4_t w;
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = pack2(x[2 * i], x[2 * i + 1]);
-        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(row) + d0) = w;
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(row) + d0));
     }
 }
 
@@ -151,8 +154,8 @@ __global__ __launch_bounds__(256) void rotate_kernel(RopeArgs a, int pieces, int
         const int h = h0 + i * heads_at_once;
         if (h < heads) {
             const Rows r = rows_of(a, t, cache_off, h);
-            lo[i] = *reinterpret_cast<const u32x4_t*>(r.in + d0);
-            if (!INTER) hi[i] = *reinterpret_cast<const u32x4_t*>(r.in + d1);
+            lo[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(r.in + d0));
+            if (!INTER) hi[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(r.in + d1));
         }
     }
     constexpr int kPairs = INTER ? 4 : 8;
