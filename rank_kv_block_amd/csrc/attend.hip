@@ -879,6 +879,9 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
                     mine_ref = y == c ? ref[y] : mine_ref;
                 }
                 if constexpr (parts == 1) {
+                    // a tile in which the row sees nothing is taken against the running maximum: it counts for nothing, and
+                    // must not raise the block's reference, from which the sum so far may lie too far to be held
+                    if (mine_sum == 0.f) mine_ref = kLowest;
                     const float both = fmaxf(wide_m, mine_ref);
                     wide_l = wide_l * exp2_of(wide_m - both) + mine_sum * exp2_of(mine_ref - both);
                     wide_m = both;
@@ -1395,6 +1398,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
                                 mine_sum = f ? other : mine_sum;
                                 mine_ref = f ? ref[h][2 * y + 1] : mine_ref;
                             } else {
+                                if (mine_sum == 0.f) mine_ref = kLowest;        // as in the stream kernel
                                 const float both = fmaxf(wide_m, mine_ref);
                                 wide_l = wide_l * exp2_of(wide_m - both) + mine_sum * exp2_of(mine_ref - both);
                                 wide_m = both;
