@@ -457,7 +457,9 @@ int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int6
  * A row past draft_len and a row that sees no token have output 0 and lse -inf.
  * Query head h reads kv head h / (num_q_heads / num_kv_heads).  Sums and the
  * softmax are held in float32.  What a masked token holds (NaN, infinities)
- * does not reach a row that cannot see it.  Lengths outside their range are
+ * does not reach a row that cannot see it.  An infinite value that a row sees
+ * makes that element of its output the infinity, however small its weight; NaN,
+ * and infinities of both signs, make it NaN.  Lengths outside their range are
  * clamped, and a block whose table entry is outside [0, max_blocks) is left out
  * of every sum; both raise the device error word.  head_dim <= 256
  * (PRED_ERR_UNSUPPORTED above); n_blocks * block_size <= 2^29 (here and in the

@@ -37,6 +37,23 @@ __device__ inline uint16_t to_bf16(float x) { return __builtin_bit_cast(uint16_t
 
 __device__ inline float fp8_value(uint32_t byte) { return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0); }
 
+// Values that are not finite.  A softmax weight is positive, so an infinite
+// value that a row sees makes that element of its output the infinity, and two
+// of opposite signs or a NaN make it NaN.  Sums of products give that only while
+// the weight is held: one that underflows, or a matrix product's second term
+// (which may be 0 or negative), turns the infinity into NaN.  So where a sum
+// ends up not finite it becomes the sum of the values that are not, without
+// weights; and sums are joined by joined().
+
+// 0 for a number, else itself
+__device__ inline float not_finite(float x) { return fabsf(x) < INFINITY ? 0.f : x; }
+
+// a fa + b fb for factors in [0, 1]: an infinity stays one whatever its factor
+__device__ inline float joined(float a, float fa, float b, float fb) {
+    const float x = a * fa + b * fb;
+    return x != x ? a + b : x;
+}
+
 // ---------------------------------------------------------------- plain kernel
 //
 // Any head size up to 256, any block size and strides: a workgroup per (row,
@@ -117,6 +134,26 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
             a.block_lse[(((int64_t)s * a.n + b) * a.M + i) * a.Hq + h] =
                 bl <= 0.f ? -INFINITY : (bm + log2_of(bl)) * kLn2;
     }
+    if constexpr (!FP8) {
+        const float lost = acc[0] * 0.f + acc[1] * 0.f + acc[2] * 0.f + acc[3] * 0.f;      // NaN where a sum is not finite
+        if (__ballot(lost != 0.f) && l == l) {
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int b = wave; b < used; b += 4) {
+                const int64_t slot = a.tables ? a.tables[(int64_t)s * a.n + b] : b;
+                if (slot < 0 || slot >= a.N) continue;
+                for (int t0 = 0; t0 < a.B && b * a.B + t0 < len; ++t0) {
+                    const int t = b * a.B + t0;
+                    if (t >= ctx && !((seen >> (t - ctx)) & 1)) continue;
+                    const int64_t at = slot * a.cache.block_stride + t0 * a.cache.token_stride + head_off;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (lane + 64 * e < a.D) sum[e] += not_finite(cache_value<FP8>(a.cache.v, at + lane + 64 * e));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = sum[e] == 0.f ? acc[e] : sum[e];
+        }
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[wave][lane + 64 * e] = acc[e];
     if (lane == 0) {
@@ -132,6 +169,8 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
         total += f * part_l[w];
         value += f * part[w][threadIdx.x];
     }
+    if (value != value)
+        value = part[0][threadIdx.x] + part[1][threadIdx.x] + part[2][threadIdx.x] + part[3][threadIdx.x];
     const bool none = total == 0.f;
     if ((int)threadIdx.x < a.D) a.out[q_at + threadIdx.x] = to_bf16(none ? 0.f : value * a.cache.v_scale / total);
     if (a.lse && threadIdx.x == 0)
@@ -313,6 +352,16 @@ __device__ inline JoinRow join_row(const AttendArgs& a, const Plan& pl, uint32_t
     j.slot = (int64_t)share.first * a.Hk + (int64_t)(j.h / g) * share.groups + r / pl.rows;
     return j;
 }
+// 4 values of a row's sums where one of them is NaN: the runs' without their factors
+__device__ inline float4 join_not_finite(const AttendArgs& a, const Plan& pl, const JoinRow& j, int D, int d4, float4 v) {
+    if (!(v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w)) return v;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < j.runs; ++x) {
+        const float4 o = reinterpret_cast<const float4*>(part_sums(a, pl, j.slot + x * j.step) + j.in_group * D)[d4];
+        sum = make_float4(sum.x + o.x, sum.y + o.y, sum.z + o.z, sum.w + o.w);
+    }
+    return make_float4(v.x != v.x ? sum.x : v.x, v.y != v.y ? sum.y : v.y, v.z != v.z ? sum.z : v.z, v.w != v.w ? sum.w : v.w);
+}
 // 4 values of a row from its sums (v, l, m), the lse by the first lane
 __device__ inline void join_store(const AttendArgs& a, int D, uint32_t row, int d4, float4 v, float l, float m) {
     const bool none = l == 0.f;
@@ -360,7 +409,7 @@ __global__ __launch_bounds__(256) void attend_join_rows_kernel(AttendArgs a, Pla
             v = make_float4(v.x + f * o[e].x, v.y + f * o[e].y, v.z + f * o[e].z, v.w + f * o[e].w);
         }
     }
-    if (j.wanted) join_store(a, D, row, d4, v, l, m);
+    if (j.wanted) join_store(a, D, row, d4, join_not_finite(a, pl, j, D, d4, v), l, m);
 }
 
 // Rows of many runs: a workgroup each, wave w taking runs w, w + 4, ..: a lane
@@ -438,7 +487,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
         v.z += fw * o.z;
         v.w += fw * o.w;
     }
-    if (part == 0) join_store(a, D, row, d4, v, l, m);
+    if (part == 0) join_store(a, D, row, d4, join_not_finite(a, pl, j, D, d4, v), l, m);
 }
 
 // ---------------------------------------------------------------- stream kernel
@@ -567,14 +616,26 @@ __device__ inline uint32_t finite_only_fp8(uint32_t w) {
 
 // A masked weight is 0, and 0 times a value that is not finite would be NaN in
 // the matrix cores.  So drafted tokens' values enter the products with 0 in the
-// place of what is not finite, and a sequence that holds any adds it afterwards
-// to the rows that see its token: the sum of weight times value is then that
-// infinity or NaN whatever the (positive) weight. 
+// place of what is not finite.  A run that holds any, or whose sums are not
+// finite (every row sees the whole context), walks its tokens once more and
+// takes what is not finite from there.  (e4m3 has no infinities, and a NaN of
+// the context needs no walk.)
+
+// Adds what is not finite among the 4 values from d on of a token's head.
 template <bool FP8>
-__device__ inline float not_finite_part(const char* row, int d) {
-    if constexpr (FP8) return (static_cast<uint8_t>(row[d]) & 0x7F) == 0x7F ? NAN : 0.f;
-    const uint32_t w = reinterpret_cast<const uint16_t*>(row)[d];
-    return (w & 0x7F80u) == 0x7F80u ? bf16_lo(w) : 0.f;
+__device__ inline void add_not_finite(float* sum, const char* row, int d) {
+    if constexpr (FP8) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(row + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (((w >> (8 * e)) & 0x7Fu) == 0x7Fu) sum[e] = NAN;
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(row + 2 * d);
+        sum[0] += not_finite(bf16_lo(w.x));
+        sum[1] += not_finite(bf16_hi(w.x));
+        sum[2] += not_finite(bf16_lo(w.y));
+        sum[3] += not_finite(bf16_hi(w.y));
+    }
 }
 // The values of a token's head, null where its block has an invalid entry.
 __device__ inline const char* value_row(const AttendArgs& a, const BlockSize& bs, int s, int kvh, int tok, int64_t item) {
@@ -948,19 +1009,38 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
         t = next;
     }
 
-    if (__ballot(odd)) {
-        for (int tok = ctx > t0 ? ctx : t0; tok < t1; ++tok) {
+    l = sum_over_c(l);
+    bool lost = false;
+    if constexpr (!FP8) {
+        float x = 0.f;      // NaN where a sum is not finite
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) x = __builtin_fmaf(o[j][v], 0.f, x);
+        lost = x != 0.f && l == l;
+    }
+    const bool all = __ballot(lost) != 0;
+    if (all || __ballot(odd)) {
+        float sum[4][J];
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int j = 0; j < J; ++j) sum[v][j] = 0.f;
+        for (int tok = all || ctx < t0 ? t0 : ctx; tok < t1; ++tok) {
             if ((tok - t0) / 32 / per % 4 != wave) continue;        // another wave's
             const char* const from = value_row(a, bs, s, kvh, tok, item);
-            if (from && ((seen >> ((tok - ctx) & 63)) & 1)) {
+            if (from && (tok < ctx || ((seen >> ((tok - ctx) & 63)) & 1))) {
 #pragma unroll
-                for (int j = 0; j < J; ++j)
+                for (int v = 0; v < 4; ++v)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) o[j][v] += not_finite_part<FP8>(from, J * (4 * c + v) + j);
+                    for (int j = 0; j < J; j += 4) add_not_finite<FP8>(sum[v] + j, from, J * (4 * c + v) + j);
             }
         }
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int j = 0; j < J; ++j) o[j][v] = sum[v][j] == 0.f ? o[j][v] : sum[v][j];
     }
-    l = sum_over_c(l);
 
     // the waves' sums: 2 and 3 into 0 and 1, then 1 into 0
 #pragma unroll
@@ -984,7 +1064,7 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) o[j][v] = o[j][v] * f + from[(4 * j + v) * 64 + lane] * f_other;
+                for (int v = 0; v < 4; ++v) o[j][v] = joined(o[j][v], f, from[(4 * j + v) * 64 + lane], f_other);
         }
         __syncthreads();
     }
@@ -1433,20 +1513,36 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
     if (pairs) walk(std::integral_constant<int, 1>(), wave % 2);
     else walk(std::integral_constant<int, 2>(), 0);
 
-    if (any_odd) {
-        for (int tok = ctx > t0 ? ctx : t0; tok < t1; ++tok) {
-            if (pairs && (tok - t0) / 32 % 2 != wave % 2) continue;         // the other wave's half
-            const char* const from = value_row(a, bs, s, kvh, tok, item);
-            if (from && ((seen >> ((tok - ctx) & 63)) & 1)) {
+    l = sum_over_f(l);
+    bool lost = false;
+    if constexpr (!FP8) {
+        float x = 0.f;      // NaN where a sum is not finite
 #pragma unroll
-                for (int d = 0; d < DT; ++d)
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        o[d][v] += not_finite_part<FP8>(from, 32 * d + v % 4 + 8 * (v / 4) + 4 * f);
+            for (int v = 0; v < 16; ++v) x = __builtin_fmaf(o[d][v], 0.f, x);
+        lost = x != 0.f && l == l;
+    }
+    const bool all = __ballot(lost) != 0;
+    if (all || any_odd) {
+        // 32 of a token's values at a time: the sums of them all would be too many registers beside o
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            float sum[16];
+#pragma unroll
+            for (int v = 0; v < 16; ++v) sum[v] = 0.f;
+            for (int tok = all || ctx < t0 ? t0 : ctx; tok < t1; ++tok) {
+                if (pairs && (tok - t0) / 32 % 2 != wave % 2) continue;         // the other wave's half
+                const char* const from = value_row(a, bs, s, kvh, tok, item);
+                if (from && (tok < ctx || ((seen >> ((tok - ctx) & 63)) & 1))) {
+#pragma unroll
+                    for (int v = 0; v < 16; v += 4) add_not_finite<FP8>(sum + v, from, 32 * d + 2 * v + 4 * f);
+                }
             }
+#pragma unroll
+            for (int v = 0; v < 16; ++v) o[d][v] = sum[v] == 0.f ? o[d][v] : sum[v];
         }
     }
-    l = sum_over_f(l);
     if (pairs) {
         // the pair's sums, through the (now unused) stage
         float* const x = reinterpret_cast<float*>(lds) + (wave / 2) * (16 * DT + 2) * 64;
@@ -1467,7 +1563,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) o[d][v] = o[d][v] * mine + x[(2 + 16 * d + v) * 64 + lane] * other;
+            for (int v = 0; v < 16; ++v) o[d][v] = joined(o[d][v], mine, x[(2 + 16 * d + v) * 64 + lane], other);
     }
     if (r >= R) return;
     const bool none = !live || l == 0.f;

@@ -74,3 +74,68 @@ def test_attend_wide_block_far_below_and_hidden(Hq, Hk, D, B, M, dtype, name, se
         for s in range(5):
             if lens[s] - M > most - B:
                 assert torch.isfinite(c.block_lse[s, n - 1]).all()
+
+
+INFINITE = [
+    # Hq, Hk, D, B, n, M, dtype, kernel: short contexts of one run, and long ones of many
+    (4, 2, 64, 16, 8, 1, torch.bfloat16, "attend_stream_kernel"),
+    (32, 8, 128, 16, 8, 1, torch.bfloat16, "attend_stream_kernel"),
+    (8, 2, 128, 32, 70, 1, torch.bfloat16, "attend_stream_kernel"),
+    (8, 2, 64, 64, 40, 6, torch.bfloat16, "attend_stream_kernel"),
+    (4, 4, 128, 16, 9, 20, torch.bfloat16, "attend_stream_kernel"),
+    (8, 2, 128, 16, 8, 13, torch.bfloat16, "attend_tree_kernel"),        # a wave pair for the rows
+    (8, 2, 64, 32, 6, 40, torch.bfloat16, "attend_tree_kernel"),
+    (16, 2, 128, 16, 130, 20, torch.bfloat16, "attend_tree_kernel"),
+    (8, 1, 64, 7, 300, 64, torch.bfloat16, "attend_tree_kernel"),
+    (16, 4, 128, 1024, 2, 10, torch.bfloat16, "attend_tree_kernel"),
+    (4, 2, 80, 16, 20, 3, torch.bfloat16, "attend_plain_kernel"),
+    (4, 1, 256, 24, 50, 1, torch.bfloat16, "attend_plain_kernel"),
+    (8, 2, 128, 16, 130, 4, FP8, "attend_stream_kernel"),
+    (16, 2, 64, 16, 130, 20, FP8, "attend_tree_kernel"),
+    (4, 2, 80, 16, 20, 3, FP8, "attend_plain_kernel"),
+]
+
+
+@pytest.mark.parametrize("Hq,Hk,D,B,n,M,dtype,name", INFINITE)
+def test_attend_values_that_are_not_finite(Hq, Hk, D, B, n, M, dtype, name):
+    """Infinities and NaN in values that rows see, in the context and in the draft, at tokens of ordinary weight and at
+    tokens whose weight is below float32's range: an infinity is that element's result, two of opposite signs and NaN
+    are NaN, and every other element, sum and row keeps its bits.  (Weights are positive: e^-150 of them here.)"""
+    inf, nan = float("inf"), float("nan")
+    _say("not finite", Hq, Hk, D, B, n, M, dtype, name)
+    length = n * B - 3
+    c = Case(2, M, Hq, Hk, D, B, n, dtype, tree="tree", lens=[length, length], drafts=[M, max(1, M // 2)])
+    ctx = length - M
+    _aimed(c)
+    far = min(ctx // 3, 640)        # whole tiles, and in the long contexts whole runs, far below the others
+    for t in range(far):
+        _aim(c, 0, t, -150.0)
+    with _handle(Hq, Hk, D, B, c.N) as p:
+        weights = name != "attend_tree_kernel" or B != 7
+        assert rk.pred_attend_kernel_name(p.handle, c.kv, M, weights) == name
+        c.run(p, weights)
+        clean = [t.clone() for t in (c.out, c.lse, c.block_lse)]
+        assert all(torch.isfinite(t).all() for t in (clean[0], clean[1][0]))
+        one = inf if dtype == torch.bfloat16 else nan
+        places = [(ctx - 1, 3, one), (far + 1, 5, -one), (ctx // 2, 7, nan), (far, 9, one), (ctx - 2, 9, -one), (0, 11, one),
+                  (far - 1, 13, -one), (far // 2, 15, one), (1, 15, -one)]
+        want = {3: one, 5: -one, 7: nan, 9: nan, 11: one, 13: -one, 15: nan}
+        for t, d, value in places:
+            c.v[int(c.tables[0, t // B]), t % B, :, d] = torch.tensor(value).to(dtype)
+        sees = [False] * M
+        if M > 1:       # a drafted token that only its own subtree sees
+            t = ctx + M // 2
+            c.v[int(c.tables[0, t // B]), t % B, :, 17] = torch.tensor(one).to(dtype)
+            sees = [bool(w >> (M // 2) & 1) for w in c.tree[0].tolist()]
+        c.run(p, weights)
+        rk.pred_device_error(p.handle)
+        expected = clean[0].clone()
+        for d, value in want.items():
+            expected[0, :, :, d] = value
+        for i in range(M):
+            if sees[i]:
+                expected[0, i, :, 17] = one
+        for d in range(D):
+            same = (c.out[..., d] == expected[..., d]) | (c.out[..., d].isnan() & expected[..., d].isnan())
+            assert same.all(), (d, c.out[0, :, :, d], expected[0, :, :, d])
+        assert torch.equal(c.lse, clean[1]) and torch.equal(c.block_lse, clean[2])
