@@ -480,7 +480,8 @@ size_t pred_attend_workspace_bytes(pred_t* p, int32_t n_seqs, int32_t n_rows, in
  * bytes), a block's tokens within 2 GiB) or "attend_tree_kernel" (the others).
  * "attend_plain_kernel" for other head sizes, cache rows off 16-byte alignment,
  * and block_lse with a block size other than 8, 16 or a multiple of 32 up to
- * 65536.  NULL for a NULL argument or n_rows outside [1, 64]. */
+ * 65536.  NULL for a NULL argument, and for n_rows, a cache or a head size that
+ * pred_attend refuses. */
 const char* pred_attend_kernel_name(pred_t* p, const pred_kv_cache* cache, int32_t n_rows, int32_t with_block_lse);
 
 /* Accumulated attention weight of each block, from pred_attend's lse and

@@ -98,6 +98,9 @@ pred::RopeArgs rope_args(pred_t* p, const pred_rope* r, const int32_t* positions
 // Tokens of a sequence: with 2^29 no sum of lengths, runs and tiles passes 32 bits.
 constexpr int64_t kMostTokens = 1ll << 29;
 
+// Head sizes that pred_attend has a kernel for.
+constexpr int kMostHead = 256;
+
 // The table's extent and the counts shared by the calls over sequences.
 int check_counts(pred_t* p, int64_t n_blocks, int32_t n_seqs, const char* what) {
     if (n_blocks < 0 || n_seqs < 0)
@@ -274,6 +277,10 @@ const char* pred_attend_kernel_name(pred_t* p, const pred_kv_cache* cache, int32
     pred::CacheView view;
     if (check_cache(p, cache, &view, "attend_kernel_name") || check_n_rows(n_rows, "attend_kernel_name"))
         return nullptr;
+    if (p->d.head_dim > kMostHead) {
+        fail(PRED_ERR_UNSUPPORTED, "attend_kernel_name: head_dim (%d) above %d", p->d.head_dim, kMostHead);
+        return nullptr;
+    }
     pred::AttendArgs a = attend_shape(p, 1, n_rows, 1);
     a.cache = view;
     float any;
@@ -292,7 +299,8 @@ int pred_attend(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32
     if ((rc = check_cache(p, cache, &view, "attend")) || (rc = check_counts(p, n_blocks, n_seqs, "attend")) ||
         (rc = check_n_rows(n_rows, "attend")))
         return rc;
-    if (p->d.head_dim > 256) return fail(PRED_ERR_UNSUPPORTED, "attend: head_dim (%d) above 256", p->d.head_dim);
+    if (p->d.head_dim > kMostHead)
+        return fail(PRED_ERR_UNSUPPORTED, "attend: head_dim (%d) above %d", p->d.head_dim, kMostHead);
     if (!block_tables && n_blocks > p->d.max_blocks)
         return fail(PRED_ERR_OUT_OF_RANGE, "attend: %lld blocks without a table, max_blocks %lld", (long long)n_blocks,
                     (long long)p->d.max_blocks);

@@ -4,7 +4,7 @@ tests/test_gpu_cache.py's."""
 import pytest
 
 import rank_kv_block_amd as rk
-from tests.test_gpu_cache import FP8, Case, _gpu, _handle, _say  # noqa: F401 (_gpu: a fixture)
+from tests.test_gpu_cache import FP8, Case, _cache_tensors, _gpu, _handle, _say  # noqa: F401 (_gpu: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +139,21 @@ def test_attend_values_that_are_not_finite(Hq, Hk, D, B, n, M, dtype, name):
             same = (c.out[..., d] == expected[..., d]) | (c.out[..., d].isnan() & expected[..., d].isnan())
             assert same.all(), (d, c.out[0, :, :, d], expected[0, :, :, d])
         assert torch.equal(c.lse, clean[1]) and torch.equal(c.block_lse, clean[2])
+
+
+def test_kernel_names_only_for_what_attend_takes():
+    """A head size, a number of rows or a cache that pred_attend refuses has no kernel."""
+    for D, M, good in ((256, 64, True), (264, 1, False), (512, 1, False), (128, 0, False), (128, 65, False)):
+        with _handle(2, 1, D, 16, 2) as p:
+            kv = rk.KVCache(*_cache_tensors(2, 16, 1, D, torch.bfloat16, "tokens", fill=0.0))
+            if good:
+                assert rk.pred_attend_kernel_name(p.handle, kv, M) == "attend_plain_kernel"
+                continue
+            with pytest.raises(rk.PredError):
+                rk.pred_attend_kernel_name(p.handle, kv, M)
+            q = torch.zeros((1, M, 2, D), dtype=torch.bfloat16, device="cuda")
+            with pytest.raises(rk.PredError):
+                rk.pred_attend(p.handle, kv, q, None, None, None, None, 1.0, torch.zeros_like(q))
+            kv = rk.KVCache(kv.k, kv.v, 2.0, 1.0)       # a bf16 cache has scales of 1
+            with pytest.raises(rk.PredError):
+                rk.pred_attend_kernel_name(p.handle, kv, 1)
