@@ -4,7 +4,7 @@ tests/test_gpu_cache.py's."""
 import pytest
 
 import rank_kv_block_amd as rk
-from tests.test_gpu_cache import FP8, Case, _cache_tensors, _gpu, _handle, _say  # noqa: F401 (_gpu: a fixture)
+from tests.test_gpu_cache import FP8, Case, Serving, _cache_tensors, _gpu, _handle, _say  # noqa: F401 (_gpu: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -157,3 +157,36 @@ def test_kernel_names_only_for_what_attend_takes():
             kv = rk.KVCache(kv.k, kv.v, 2.0, 1.0)       # a bf16 cache has scales of 1
             with pytest.raises(rk.PredError):
                 rk.pred_attend_kernel_name(p.handle, kv, 1)
+
+
+def test_two_graphs_keep_their_workspaces():
+    """The serving step captured twice, each graph with a workspace of its own that lives as long as it does: the graphs
+    take turns, other tensors come and go between the replays, and every replay is the eager step's result."""
+    a, b = Serving(torch.bfloat16), Serving(torch.bfloat16)
+    for w in (a, b):
+        w.feed(0)
+        w.device_step()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        b.ws = torch.empty_like(b.ws)
+        state = [t.clone() for t in (b.tables, b.mass, b.lens)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            b.device_step()
+        graphs.append((graph, b.ws))
+        for t, old in zip((b.tables, b.mass, b.lens), state):
+            t.copy_(old)
+    assert graphs[0][1].data_ptr() != graphs[1][1].data_ptr()
+    for step in range(1, 30):
+        a.feed(step)
+        a.device_step()
+        b.feed(step)
+        others = [torch.full_like(b.ws, 255) for _ in range(4)]
+        graphs[step % 2][0].replay()
+        torch.cuda.synchronize()
+        assert all((t == 255).all() for t in others), step
+        for x, y in zip(a.state(), b.state()):
+            assert torch.equal(x, y), step
+    a.p.close()
+    b.p.close()
