@@ -554,7 +554,9 @@ __device__ inline float sum_over_c(float x) {
 }
 
 // Turns a product q k into units of log2: above 0, so that a masked -inf stays
-// one (the queries carry a negative scale's sign).
+// one (the queries carry a negative scale's sign).  A scale of 0, which weighs
+// every token alike, is 2^-120 here: products below 2^96 differ by less than
+// 2^-24 then.
 __device__ inline float log2_scale(const AttendArgs& a) {
     return fmaxf(fabsf(a.scale) * a.cache.k_scale * kLog2e, 0x1p-120f);
 }

@@ -330,8 +330,7 @@ int pred_attend(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32
     a.lse = lse;
     a.block_lse = block_lse;
     a.ws = workspace;
-    // a scale of 0 weighs every token alike; the kernels divide by it, and products of 2^-100 are as equal
-    a.scale = scale == 0.f ? 0x1p-100f : scale;
+    a.scale = scale;
     const hipError_t e = pred::launch_attend(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "attend launch");
     return ok();
