@@ -428,7 +428,8 @@ int pred_rotate(pred_t* p, const pred_rope* rope, const pred_bf16* x, int64_t x_
  *              word.  Two tokens with one slot race.
  *   q_out      device, [n_tokens, num_q_heads, head_dim] bf16; may be q itself if q_stride is num_q_heads * head_dim
  * A bf16 cache takes keys and values rounded once; an FP8 cache takes value /
- * scale clamped to +-448 and rounded once (nearest, ties to even), NaN kept.
+ * scale, a float32 quotient, clamped to +-448 and rounded to the nearest (ties to
+ * even), NaN kept.
  * rope->backward must be 0, and the cache's k and v must not overlap (one
  * address for both is PRED_ERR_OUT_OF_RANGE). */
 int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int64_t q_stride, const pred_bf16* k,
@@ -455,8 +456,9 @@ int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int6
  *                 as they were
  *   workspace     device scratch of pred_attend_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0)
  * A row past draft_len and a row that sees no token have output 0 and lse -inf.
- * Query head h reads kv head h / (num_q_heads / num_kv_heads).  Sums and the
- * softmax are held in float32.  What a masked token holds (NaN, infinities)
+ * Query head h reads kv head h / (num_q_heads / num_kv_heads).  Scores, sums and
+ * the softmax are held in float32; in the stream and tree kernels a weight
+ * enters its product with a value as two bf16 terms, 16 of its bits.  What a masked token holds (NaN, infinities)
  * does not reach a row that cannot see it.  An infinite value that a row sees
  * makes that element of its output the infinity, however small its weight; NaN,
  * and infinities of both signs, make it NaN.  Lengths outside their range are
@@ -471,7 +473,10 @@ int pred_attend(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32
 
 /* Workspace of pred_attend for this shape on this handle (partial results of a
  * long context split over workgroups); 0 for a NULL handle or counts < 1.  Calls
- * that may run at the same time need workspaces of their own. */
+ * that may run at the same time need workspaces of their own.  It grows with the
+ * queries per kv head and hardly with the context: on 256 CUs 1 MiB for one
+ * sequence of 131072 tokens, 9 MiB for 64 sequences of one row (32 query and 8 kv
+ * heads of 128), 292 MiB for 16 sequences of 64 rows (64 and 8 heads). */
 size_t pred_attend_workspace_bytes(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_blocks);
 
 /* Name of the kernel pred_attend runs for this handle, cache and shape (host

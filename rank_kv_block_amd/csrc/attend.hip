@@ -61,7 +61,9 @@ __device__ inline float joined(float a, float fa, float b, float fb) {
 // 64 tokens of a block at a time, a lane each, then adds their values with a
 // lane per value.  Every query head reads its kv head's cache for itself, so
 // this kernel is for the shapes the others do not take (16 sequences of 8192
-// tokens, 32 queries of 64 over 8 e4m3 heads: 2021 us, the tree kernel 39).
+// tokens, 32 queries of 64 over 8 e4m3 heads: 2021 us, the tree kernel 39; one
+// sequence of 16384 tokens, 32 queries over 8 bf16 heads: 4.9 ms at a head size
+// of 80 and 13.1 ms at 256, the stream kernel 18 us at 128).
 template <bool FP8>
 __device__ inline float cache_value(const void* p, int64_t at) {
     if constexpr (FP8) return fp8_value(static_cast<const uint8_t*>(p)[at]);
@@ -493,7 +495,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
 // ---------------------------------------------------------------- stream kernel
 //
 // Up to 32 queries per kv head (a token, or a small draft): HBM bound, every
-// key and value read once.  Each of a workgroup's four waves works alone on
+// key and value read once for each 16 queries.  Each of a workgroup's four waves works alone on
 // every fourth tile of 32 tokens, from loads to sums, with no LDS and no
 // barrier, and the waves' sums meet at the end.
 //
@@ -521,10 +523,12 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
 // between lanes.
 //
 // Measured, 8 kv heads of 128 with 4 queries each: 131072 bf16 tokens of one
-// sequence with block sums (537 MB) 92 to 96 us, 5.7 TB/s; 64 e4m3 sequences of
-// up to 32768 tokens (2.7 GB) 439 us, 6.1 TB/s, where nothing but streaming reads
-// reaches 7.1.  About 18 us of a call are its start (lengths, table, first tiles)
-// and end: 1024 tokens of one head of 64 take 7.7 us.
+// sequence with block sums (537 MB) 96 us, 5.6 TB/s; 64 e4m3 sequences of up to
+// 32768 tokens (2.7 GB) 440 us, 6.1 TB/s, 256 of up to 8192 449 us, where nothing
+// but streaming reads reaches 7.1.  About 18 us of a call are its start (lengths,
+// table, first tiles) and end: 1024 tokens of one head of 64 take 8.0 us.  17 to
+// 32 queries are two groups: 131072 tokens with 32 queries a head take 142 us and
+// move 771 MB, with 16 queries 95 us and 538 MB.
 template <int D_, bool FP8_>
 struct StreamLayout {
     static constexpr int D = D_;
@@ -702,7 +706,7 @@ __device__ inline void write_dead_rows(const AttendArgs& a, const Item& it, cons
 }
 
 // BYTES from a uniform address and a lane's offset, nontemporal (each byte is
-// read once).
+// read once by a group of 16 queries).
 template <int BYTES>
 __device__ inline void stream_load(uint32_t* dst, const char* base, uint32_t off) {
     if constexpr (BYTES == 16) {
@@ -1122,12 +1126,15 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 // the row so that the 16 rows of a key read, and the 4 rows of a transpose read,
 // fall on different banks.
 //
-// Bound: at 512 queries per kv head the matrix cores and what feeds them (the
-// cache's bytes would take a quarter of the time); the weights' second bf16 term
-// makes the value product twice as long.  Measured, 16 sequences of 16384 tokens,
-// 64 rows of 8 queries for each of 8 heads of 128: 909 us, 600 TFLOP/s (a matrix
-// product of the library's reaches 1233); with block sums and lengths and drafts
-// that vary 489 us.  13 rows over 8 sequences of 5k tokens: 58 us.
+// Bound: a tile's products, exponentials and LDS reads follow one another in each
+// wave, with two waves a SIMD (the registers' limit), so the matrix cores idle for
+// more than half of the time (the cache's bytes would take a quarter of it); the
+// weights' second bf16 term makes the value product twice as long.  Measured, 16 sequences of 16384 tokens, 64 rows of 8 queries for each of
+// 8 heads of 128: 891 us, 617 TFLOP/s (a matrix product of the library's reaches
+// 1233), the matrix cores busy in 46% of the SIMDs' cycles; with block sums and
+// lengths and drafts that vary 484 us (458 from an e4m3 cache), 24%.  13 rows over
+// 8 sequences of 5k tokens: 58 us (50), 16%: an item's start and a chain of 10 to
+// 12 tiles.
 template <int D>
 struct TreeLds {
     static constexpr int kRow = 2 * D;              // bytes of a row
@@ -1600,7 +1607,9 @@ enum class Kind { Stream, Tree, Plain };
 int queries_of(const AttendArgs& a) { return a.M * (a.Hq / a.Hk); }
 
 constexpr int kRounds = 8;              // most workgroups a CU's places get one after another
-constexpr int kStreamQueries = 32;      // queries per kv head of the stream kernel
+// Queries per kv head of the stream kernel.  Two groups of 16 read most bytes twice: over 131072 tokens of one sequence
+// 32 queries take 142 us with it, and 40 take 111 with the tree kernel; where they cross below 32 has not been measured.
+constexpr int kStreamQueries = 32;
 
 Kind kind_of(const AttendArgs& a) {
     const int item = a.cache.fp8 ? 1 : 2;
@@ -1629,7 +1638,8 @@ Plan plan_of(const AttendArgs& a, bool tree) {
     // whole tiles (four waves take one each in the stream kernel), or whole blocks where a block's sum spans tiles
     pl.unit = tree ? 64 : 128;
     if (a.block_lse && a.B > 32) pl.unit = tree ? (a.B % 64 == 0 ? a.B : 2 * a.B) : 4 * a.B;
-    // Two workgroups fit a CU.  Items of a batch are of uneven length where a run ends early, so more rounds than one
+    // Two workgroups a CU, what the registers of the variants for 128 values a head and bf16 leave room for (the stream
+    // kernel's for 64 values would fit four, its e4m3 one for 128 three, which the plan does not use).  Items of a batch are of uneven length where a run ends early, so more rounds than one
     // even them out (64 sequences, FP8: 503 us with 2, 463 with 4, 449 with 6), but a run has to be worth its start
     // and its partial results (8 sequences of 5k tokens, 13 rows: 75 us with 1, 91 with 2, 109 with 4).
     pl.slots = 2 * a.n_cu;

@@ -16,8 +16,9 @@ namespace {
 //
 // Measured: 8192 blocks of one sequence, one row of 32 heads (1.1 MB) 3.3 us; 64
 // sequences of 2048 blocks, 16 rows of which 1 to 16 count (51 MB, in pieces of
-// 128 bytes between rows that do not count) 17.9 us, 2.8 TB/s.  Four rows' loads
-// in flight a lane took 19.4 us.
+// 128 bytes between rows that do not count; the memory reads 57) 17.9 us, 2.8
+// TB/s: a block's rows follow one another, and each loads lse again.  Four rows'
+// loads in flight a lane took 19.4 us.
 template <int VEC>
 __global__ __launch_bounds__(256) void weight_kernel(WeightArgs a, int lanes, uint32_t groups) {
     const int s = blockIdx.x / groups;
@@ -73,8 +74,9 @@ __global__ __launch_bounds__(256) void weight_kernel(WeightArgs a, int lanes, ui
 // in LDS of the digits of the keys that still match.  Rows up to 1024 E keep
 // their keys in registers (a protected entry's above every key); longer ones (E
 // = 0) are copied to the workspace and read from there.  Bound: latency, of a
-// row of 8 bytes an entry on one CU: 6.4 us for 64 rows of 2048, 32 us for one of
-// 32768.  (Fixing the key bit by bit from counts took 0.5 us a step: 12.8 and 44
+// row of 8 bytes an entry on one CU: 6.5 us for 64 rows of 2048, 11 us for one of
+// 8192, 32 us for one of 32768; through the workspace 122 us for one of 65536 and
+// 258 us for one of 131072.  (Fixing the key bit by bit from counts took 0.5 us a step: 12.8 and 44
 // us.)
 constexpr int kWaves = 16;
 constexpr uint32_t kNoKey = 0xFFFFFFFFu;    // above every order key

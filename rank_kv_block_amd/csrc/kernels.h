@@ -175,7 +175,7 @@ struct AttendArgs {
     int n_cu;
 };
 // Tokens in a sequence's cache and how many of them are drafted rows; values
-// outside their range are clamped (flagged by attend_check_lengths).
+// outside their range are clamped (attend.hip's check_lengths flags them).
 __device__ inline int kv_len_of(const int32_t* kv_len, int s, int64_t most) {
     if (!kv_len) return (int)most;
     const int v = kv_len[s];

@@ -17,9 +17,9 @@
 // pieces of up to kHeads heads, whose loads are all in flight at once.
 //
 // Measured: 8190 tokens of 64 heads of 128 (268 MB) 48 us, 5.6 TB/s, where a
-// copy of 2 GiB reaches 4.9 (52 us without the nontemporal loads and stores);
-// 2048 tokens of 32 + 8 + 8 heads into an e4m3 cache (46 MB) 12.3 us; one token
-// of 4 + 1 + 1 heads of 64 3.4 us.
+// nontemporal copy of as much takes 42 us, 6.4 TB/s (52 us without the nontemporal
+// loads and stores); 2048 tokens of 32 + 8 + 8 heads into an e4m3 cache (46 MB)
+// 12.3 us; one token of 4 + 1 + 1 heads of 64 3.4 us.
 #include "common.h"
 #include "kernels.h"
 
@@ -211,7 +211,8 @@ __device__ inline void store1(float x, void* row, int d, bool fp8, float scale) 
 
 // Rotations whose pairs do not fill 16-byte pieces (rot_dim not a multiple of
 // 16, or 8 where interleaved): a lane per pair, or per value that does not turn,
-// 2 bytes a load.
+// 2 bytes a load.  8190 tokens of 64 heads of 80, 20 of them turning (168 MB): 166
+// us; with all 80 turning, in 16-byte pieces, 46.
 __global__ __launch_bounds__(256) void rotate_pairs_kernel(RopeArgs a) {
     const int half = a.rot / 2, units = half + (a.D - a.rot), heads = a.Hq + 2 * a.Hk;
     const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
