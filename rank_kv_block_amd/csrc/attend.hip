@@ -495,9 +495,9 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
 // ---------------------------------------------------------------- stream kernel
 //
 // Up to 32 queries per kv head (a token, or a small draft): HBM bound, every
-// key and value read once for each 16 queries.  Each of a workgroup's four waves works alone on
-// every fourth tile of 32 tokens, from loads to sums, with no LDS and no
-// barrier, and the waves' sums meet at the end.
+// key and value read once for each 16 queries.  Each of a workgroup's four waves
+// works alone on every fourth tile of 32 tokens, from loads to sums, with no LDS
+// and no barrier, and the waves' sums meet at the end.
 //
 // A wave-load takes 1 KiB, whole rows of TPL tokens (row = a token's head, RB
 // bytes).  Both products run on v_mfma_f32_16x16x32_bf16, queries as the second
@@ -1129,12 +1129,12 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 // Bound: a tile's products, exponentials and LDS reads follow one another in each
 // wave, with two waves a SIMD (the registers' limit), so the matrix cores idle for
 // more than half of the time (the cache's bytes would take a quarter of it); the
-// weights' second bf16 term makes the value product twice as long.  Measured, 16 sequences of 16384 tokens, 64 rows of 8 queries for each of
-// 8 heads of 128: 891 us, 617 TFLOP/s (a matrix product of the library's reaches
-// 1233), the matrix cores busy in 46% of the SIMDs' cycles; with block sums and
-// lengths and drafts that vary 484 us (458 from an e4m3 cache), 24%.  13 rows over
-// 8 sequences of 5k tokens: 58 us (50), 16%: an item's start and a chain of 10 to
-// 12 tiles.
+// weights' second bf16 term makes the value product twice as long.  Measured, 16
+// sequences of 16384 tokens, 64 rows of 8 queries for each of 8 heads of 128: 891
+// us, 617 TFLOP/s (a matrix product of the library's reaches 1233), the matrix
+// cores busy in 46% of the SIMDs' cycles; with block sums and lengths and drafts
+// that vary 484 us (458 from an e4m3 cache), 24%.  13 rows over 8 sequences of 5k
+// tokens: 58 us (50), 16%: an item's start and a chain of 10 to 12 tiles.
 template <int D>
 struct TreeLds {
     static constexpr int kRow = 2 * D;              // bytes of a row
@@ -1638,10 +1638,11 @@ Plan plan_of(const AttendArgs& a, bool tree) {
     // whole tiles (four waves take one each in the stream kernel), or whole blocks where a block's sum spans tiles
     pl.unit = tree ? 64 : 128;
     if (a.block_lse && a.B > 32) pl.unit = tree ? (a.B % 64 == 0 ? a.B : 2 * a.B) : 4 * a.B;
-    // Two workgroups a CU, what the registers of the variants for 128 values a head and bf16 leave room for (the stream
-    // kernel's for 64 values would fit four, its e4m3 one for 128 three, which the plan does not use).  Items of a batch are of uneven length where a run ends early, so more rounds than one
-    // even them out (64 sequences, FP8: 503 us with 2, 463 with 4, 449 with 6), but a run has to be worth its start
-    // and its partial results (8 sequences of 5k tokens, 13 rows: 75 us with 1, 91 with 2, 109 with 4).
+    // Two workgroups a CU, what the registers of the bf16 variants for 128 values a head leave room for (the stream
+    // kernel's for 64 values would fit four, its e4m3 one for 128 three, which the plan does not use).  Items of a batch
+    // are of uneven length where a run ends early, so more rounds than one even them out (64 sequences, FP8: 503 us
+    // with 2, 463 with 4, 449 with 6), but a run has to be worth its start and its partial results (8 sequences of 5k
+    // tokens, 13 rows: 75 us with 1, 91 with 2, 109 with 4).
     pl.slots = 2 * a.n_cu;
     pl.run = tree ? 2048 : 2560;
     const double most = (double)a.S * a.n * a.B * pl.groups * a.Hk / pl.slots / pl.run;
