@@ -457,15 +457,15 @@ int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int6
  *   workspace     device scratch of pred_attend_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0)
  * A row past draft_len and a row that sees no token have output 0 and lse -inf.
  * Query head h reads kv head h / (num_q_heads / num_kv_heads).  Scores, sums and
- * the softmax are held in float32; in the stream and tree kernels a weight
- * enters its product with a value as two bf16 terms, 16 of its bits.  What a masked token holds (NaN, infinities)
- * does not reach a row that cannot see it.  An infinite value that a row sees
- * makes that element of its output the infinity, however small its weight; NaN,
- * and infinities of both signs, make it NaN.  Lengths outside their range are
- * clamped, and a block whose table entry is outside [0, max_blocks) is left out
- * of every sum; both raise the device error word.  head_dim <= 256
- * (PRED_ERR_UNSUPPORTED above); n_blocks * block_size <= 2^29 (here and in the
- * two calls below). */
+ * the softmax are held in float32; in the stream and tree kernels a weight enters
+ * its product with a value as two bf16 terms, 16 of its bits.  What a masked token
+ * holds (NaN, infinities) does not reach a row that cannot see it.  An infinite
+ * value that a row sees makes that element of its output the infinity, however
+ * small its weight; NaN, and infinities of both signs, make it NaN.  Lengths
+ * outside their range are clamped, and a block whose table entry is outside [0,
+ * max_blocks) is left out of every sum; both raise the device error word.
+ * head_dim <= 256 (PRED_ERR_UNSUPPORTED above); n_blocks * block_size <= 2^29
+ * (here and in the two calls below). */
 int pred_attend(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32_t n_rows, const uint64_t* tree,
                 const int32_t* block_tables, int64_t n_blocks, int32_t n_seqs, const int32_t* kv_len,
                 const int32_t* draft_len, float scale, pred_bf16* out, float* lse, float* block_lse, void* workspace,
