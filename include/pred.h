@@ -343,9 +343,11 @@ size_t pred_rank_workspace_bytes(int64_t n_blocks, int64_t n_segments);
  * num_kv_heads, head_dim, block_size and max_blocks from the handle, and the
  * handle's device must be the current one (PRED_ERR_OUT_OF_RANGE otherwise). */
 
-/* Element type of a KV cache: bf16, or 8-bit e4m3 (1 sign, 4 exponent, 3
- * fraction bits, no infinities, largest value 448). */
-enum { PRED_KV_BF16 = 0, PRED_KV_FP8 = 1 };
+/* Element type of a KV cache: bf16; 8-bit e4m3 (1 sign, 4 exponent, 3 fraction
+ * bits, no infinities, largest value 448); or 4-bit e2m1 (0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and their negatives) with one power of two for each 32 of a head's values,
+ * 17/32 of a byte a value. */
+enum { PRED_KV_BF16 = 0, PRED_KV_FP8 = 1, PRED_KV_FP4 = 2 };
 
 /* One layer's paged KV cache, memory of the caller's.  Token t of block b, head
  * h is head_dim consecutive elements at
@@ -355,14 +357,26 @@ enum { PRED_KV_BF16 = 0, PRED_KV_FP8 = 1 };
  * [max_blocks, num_kv_heads, block_size, head_dim] (A_g's) are views of it.
  * k, v and every stride must be multiples of 16 bytes (bf16) or 8 bytes (FP8),
  * token_stride and head_stride >= head_dim, and block_stride at least one
- * block's extent.  An element stands for scale * stored; with bf16 both scales
- * must be 1. */
+ * block's extent.  An element stands for scale * stored; with bf16 and FP4 both
+ * scales must be 1.
+ *
+ * FP4: head_dim and the strides are multiples of 32, k and v 16-byte aligned.
+ * The element at offset x is the low (x even) or high nibble of byte x / 2, and
+ * stands for its e2m1 value times 2^(b - 127), b the byte at offset x / 32 of
+ * k_scales or v_scales; b = 255 makes its 32 values NaN; 0, 1, 253 and 254, whose
+ * values bf16 does not all hold, are not written by the library and must not be
+ * given.  So a cache [max_blocks,
+ * block_size, num_kv_heads, head_dim / 2] of bytes has scales [.., head_dim / 32]
+ * with the same order of dimensions.  The other types do not read k_scales and
+ * v_scales. */
 typedef struct {
     void* k;
     void* v;
     int64_t block_stride, token_stride, head_stride;
     int32_t dtype;
     float k_scale, v_scale;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
 } pred_kv_cache;
 
 /* How a rotation's frequencies are stretched for contexts longer than the model
@@ -429,13 +443,73 @@ int pred_rotate(pred_t* p, const pred_rope* rope, const pred_bf16* x, int64_t x_
  *   q_out      device, [n_tokens, num_q_heads, head_dim] bf16; may be q itself if q_stride is num_q_heads * head_dim
  * A bf16 cache takes keys and values rounded once; an FP8 cache takes value /
  * scale, a float32 quotient, clamped to +-448 and rounded to the nearest (ties to
- * even), NaN kept.
+ * even), NaN kept.  An FP4 cache takes values rounded to bf16: the scale of 32 is
+ * the smallest power of two, at least 2^-125 and at most 2^125, that keeps the
+ * largest of them within 6, each value then the nearest (ties to the even pattern); a value that
+ * is not finite makes its 32 values NaN.
  * rope->backward must be 0, and the cache's k and v must not overlap (one
  * address for both is PRED_ERR_OUT_OF_RANGE). */
 int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int64_t q_stride, const pred_bf16* k,
                       int64_t k_stride, const pred_bf16* v, int64_t v_stride, int64_t n_tokens,
                       const int32_t* positions, const int64_t* slots, const pred_kv_cache* cache, pred_bf16* q_out,
                       void* stream);
+
+/* A norm of a head's values, as models put on queries and keys before the rotation:
+ *   x -> x / sqrt(mean(x^2) + eps) * (offset + weight)
+ * over the head_dim values of each head, in float32 (a sum of squares above
+ * float32's range gives 0 or NaN).  weight: device, [head_dim] bf16, 16-byte aligned, or NULL
+ * for a factor of 1 (offset then counts for nothing).  eps > 0. */
+typedef struct {
+    const pred_bf16* weight;
+    float eps;
+    float offset;
+} pred_norm;
+
+/* pred_rotate with a norm before it, in one pass: out = R(pos) norm(x), rounded
+ * once.  rope NULL: the norm alone (positions may be NULL); rope->backward must
+ * be 0.  The other arguments and their limits are pred_rotate's; out may be x
+ * itself. */
+int pred_norm_rotate(pred_t* p, const pred_norm* norm, const pred_rope* rope, const pred_bf16* x, int64_t x_stride,
+                     int64_t n_tokens, int32_t n_heads, const int32_t* positions, pred_bf16* out, int64_t out_stride,
+                     void* stream);
+
+/* Its gradient: from x as it went in and dy, the gradient of out (bf16, tokens
+ * dy_stride apart),
+ *   dx       bf16, tokens dx_stride apart; may be x or dy itself (same stride), else it must not overlap them
+ *   dweight  device, [head_dim] float32 or NULL: the gradient of (offset + weight), summed over tokens and heads in
+ *            float32 in a fixed order (equal inputs give equal bits); written, not added to
+ *   workspace  pred_norm_rotate_workspace_bytes() bytes, 16-byte aligned; NULL without dweight
+ * With dweight a second launch adds the workgroups' sums. */
+int pred_norm_rotate_backward(pred_t* p, const pred_norm* norm, const pred_rope* rope, const pred_bf16* x,
+                              int64_t x_stride, int64_t n_tokens, int32_t n_heads, const int32_t* positions,
+                              const pred_bf16* dy, int64_t dy_stride, pred_bf16* dx, int64_t dx_stride, float* dweight,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace of pred_norm_rotate_backward with dweight, at most 4096 * head_dim
+ * bytes; 0 for a NULL handle or counts < 1.  Calls that may run at the same time
+ * need workspaces of their own. */
+size_t pred_norm_rotate_workspace_bytes(pred_t* p, int64_t n_tokens, int32_t n_heads);
+
+/* pred_rotate_store with norms before the rotation, in the same launch: q_norm on
+ * the queries, k_norm on the keys, either NULL for none; rope NULL for no
+ * rotation (positions may be NULL then). */
+int pred_norm_rotate_store(pred_t* p, const pred_norm* q_norm, const pred_norm* k_norm, const pred_rope* rope,
+                           const pred_bf16* q, int64_t q_stride, const pred_bf16* k, int64_t k_stride,
+                           const pred_bf16* v, int64_t v_stride, int64_t n_tokens, const int32_t* positions,
+                           const int64_t* slots, const pred_kv_cache* cache, pred_bf16* q_out, void* stream);
+
+/* Keys and values into the cache as they are (already rotated, or of a layer
+ * without rotation), rounded as by pred_rotate_store; k, v and slots as there. */
+int pred_store(pred_t* p, const pred_bf16* k, int64_t k_stride, const pred_bf16* v, int64_t v_stride, int64_t n_tokens,
+               const int64_t* slots, const pred_kv_cache* cache, void* stream);
+
+/* Cached tokens read back: what the elements at `slots` (as for pred_rotate_store)
+ * stand for, rounded to bf16 (exact for bf16 and FP4 caches), into k_out and
+ * v_out, device, [n_tokens, num_kv_heads, head_dim] bf16, 16-byte aligned.  A
+ * token whose slot is -1 or outside the cache leaves its rows as they were; the
+ * latter raises the device error word. */
+int pred_load(pred_t* p, const pred_kv_cache* cache, int64_t n_tokens, const int64_t* slots, pred_bf16* k_out,
+              pred_bf16* v_out, void* stream);
 
 /* Attention of each sequence's newest tokens over its cached ones: one token
  * (n_rows = 1, a decode step) or a tree of drafted tokens to verify.  A

@@ -143,3 +143,78 @@ def evict(table, mass, length, block, budget, first, last):
         new_table[at] = table[b]
         new_mass[at] = 0.0 if b in gone else mass[b]
     return new_table, new_mass, length - count * block, count
+
+
+# ---------------------------------------------------------------- norms
+
+def norm(x, weight, eps, offset=0.0):
+    """x [.., D] float64, each head divided by the root of its mean square, times offset + weight (None: times 1)."""
+    factor = 1.0 if weight is None else offset + np.asarray(weight, np.float64)
+    return x / np.sqrt((x * x).sum(-1, keepdims=True) / x.shape[-1] + eps) * factor
+
+
+def norm_rotate_gradient(x, dy, positions, freq, weight, eps, offset=0.0, mscale=1.0, interleaved=False):
+    """Gradients (dx, dweight) of <rotate(norm(x)), dy>, from the derivative of each norm: d(x_i / s) / d x_j =
+    (delta_ij - x_i x_j / (D s^2)) / s with s the root."""
+    D = x.shape[-1]
+    g = np.array(dy) if freq is None else rotate(dy, positions, freq, mscale, interleaved, backward=True)
+    factor = np.ones(D) if weight is None else offset + np.asarray(weight, np.float64)
+    dx, dw = np.zeros_like(x), np.zeros(D)
+    for t in range(x.shape[0]):
+        for h in range(x.shape[1]):
+            v = x[t, h]
+            s = math.sqrt((v * v).sum() / D + eps)
+            dx[t, h] = ((np.eye(D) - np.outer(v, v) / (D * s * s)) / s) @ (g[t, h] * factor)
+            dw += g[t, h] * v / s
+    return dx, dw
+
+
+# ---------------------------------------------------------------- a cache in 4 bits
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def quantise(x):
+    """x [.., D] float64 -> (codes [.., D] of 4 bits, scale bytes [.., D / 32]): each 32 values in units of the smallest
+    power of two, 2^-125 to 2^125, that keeps the largest within 6; each the nearest, ties to the even code."""
+    flat = np.asarray(x, np.float64).reshape(-1, 32)
+    codes, scales = np.zeros(flat.shape, np.uint8), np.zeros(len(flat), np.uint8)
+    for i, group in enumerate(flat):
+        if not np.all(np.isfinite(group)):
+            scales[i] = 255
+            continue
+        e = -125
+        while e < 125 and np.abs(group).max() > 6 * 2.0 ** e:
+            e += 1
+        scales[i] = e + 127
+        for j, v in enumerate(group):
+            far = np.abs(np.abs(v) / 2.0 ** e - E2M1)
+            near = np.nonzero(far == far.min())[0]
+            code = near[0] if len(near) == 1 else near[near % 2 == 0][0]
+            codes[i, j] = code + (8 if np.signbit(v) else 0)
+    return codes.reshape(x.shape), scales.reshape(*x.shape[:-1], x.shape[-1] // 32)
+
+
+def dequantise(codes, scales):
+    """The values codes [.., D] and scale bytes [.., D / 32] stand for, float64."""
+    value = np.where(codes & 8, -1.0, 1.0) * E2M1[codes & 7]
+    factor = np.where(scales == 255, np.nan, 2.0 ** (scales.astype(np.float64) - 127))
+    return value * np.repeat(factor, 32, -1)
+
+
+def unpacked(packed):
+    """Bytes [.., D / 2] -> codes [.., D], the low nibble first."""
+    return np.stack((packed & 15, packed >> 4), -1).reshape(*packed.shape[:-1], -1)
+
+
+# ---------------------------------------------------------------- windows
+
+def seen_in_window(rows, length, count, window, sinks):
+    """[rows, length] bool: the newest `count` tokens are the rows; each sees the `window` newest tokens up to itself
+    and the first `sinks` (rows at or past `count`: nothing)."""
+    see = np.zeros((rows, length), bool)
+    for i in range(min(rows, count)):
+        pos = length - count + i
+        for t in range(pos + 1):
+            see[i, t] = pos - t < window or t < sinks
+    return see

@@ -13,7 +13,7 @@ import numpy as np
 from . import _lib
 from ._lib import (PRED_FLAG_ZERO_AG, PRED_OK, PredDims, ERROR_NAMES, PRED_NOALLOC_SCRATCH_BYTES,  # noqa: F401
                    PRED_SCORE_PATH_AUTO, PRED_SCORE_PATH_DECODE, PRED_SCORE_PATH_GENERIC,
-                   PRED_KV_BF16, PRED_KV_FP8, PRED_ROPE_NONE, PRED_ROPE_LINEAR, PRED_ROPE_NTK, PRED_ROPE_LLAMA3,
+                   PRED_KV_BF16, PRED_KV_FP8, PRED_KV_FP4, PRED_ROPE_NONE, PRED_ROPE_LINEAR, PRED_ROPE_NTK, PRED_ROPE_LLAMA3,
                    PRED_ROPE_YARN,
                    PRED_ERR_INVALID_DIMS, PRED_ERR_OUT_OF_RANGE, PRED_ERR_OOM, PRED_ERR_UNSUPPORTED,
                    PRED_ERR_NULL_ARG, PRED_ERR_HIP, PRED_ERR_WORKSPACE, PRED_ERR_DEVICE)
@@ -323,9 +323,10 @@ def pred_decode_step(h, layer0, k_new, new_table, q, q_proj, block_tables, last_
 
 # ------------------------------------------------------------------ the paged KV cache
 
-from .cache import (KVCache, Rope, pred_accumulate_weight, pred_attend, pred_attend_kernel_name,  # noqa: E402,F401
-                    pred_attend_workspace_bytes, pred_evict_blocks, pred_evict_workspace_bytes, pred_rope_turns,
-                    pred_rotate, pred_rotate_store)
+from .cache import (KVCache, Norm, Rope, pred_accumulate_weight, pred_attend, pred_attend_kernel_name,  # noqa: E402,F401
+                    pred_attend_workspace_bytes, pred_evict_blocks, pred_evict_workspace_bytes, pred_load,
+                    pred_norm_rotate, pred_norm_rotate_backward, pred_norm_rotate_store,
+                    pred_norm_rotate_workspace_bytes, pred_rope_turns, pred_rotate, pred_rotate_store, pred_store)
 
 
 # ------------------------------------------------------------------ inspection

@@ -31,6 +31,7 @@ PRED_SCORE_PATH_GENERIC = 2
 
 PRED_KV_BF16 = 0
 PRED_KV_FP8 = 1
+PRED_KV_FP4 = 2
 
 PRED_ROPE_NONE = 0
 PRED_ROPE_LINEAR = 1
@@ -72,6 +73,8 @@ class PredKvCache(ctypes.Structure):
         ("dtype", ctypes.c_int32),
         ("k_scale", ctypes.c_float),
         ("v_scale", ctypes.c_float),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
     ]
 
 
@@ -95,6 +98,14 @@ class PredRope(ctypes.Structure):
     ]
 
 
+class PredNorm(ctypes.Structure):
+    _fields_ = [
+        ("weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("offset", ctypes.c_float),
+    ]
+
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
@@ -104,6 +115,7 @@ _sz = ctypes.c_size_t
 _PD = ctypes.POINTER(PredDims)
 _PC = ctypes.POINTER(PredKvCache)
 _PR = ctypes.POINTER(PredRope)
+_PN = ctypes.POINTER(PredNorm)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -140,6 +152,14 @@ SIGNATURES = {
                                        ctypes.POINTER(_f32)]),
     "pred_rotate": (ctypes.c_int, [_vp, _PR, _vp, _i64, _i64, _i32, _vp, _vp, _i64, _vp]),
     "pred_rotate_store": (ctypes.c_int, [_vp, _PR, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _PC, _vp, _vp]),
+    "pred_norm_rotate": (ctypes.c_int, [_vp, _PN, _PR, _vp, _i64, _i64, _i32, _vp, _vp, _i64, _vp]),
+    "pred_norm_rotate_backward": (ctypes.c_int, [_vp, _PN, _PR, _vp, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _vp,
+                                                 _vp, _sz, _vp]),
+    "pred_norm_rotate_workspace_bytes": (_sz, [_vp, _i64, _i32]),
+    "pred_norm_rotate_store": (ctypes.c_int, [_vp, _PN, _PN, _PR, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _PC,
+                                              _vp, _vp]),
+    "pred_store": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, _i64, _vp, _PC, _vp]),
+    "pred_load": (ctypes.c_int, [_vp, _PC, _i64, _vp, _vp, _vp, _vp]),
     "pred_attend": (ctypes.c_int, [_vp, _PC, _vp, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _sz,
                                    _vp]),
     "pred_attend_workspace_bytes": (_sz, [_vp, _i32, _i32, _i64]),

@@ -1,8 +1,8 @@
 """Binding of the paged KV cache operators (include/pred.h, "the paged KV cache").
 
 As in the package's other calls, the functions carry the C names and only
-marshal arguments.  ``KVCache`` and ``Rope`` describe a cache and a rotation once,
-for all the calls of a program that keeps them.
+marshal arguments.  ``KVCache``, ``Rope`` and ``Norm`` describe a cache, a rotation and a
+norm once, for all the calls of a program that keeps them.
 """
 
 import ctypes
@@ -10,20 +10,21 @@ import ctypes
 import numpy as np
 
 from . import _lib
-from ._lib import PredKvCache, PredRope, PredRopeScaling
+from ._lib import PredKvCache, PredNorm, PredRope, PredRopeScaling
 
 _KINDS = {"none": _lib.PRED_ROPE_NONE, "linear": _lib.PRED_ROPE_LINEAR, "ntk": _lib.PRED_ROPE_NTK,
           "llama3": _lib.PRED_ROPE_LLAMA3, "yarn": _lib.PRED_ROPE_YARN}
 
 # torch and the dtypes a tensor may have, from the first call that takes tensors on (the package itself needs none)
-torch = _BF16 = _FP8 = _WORD = _I32 = _F32 = _current_raw = None
+torch = _BF16 = _FP8 = _E8M0 = _WORD = _I32 = _F32 = _current_raw = None
 
 
 def _load_torch():
-    global torch, _BF16, _FP8, _WORD, _I32, _F32, _current_raw
+    global torch, _BF16, _FP8, _E8M0, _WORD, _I32, _F32, _current_raw
     import torch as t
     _BF16 = (t.bfloat16, t.int16, t.uint16)
     _FP8 = (t.float8_e4m3fn, t.uint8)
+    _E8M0 = tuple(x for x in (t.uint8, getattr(t, "float8_e8m0fnu", None)) if x is not None)
     _WORD = (t.int64, t.uint64)
     _I32, _F32 = (t.int32,), (t.float32,)
     _current_raw = getattr(t._C, "_cuda_getCurrentRawStream", None)
@@ -104,34 +105,59 @@ class _Args:
 class KVCache:
     """One layer's paged cache: ``k`` and ``v`` [max_blocks, block_size, num_kv_heads, head_dim], bf16 or e4m3
     (float8_e4m3fn or uint8), views with equal strides whose last dimension is contiguous.  An element stands for
-    ``k_scale`` (``v_scale``) times what is stored; a bf16 cache has scales of 1.  Keeps the tensors alive."""
+    ``k_scale`` (``v_scale``) times what is stored; a bf16 cache has scales of 1.  With ``k_scales`` and ``v_scales``
+    (uint8 or float8_e8m0fnu [.., head_dim / 32]) the cache is held in 4 bits: ``k`` and ``v`` are [.., head_dim / 2]
+    uint8, two e2m1 values a byte, the even one low, and the scales views of the same order of dimensions.  Keeps the
+    tensors alive."""
 
-    __slots__ = ("k", "v", "shape", "device", "_struct", "_ref")
+    __slots__ = ("k", "v", "k_scales", "v_scales", "shape", "device", "_struct", "_ref")
 
-    def __init__(self, k, v, k_scale=1.0, v_scale=1.0):
+    def __init__(self, k, v, k_scale=1.0, v_scale=1.0, k_scales=None, v_scales=None):
         if torch is None:
             _load_torch()
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("a 4-bit cache has both k_scales and v_scales")
+        fp4 = k_scales is not None
         for t, what in ((k, "k"), (v, "v")):
             if not isinstance(t, torch.Tensor) or t.dim() != 4:
                 raise TypeError(f"{what}: expected a tensor [max_blocks, block_size, num_kv_heads, head_dim]")
             if t.device.type != "cuda":
                 raise ValueError(f"{what}: tensor must live on the GPU")
-            if t.dtype not in _BF16 + _FP8:
-                raise TypeError(f"{what}: dtype {t.dtype} not in {_BF16 + _FP8}")
+            if t.dtype not in (_FP8[1:] if fp4 else _BF16 + _FP8):
+                raise TypeError(f"{what}: dtype {t.dtype} not in {_FP8[1:] if fp4 else _BF16 + _FP8}")
         if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.device != v.device:
             raise ValueError("k and v must have one shape, one dtype, one device and the same strides")
         if k.shape[3] > 1 and k.stride(3) != 1:
             raise ValueError("the last dimension must be contiguous")
-        self.k, self.v, self.shape, self.device = k, v, tuple(k.shape), k.get_device()
-        n, block, heads, dim = self.shape
+        self.k, self.v, self.device = k, v, k.get_device()
+        self.k_scales, self.v_scales = k_scales, v_scales
+        per = 2 if fp4 else 1       # values of an element of the tensors
+        n, block, heads, dim = self.shape = (*k.shape[:3], per * k.shape[3])
         # a dimension of one element is never stepped over, whatever its stride says
-        token = k.stride(1) if block > 1 else max(dim, heads * k.stride(2) if heads > 1 else dim)
-        head = k.stride(2) if heads > 1 else max(dim, dim if block == 1 else block * token)
+        token = per * k.stride(1) if block > 1 else max(dim, heads * per * k.stride(2) if heads > 1 else dim)
+        head = per * k.stride(2) if heads > 1 else max(dim, dim if block == 1 else block * token)
         extent = (block - 1) * token + (heads - 1) * head + dim
-        stride = k.stride(0) if n > 1 else -(-extent // 16) * 16
+        stride = per * k.stride(0) if n > 1 else -(-extent // 32) * 32
+        scales = self._scales_at((stride, token, head)) if fp4 else (None, None)
         self._struct = PredKvCache(k.data_ptr(), v.data_ptr(), stride, token, head,
-                                   _lib.PRED_KV_FP8 if k.dtype in _FP8 else _lib.PRED_KV_BF16, k_scale, v_scale)
+                                   _lib.PRED_KV_FP4 if fp4 else _lib.PRED_KV_FP8 if k.dtype in _FP8 else _lib.PRED_KV_BF16,
+                                   k_scale, v_scale, *scales)
         self._ref = ctypes.byref(self._struct)
+
+    def _scales_at(self, strides):
+        """The scales' addresses, once they are seen to lie as the values do: a byte each 32 of them."""
+        want = (*self.shape[:3], self.shape[3] // 32)
+        for t, what in ((self.k_scales, "k_scales"), (self.v_scales, "v_scales")):
+            if not isinstance(t, torch.Tensor) or t.dtype not in _E8M0:
+                raise TypeError(f"{what}: expected a tensor of {_E8M0}")
+            if t.get_device() != self.device:
+                raise ValueError(f"{what}: tensor must live on the GPU of k and v ({self.device}), not on {t.device}")
+            if tuple(t.shape) != want or self.shape[3] % 32:
+                raise ValueError(f"{what} must be {list(want)} with head_dim a multiple of 32, not {list(t.shape)}")
+            if want[3] > 1 and t.stride(3) != 1 or any(
+                    n > 1 and 32 * t.stride(i) != s for i, (n, s) in enumerate(zip(want[:3], strides))):
+                raise ValueError(f"{what}: strides {t.stride()} must be 1/16 of the bytes' {self.k.stride()}")
+        return self.k_scales.data_ptr(), self.v_scales.data_ptr()
 
     def _of(self, d, args):
         if self.shape != (d.max_blocks, d.block_size, d.num_kv_heads, d.head_dim):
@@ -161,6 +187,33 @@ class Rope:
     def _on(self, args):
         if self.device != args.device:
             raise ValueError(f"turns must live on the current GPU ({args.device}), not on {self.device}")
+        return self._ref
+
+
+class Norm:
+    """A norm of each head's values: x / sqrt(mean(x^2) + eps) * (offset + weight), weight [head_dim] bf16 on the GPU or
+    None for a factor of 1.  Keeps the weight alive."""
+
+    __slots__ = ("weight", "device", "_struct", "_ref")
+
+    def __init__(self, weight, eps, offset=0.0):
+        if torch is None:
+            _load_torch()
+        if weight is not None:
+            if not isinstance(weight, torch.Tensor) or weight.dtype not in _BF16 or weight.device.type != "cuda":
+                raise TypeError("weight: expected a bf16 tensor on the GPU")
+            if weight.dim() != 1 or not weight.is_contiguous():
+                raise ValueError(f"weight must be contiguous [head_dim], not {list(weight.shape)}")
+        self.weight, self.device = weight, None if weight is None else weight.get_device()
+        self._struct = PredNorm(None if weight is None else weight.data_ptr(), eps, offset)
+        self._ref = ctypes.byref(self._struct)
+
+    def _of(self, d, args):
+        if self.weight is not None:
+            if self.device != args.device:
+                raise ValueError(f"weight must live on the current GPU ({args.device}), not on {self.device}")
+            if self.weight.shape[0] != d.head_dim:
+                raise ValueError(f"weight must be [{d.head_dim}], not {list(self.weight.shape)}")
         return self._ref
 
 
@@ -206,6 +259,84 @@ def pred_rotate_store(h, rope, q, k, v, positions, slots, cache, q_out, stream=N
         h, rope._on(a), qp, qs, kp, ks, vp, vs, n, a.ptr(positions, "positions", _I32, (n,)),
         a.ptr(slots, "slots", _WORD[:1], (n,)), cache._of(d, a),
         a.ptr(q_out, "q_out", _BF16, (n, d.num_q_heads, d.head_dim)), _raw_stream(stream, a.device)))
+
+
+def _positions(a, rope, positions, n):
+    return None if rope is None and positions is None else a.ptr(positions, "positions", _I32, (n,))
+
+
+def pred_norm_rotate(h, norm, rope, x, positions, out, stream=None):
+    """x [n_tokens, n_heads, head_dim] bf16 (tokens may lie apart), each head normed, then rotated to its positions
+    [n_tokens] int32 (rope None: the norm alone) into out (x itself for in place)."""
+    d, a = _dims(h), _Args()
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise TypeError("x: expected a tensor [n_tokens, n_heads, head_dim]")
+    n, heads = x.shape[0], x.shape[1]
+    xp, xs = a.rows(x, "x", n, heads, d.head_dim)
+    op, os_ = a.rows(out, "out", n, heads, d.head_dim)
+    _check(_lib.load().pred_norm_rotate(h, norm._of(d, a), rope and rope._on(a), xp, xs, n, heads,
+                                        _positions(a, rope, positions, n), op, os_, _raw_stream(stream, a.device)))
+
+
+def pred_norm_rotate_workspace_bytes(h, n_tokens, n_heads):
+    return _lib.load().pred_norm_rotate_workspace_bytes(h, n_tokens, n_heads)
+
+
+def pred_norm_rotate_backward(h, norm, rope, x, positions, dy, dx, dweight=None, workspace=None, stream=None):
+    """Gradients of pred_norm_rotate(h, norm, rope, x, positions, out) from out's gradient dy: dx (like x; x or dy itself
+    for in place) and dweight [head_dim] float32 or None (which needs a workspace)."""
+    d, a = _dims(h), _Args()
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise TypeError("x: expected a tensor [n_tokens, n_heads, head_dim]")
+    n, heads = x.shape[0], x.shape[1]
+    xp, xs = a.rows(x, "x", n, heads, d.head_dim)
+    yp, ys = a.rows(dy, "dy", n, heads, d.head_dim)
+    dp, ds = a.rows(dx, "dx", n, heads, d.head_dim)
+    ws, ws_bytes = a.buffer(workspace, "workspace")
+    _check(_lib.load().pred_norm_rotate_backward(
+        h, norm._of(d, a), rope and rope._on(a), xp, xs, n, heads, _positions(a, rope, positions, n), yp, ys, dp, ds,
+        a.ptr(dweight, "dweight", _F32, (d.head_dim,)), ws, ws_bytes, _raw_stream(stream, a.device)))
+
+
+def pred_norm_rotate_store(h, q_norm, k_norm, rope, q, k, v, positions, slots, cache, q_out, stream=None):
+    """pred_rotate_store with q_norm on the queries and k_norm on the keys before the rotation (None: no norm, no
+    rotation)."""
+    d, a = _dims(h), _Args()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q: expected a tensor [n_tokens, num_q_heads, head_dim]")
+    n = q.shape[0]
+    qp, qs = a.rows(q, "q", n, d.num_q_heads, d.head_dim)
+    kp, ks = a.rows(k, "k", n, d.num_kv_heads, d.head_dim)
+    vp, vs = a.rows(v, "v", n, d.num_kv_heads, d.head_dim)
+    _check(_lib.load().pred_norm_rotate_store(
+        h, q_norm and q_norm._of(d, a), k_norm and k_norm._of(d, a), rope and rope._on(a), qp, qs, kp, ks, vp, vs, n,
+        _positions(a, rope, positions, n), a.ptr(slots, "slots", _WORD[:1], (n,)), cache._of(d, a),
+        a.ptr(q_out, "q_out", _BF16, (n, d.num_q_heads, d.head_dim)), _raw_stream(stream, a.device)))
+
+
+def pred_store(h, k, v, slots, cache, stream=None):
+    """k, v [n_tokens, num_kv_heads, head_dim] bf16 (tokens may lie apart) into the cache at slots [n_tokens] int64, as
+    they are."""
+    d, a = _dims(h), _Args()
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise TypeError("k: expected a tensor [n_tokens, num_kv_heads, head_dim]")
+    n = k.shape[0]
+    kp, ks = a.rows(k, "k", n, d.num_kv_heads, d.head_dim)
+    vp, vs = a.rows(v, "v", n, d.num_kv_heads, d.head_dim)
+    _check(_lib.load().pred_store(h, kp, ks, vp, vs, n, a.ptr(slots, "slots", _WORD[:1], (n,)), cache._of(d, a),
+                                  _raw_stream(stream, a.device)))
+
+
+def pred_load(h, cache, slots, k_out, v_out, stream=None):
+    """The cached tokens at slots [n_tokens] int64 (-1: none) into k_out, v_out [n_tokens, num_kv_heads, head_dim] bf16."""
+    d, a = _dims(h), _Args()
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise TypeError("slots: expected a tensor [n_tokens]")
+    n = slots.shape[0]
+    shape = (n, d.num_kv_heads, d.head_dim)
+    _check(_lib.load().pred_load(h, cache._of(d, a), n, a.ptr(slots, "slots", _WORD[:1], (n,)),
+                                 a.ptr(k_out, "k_out", _BF16, shape), a.ptr(v_out, "v_out", _BF16, shape),
+                                 _raw_stream(stream, a.device)))
 
 
 def pred_attend_workspace_bytes(h, n_seqs, n_rows, n_blocks):

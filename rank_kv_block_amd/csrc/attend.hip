@@ -14,6 +14,15 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // for a masked score before the first real one.
 constexpr float kLowest = -3.402823466e38f;
 
+// How a cache holds its values.
+enum Held : int { BF16, FP8, FP4 };
+// bytes of x values (or of a stride of x)
+template <Held HELD>
+__host__ __device__ inline int64_t bytes_of(int64_t x) {
+    return HELD == FP4 ? x / 2 : (HELD == FP8 ? x : 2 * x);
+}
+inline Held held_of(const CacheView& c) { return c.fp4 ? FP4 : (c.fp8 ? FP8 : BF16); }
+
 __device__ inline float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ inline float log2_of(float x) { return __builtin_amdgcn_logf(x); }
 
@@ -64,15 +73,22 @@ __device__ inline float joined(float a, float fa, float b, float fb) {
 // tokens, 32 queries of 64 over 8 e4m3 heads: 2021 us, the tree kernel 39; one
 // sequence of 16384 tokens, 32 queries over 8 bf16 heads: 4.9 ms at a head size
 // of 80 and 13.1 ms at 256, the stream kernel 18 us at 128).
-template <bool FP8>
-__device__ inline float cache_value(const void* p, int64_t at) {
-    if constexpr (FP8) return fp8_value(static_cast<const uint8_t*>(p)[at]);
-    else return bf16_lo(static_cast<const uint16_t*>(p)[at]);
+template <Held HELD>
+__device__ inline float cache_value(const void* p, const uint8_t* scales, int64_t at) {
+    if constexpr (HELD == FP4) {
+        const uint32_t byte = static_cast<const uint8_t*>(p)[at / 2];
+        const auto pair = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(byte, __uint_as_float((uint32_t)scales[at / 32] << 23), 0);
+        return at % 2 ? pair[1] : pair[0];
+    } else if constexpr (HELD == FP8) {
+        return fp8_value(static_cast<const uint8_t*>(p)[at]);
+    } else {
+        return bf16_lo(static_cast<const uint16_t*>(p)[at]);
+    }
 }
 
 constexpr int kPlainHead = 256;     // largest head size
 
-template <bool FP8>
+template <Held HELD>
 __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
     __shared__ float q_row[kPlainHead];
     __shared__ float part[4][kPlainHead];
@@ -104,7 +120,7 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
             float x = 0.f;
             if (sees) {
                 const int64_t at = base + lane * a.cache.token_stride;
-                for (int d = 0; d < a.D; ++d) x += q_row[d] * cache_value<FP8>(a.cache.k, at + d);
+                for (int d = 0; d < a.D; ++d) x += q_row[d] * cache_value<HELD>(a.cache.k, a.cache.k_scales, at + d);
             }
             x = sees ? x * scale : -INFINITY;
             float top = x;
@@ -129,14 +145,14 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
                 const int64_t at = base + tok * a.cache.token_stride;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (lane + 64 * e < a.D) acc[e] += w * cache_value<FP8>(a.cache.v, at + lane + 64 * e);
+                    if (lane + 64 * e < a.D) acc[e] += w * cache_value<HELD>(a.cache.v, a.cache.v_scales, at + lane + 64 * e);
             }
         }
         if (a.block_lse && lane == 0)
             a.block_lse[(((int64_t)s * a.n + b) * a.M + i) * a.Hq + h] =
                 bl <= 0.f ? -INFINITY : (bm + log2_of(bl)) * kLn2;
     }
-    if constexpr (!FP8) {
+    if constexpr (HELD == BF16) {
         const float lost = acc[0] * 0.f + acc[1] * 0.f + acc[2] * 0.f + acc[3] * 0.f;      // NaN where a sum is not finite
         if (__ballot(lost != 0.f) && l == l) {
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -149,7 +165,7 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
                     const int64_t at = slot * a.cache.block_stride + t0 * a.cache.token_stride + head_off;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (lane + 64 * e < a.D) sum[e] += not_finite(cache_value<FP8>(a.cache.v, at + lane + 64 * e));
+                        if (lane + 64 * e < a.D) sum[e] += not_finite(cache_value<HELD>(a.cache.v, a.cache.v_scales, at + lane + 64 * e));
                 }
             }
 #pragma unroll
@@ -529,18 +545,17 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
 // table, first tiles) and end: 1024 tokens of one head of 64 take 8.0 us.  17 to
 // 32 queries are two groups: 131072 tokens with 32 queries a head take 142 us and
 // move 771 MB, with 16 queries 95 us and 538 MB.
-template <int D_, bool FP8_>
+template <int D, Held HELD>
 struct StreamLayout {
-    static constexpr int D = D_;
-    static constexpr bool FP8 = FP8_;
-    static constexpr int RB = D * (FP8 ? 1 : 2);    // bytes of a row
+    static constexpr int RB = (int)(HELD == FP4 ? D / 2 : (HELD == FP8 ? D : 2 * D));       // bytes of a row
     static constexpr int TPL = 1024 / RB;           // tokens of a wave-load
     static constexpr int NK = 32 / TPL;             // key loads of a tile
     static constexpr int W = TPL / 4;               // tokens a lane scores per load
     static constexpr int H = RB / 64;               // 64-byte parts of a row
-    static constexpr int KP = FP8 ? 2 : 1;          // products of 32 values per part
+    static constexpr int KP = HELD == FP4 ? 4 : (HELD == FP8 ? 2 : 1);      // products of 32 values per part
     static constexpr int J = D / 16;                // values a lane holds of a token
     static constexpr int VW = RB / 64;              // 4-byte words of them as stored
+    static_assert(H >= 1, "a token's head fills a lane group");
 };
 
 // max / sum over the four lanes (n, 0..3) of a query
@@ -575,6 +590,15 @@ __device__ inline bf16x8_t signed_by(float scale, bf16x8_t x) {
 template <bool HI>
 __device__ inline uint32_t fp8x2_to_bf16(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI));
+}
+
+// eight e2m1 values as eight bf16 times the power of two of a scale byte, exact
+__device__ inline u32x4_t fp4x8_to_bf16(uint32_t w, uint32_t scale_byte) {
+    const float scale = __uint_as_float(scale_byte << 23);
+    return u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3))};
 }
 
 // Division of a token's index by the block size: one 64-bit product.  With
@@ -624,13 +648,17 @@ __device__ inline uint32_t finite_only_fp8(uint32_t w) {
 // the matrix cores.  So drafted tokens' values enter the products with 0 in the
 // place of what is not finite.  A run that holds any, or whose sums are not
 // finite (every row sees the whole context), walks its tokens once more and
-// takes what is not finite from there.  (e4m3 has no infinities, and a NaN of
-// the context needs no walk.)
+// takes what is not finite from there.  (e4m3 and a 4-bit cache have no
+// infinities, and a NaN of the context needs no walk.)
 
-// Adds what is not finite among the 4 values from d on of a token's head.
-template <bool FP8>
+// Adds what is not finite among the 4 values from d on of a token's head, `row` from value_row.
+template <Held HELD>
 __device__ inline void add_not_finite(float* sum, const char* row, int d) {
-    if constexpr (FP8) {
+    if constexpr (HELD == FP4) {
+        if ((uint8_t)row[d / 32] == 255u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = NAN;
+    } else if constexpr (HELD == FP8) {
         const uint32_t w = *reinterpret_cast<const uint32_t*>(row + d);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -643,14 +671,16 @@ __device__ inline void add_not_finite(float* sum, const char* row, int d) {
         sum[3] += not_finite(bf16_hi(w.y));
     }
 }
-// The values of a token's head, null where its block has an invalid entry.
-__device__ inline const char* value_row(const AttendArgs& a, const BlockSize& bs, int s, int kvh, int tok, int64_t item) {
+// The values of a token's head (of a 4-bit cache their scales), null where its block has an invalid entry.
+template <Held HELD>
+__device__ inline const char* value_row(const AttendArgs& a, const BlockSize& bs, int s, int kvh, int tok) {
     const int b = bs.block(tok);
     const int64_t slot = a.tables ? a.tables[(int64_t)s * a.n + b] : b;
     if (slot < 0 || slot >= a.N) return nullptr;
-    return static_cast<const char*>(a.cache.v) +
-           (slot * a.cache.block_stride + (int64_t)(tok - b * bs.B) * a.cache.token_stride +
-            (int64_t)kvh * a.cache.head_stride) * item;
+    const int64_t at = slot * a.cache.block_stride + (int64_t)(tok - b * bs.B) * a.cache.token_stride +
+                       (int64_t)kvh * a.cache.head_stride;
+    if constexpr (HELD == FP4) return reinterpret_cast<const char*>(a.cache.v_scales) + at / 32;
+    return static_cast<const char*>(a.cache.v) + bytes_of<HELD>(at);
 }
 
 // The blocks of one sequence as a wave walks it: 64 blocks at a time, a lane
@@ -725,9 +755,9 @@ __device__ inline void stream_load(uint32_t* dst, const char* base, uint32_t off
     }
 }
 
-template <int D, bool FP8>
+template <int D, Held HELD>
 __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Plan pl, BlockSize bs) {
-    using L = StreamLayout<D, FP8>;
+    using L = StreamLayout<D, HELD>;
     constexpr int NK = L::NK, W = L::W, H = L::H, KP = L::KP, J = L::J, TPL = L::TPL, VW = L::VW;
     __shared__ float exchange[2][(J * 4 + 2) * 64];
 
@@ -765,15 +795,17 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
             if (live) q[j][k] = signed_by(a.scale, load8(a.q + row * D + 8 * KP * (4 * j + c) + 8 * k));
         }
 
-    const int64_t item = FP8 ? 1 : 2;
-    const int ts = (int)(a.cache.token_stride * item), block_ts = bs.B * ts;
-    const int64_t block_bytes = a.cache.block_stride * item, head_off = kvh * a.cache.head_stride * item;
+    const int ts = (int)bytes_of<HELD>(a.cache.token_stride), block_ts = bs.B * ts;
+    const int64_t block_bytes = bytes_of<HELD>(a.cache.block_stride), head_off = bytes_of<HELD>(kvh * a.cache.head_stride);
     const char* const kp = static_cast<const char*>(a.cache.k) + head_off;
     const char* const vp = static_cast<const char*>(a.cache.v) + head_off;
     const uint32_t k_off = n / H * ts + 16 * (4 * (n % H) + c);
     uint32_t v_off[W];
 #pragma unroll
     for (int w = 0; w < W; ++w) v_off[w] = (W * c + w) * ts + n * (VW * 4);
+    // of a 4-bit cache: 16 bytes of values have a scale byte
+    const uint8_t* const ksp = HELD == FP4 ? a.cache.k_scales + head_off / 16 : nullptr;
+    const uint8_t* const vsp = HELD == FP4 ? a.cache.v_scales + head_off / 16 : nullptr;
 
     TableWindow table;
     table.row = a.tables ? a.tables + (int64_t)s * a.n : nullptr;
@@ -786,6 +818,7 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
     // Where a tile's wave-loads begin (each inside one block), moving the window if the tile is past it.
     int64_t place[NK];
     uint32_t kr[NK][4], vr[8][VW];
+    uint32_t k_sc[NK], v_sc[8];     // their scale bytes
     auto places = [&](int t) {
         const int b = bs.block(t), last = bs.block(t + 31 < t1 ? t + 31 : t1 - 1);
         if (last >= table.first + 64) table.load(a, b, block_bytes, lane);
@@ -801,13 +834,19 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
     };
     auto load_k = [&]() {
 #pragma unroll
-        for (int u = 0; u < NK; ++u) stream_load<16>(kr[u], kp + place[u], k_off);
+        for (int u = 0; u < NK; ++u) {
+            stream_load<16>(kr[u], kp + place[u], k_off);
+            if constexpr (HELD == FP4) k_sc[u] = (ksp + (place[u] >> 4))[k_off / 16];
+        }
     };
     auto load_v = [&]() {
 #pragma unroll
         for (int u = 0; u < NK; ++u)
 #pragma unroll
-            for (int w = 0; w < W; ++w) stream_load<VW * 4>(vr[u * W + w], vp + place[u], v_off[w]);
+            for (int w = 0; w < W; ++w) {
+                stream_load<VW * 4>(vr[u * W + w], vp + place[u], v_off[w]);
+                if constexpr (HELD == FP4) v_sc[u * W + w] = (vsp + (place[u] >> 4))[v_off[w] / 16];
+            }
     };
 
     f32x4_t o[J];
@@ -832,7 +871,10 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 #pragma unroll
         for (int u = 0; u < NK; ++u) {
             bf16x8_t key[KP];
-            if constexpr (FP8) {
+            if constexpr (HELD == FP4) {
+#pragma unroll
+                for (int kk = 0; kk < KP; ++kk) key[kk] = __builtin_bit_cast(bf16x8_t, fp4x8_to_bf16(kr[u][kk], k_sc[u]));
+            } else if constexpr (HELD == FP8) {
                 key[0] = __builtin_bit_cast(bf16x8_t, (u32x4_t){fp8x2_to_bf16<false>(kr[u][0]), fp8x2_to_bf16<true>(kr[u][0]),
                                                                 fp8x2_to_bf16<false>(kr[u][1]), fp8x2_to_bf16<true>(kr[u][1])});
                 key[KP - 1] = __builtin_bit_cast(bf16x8_t, (u32x4_t){fp8x2_to_bf16<false>(kr[u][2]), fp8x2_to_bf16<true>(kr[u][2]),
@@ -877,13 +919,19 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
                 const int at = tok - ctx;
                 const bool sees = there && (at < 0 || ((seen >> (at & 63)) & 1));
                 x[e] = sees ? x[e] : -INFINITY;
+                if constexpr (HELD == FP4) {
+                    const bool bad = v_sc[e] == 255u;
+                    odd |= bad && there && at >= 0;
+                    if (!there || (bad && at >= 0)) vr[e][0] = v_sc[e] = 0u;
+                } else {
 #pragma unroll
-                for (int y = 0; y < VW; ++y) {
-                    vr[e][y] = there ? vr[e][y] : 0u;       // no value there at all
-                    const uint32_t finite = FP8 ? finite_only_fp8(vr[e][y]) : finite_only(vr[e][y]);
-                    if (at >= 0 && finite != vr[e][y]) {
-                        vr[e][y] = finite;
-                        odd = true;
+                    for (int y = 0; y < VW; ++y) {
+                        vr[e][y] = there ? vr[e][y] : 0u;       // no value there at all
+                        const uint32_t finite = HELD == FP8 ? finite_only_fp8(vr[e][y]) : finite_only(vr[e][y]);
+                        if (at >= 0 && finite != vr[e][y]) {
+                            vr[e][y] = finite;
+                            odd = true;
+                        }
                     }
                 }
             }
@@ -989,7 +1037,11 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
         uint32_t vw[8][J / 2];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if constexpr (FP8) {
+            if constexpr (HELD == FP4) {
+                const u32x4_t w = fp4x8_to_bf16(vr[e][0], v_sc[e]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) vw[e][y] = w[y];
+            } else if constexpr (HELD == FP8) {
 #pragma unroll
                 for (int y = 0; y < VW; ++y) {
                     vw[e][2 * y] = fp8x2_to_bf16<false>(vr[e][y]);
@@ -1017,7 +1069,7 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 
     l = sum_over_c(l);
     bool lost = false;
-    if constexpr (!FP8) {
+    if constexpr (HELD == BF16) {
         float x = 0.f;      // NaN where a sum is not finite
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -1034,12 +1086,12 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
             for (int j = 0; j < J; ++j) sum[v][j] = 0.f;
         for (int tok = all || ctx < t0 ? t0 : ctx; tok < t1; ++tok) {
             if ((tok - t0) / 32 / per % 4 != wave) continue;        // another wave's
-            const char* const from = value_row(a, bs, s, kvh, tok, item);
+            const char* const from = value_row<HELD>(a, bs, s, kvh, tok);
             if (from && (tok < ctx || ((seen >> ((tok - ctx) & 63)) & 1))) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
 #pragma unroll
-                    for (int j = 0; j < J; j += 4) add_not_finite<FP8>(sum[v] + j, from, J * (4 * c + v) + j);
+                    for (int j = 0; j < J; j += 4) add_not_finite<HELD>(sum[v] + j, from, J * (4 * c + v) + j);
             }
         }
 #pragma unroll
@@ -1164,12 +1216,13 @@ typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 
 // BLOCKS: block sums a half tile has: 0 without block_lse, 1 for blocks of 32
 // tokens or more, 2 for 16, 4 for 8.
-template <int D, bool FP8, int BLOCKS>
+template <int D, Held HELD, int BLOCKS>
 __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan pl, BlockSize bs) {
     using T = TreeLds<D>;
-    constexpr int RB = D * (FP8 ? 1 : 2);       // bytes of a cache row
+    constexpr int RB = (int)(HELD == FP4 ? D / 2 : (HELD == FP8 ? D : 2 * D));      // bytes of a cache row
     constexpr int CR = RB / 16;                 // 16-byte pieces of it
-    constexpr int NR = 64 * CR / 256;           // pieces a thread stages, of keys and of values
+    constexpr int NR = (64 * CR + 255) / 256;   // pieces a thread stages, of keys and of values
+    constexpr int SPREAD = 2 * D / RB;          // pieces of an LDS row that one becomes
     constexpr int KS = D / 16, DT = D / 32;
     __shared__ __attribute__((aligned(16))) char lds[4 * T::kTile];     // keys 0, keys 1, values 0, values 1
     __shared__ int any_odd;         // a drafted token's value is not finite
@@ -1208,8 +1261,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
         if (live) q[k] = signed_by(a.scale, load8(a.q + row * D + 16 * k + 8 * f));
     }
 
-    const int64_t item = FP8 ? 1 : 2;
-    const int64_t head_off = kvh * a.cache.head_stride * item;
+    const int64_t head_off = bytes_of<HELD>(kvh * a.cache.head_stride);
     const char* const kp = static_cast<const char*>(a.cache.k) + head_off;
     const char* const vp = static_cast<const char*>(a.cache.v) + head_off;
     const int32_t* const table = a.tables ? a.tables + (int64_t)s * a.n : nullptr;
@@ -1227,10 +1279,12 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
         const int tok = t + lane;
         const bool none = tok >= t1 || slot < 0 || slot >= a.N;
         nowhere = __ballot(none);
-        return none ? 0 : (slot * a.cache.block_stride + (int64_t)(tok - bs.block(tok) * bs.B) * a.cache.token_stride) * item;
+        return none ? 0 : bytes_of<HELD>(slot * a.cache.block_stride + (int64_t)(tok - bs.block(tok) * bs.B) * a.cache.token_stride);
     };
     const int my_tok = threadIdx.x / CR, my_piece = threadIdx.x % CR;     // and tokens 256 / CR further on
+    const bool mine_in = 256 / CR * NR <= 64 || my_tok < 64;     // (64 values in 4 bits: half of the threads have a piece)
     u32x4_t ks[NR], vs[NR];
+    uint32_t k_sc[NR], v_sc[NR];        // a piece's scale byte
     auto load_tile = [&](int64_t off) {
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
@@ -1239,21 +1293,34 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
                               16 * my_piece;
             ks[x] = *reinterpret_cast<const u32x4_t*>(kp + o);
             vs[x] = *reinterpret_cast<const u32x4_t*>(vp + o);
+            if constexpr (HELD == FP4) {
+                k_sc[x] = a.cache.k_scales[(head_off + o) >> 4];
+                v_sc[x] = a.cache.v_scales[(head_off + o) >> 4];
+            }
         }
     };
     // 256 / CR is a multiple of 16, so a thread's rows share their permutation and lie a fixed step apart
-    const int k_to = T::key(my_tok, FP8 ? 2 * my_piece : my_piece), v_to = T::value(my_tok, FP8 ? 2 * my_piece : my_piece);
+    const int k_to = T::key(my_tok, SPREAD * my_piece), v_to = T::value(my_tok, SPREAD * my_piece);
     auto store_tile = [&](int buf, int t, uint64_t nowhere) {
+        if (!mine_in) return;
         if (t + 64 > ctx || nowhere != 0) {
             bool odd = false;
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
                 const int tok = my_tok + 256 / CR * x;
                 const bool none = (nowhere >> tok) & 1, tail = t + tok >= ctx;
+                if constexpr (HELD == FP4) {
+                    const bool bad = v_sc[x] == 255u;
+                    odd |= bad && tail && !none;
+                    if (none || (bad && tail)) {
+                        vs[x] = u32x4_t{0, 0, 0, 0};
+                        v_sc[x] = 0;
+                    }
+                }
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
+                for (int y = 0; y < 4 && HELD != FP4; ++y) {
                     const uint32_t w = none ? 0u : vs[x][y];
-                    const uint32_t finite = FP8 ? finite_only_fp8(w) : finite_only(w);
+                    const uint32_t finite = HELD == FP8 ? finite_only_fp8(w) : finite_only(w);
                     odd |= tail && finite != w;
                     vs[x][y] = tail ? finite : w;
                 }
@@ -1265,7 +1332,14 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             constexpr int kStep = 256 / CR * T::kRow;
-            if constexpr (FP8) {
+            if constexpr (HELD == FP4) {
+                // the piece's quarters are pieces 4 p .. 4 p + 3: as below
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    *reinterpret_cast<u32x4_t*>(lds + buf * T::kTile + (k_to ^ (16 * y)) + x * kStep) = fp4x8_to_bf16(ks[x][y], k_sc[x]);
+                    *reinterpret_cast<u32x4_t*>(lds + (2 + buf) * T::kTile + (v_to ^ (16 * y)) + x * kStep) = fp4x8_to_bf16(vs[x][y], v_sc[x]);
+                }
+            } else if constexpr (HELD == FP8) {
                 // the piece's two halves are pieces 2 p and 2 p + 1: the permutation flips at most their last bit
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
@@ -1340,9 +1414,9 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
             int64_t off = 0;
             if (more) {
                 off = offset_of(t + 64, slot, nowhere_next);
-                direct = !FP8 && t + 128 <= ctx && nowhere_next == 0;
+                direct = HELD == BF16 && t + 128 <= ctx && nowhere_next == 0;
                 if (direct) direct_tile(buf ^ 1, off);
-                else if (FP8) load_tile(off);
+                else if (HELD != BF16) load_tile(off);
                 slot = entry_of(t + 128);
             }
             uint64_t wrong = nowhere;       // invalid entries: tokens past the run's end are none
@@ -1512,7 +1586,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
             if (direct) {
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // in LDS before the barrier
             } else if (more) {
-                if (!FP8) load_tile(off);
+                if (HELD == BF16) load_tile(off);
                 store_tile(buf ^ 1, t + 64, nowhere_next);
             }
             nowhere = nowhere_next;
@@ -1524,7 +1598,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
 
     l = sum_over_f(l);
     bool lost = false;
-    if constexpr (!FP8) {
+    if constexpr (HELD == BF16) {
         float x = 0.f;      // NaN where a sum is not finite
 #pragma unroll
         for (int d = 0; d < DT; ++d)
@@ -1542,10 +1616,10 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
             for (int v = 0; v < 16; ++v) sum[v] = 0.f;
             for (int tok = all || ctx < t0 ? t0 : ctx; tok < t1; ++tok) {
                 if (pairs && (tok - t0) / 32 % 2 != wave % 2) continue;         // the other wave's half
-                const char* const from = value_row(a, bs, s, kvh, tok, item);
+                const char* const from = value_row<HELD>(a, bs, s, kvh, tok);
                 if (from && (tok < ctx || ((seen >> ((tok - ctx) & 63)) & 1))) {
 #pragma unroll
-                    for (int v = 0; v < 16; v += 4) add_not_finite<FP8>(sum + v, from, 32 * d + 2 * v + 4 * f);
+                    for (int v = 0; v < 16; v += 4) add_not_finite<HELD>(sum + v, from, 32 * d + 2 * v + 4 * f);
                 }
             }
 #pragma unroll
@@ -1612,20 +1686,22 @@ constexpr int kRounds = 8;              // most workgroups a CU's places get one
 constexpr int kStreamQueries = 32;
 
 Kind kind_of(const AttendArgs& a) {
-    const int item = a.cache.fp8 ? 1 : 2;
+    const Held held = held_of(a.cache);
+    auto bytes = [held](int64_t x) { return held == FP4 ? bytes_of<FP4>(x) : (held == FP8 ? bytes_of<FP8>(x) : bytes_of<BF16>(x)); };
     if (a.D != 64 && a.D != 128) return Kind::Plain;
     // a block's sum is taken inside a tile, or over whole tiles
     if (a.block_lse && (!(a.B % 32 == 0 || a.B == 16 || a.B == 8) || a.B > 65536)) return Kind::Plain;
     // 16-byte loads
     if (!aligned_to(a.cache.k, 16) || !aligned_to(a.cache.v, 16) ||
-        ((a.cache.block_stride | a.cache.token_stride | a.cache.head_stride) * item) % 16 != 0)
+        bytes(a.cache.block_stride | a.cache.token_stride | a.cache.head_stride) % 16 != 0)
         return Kind::Plain;
     // the stream kernel's wave-loads take tokens of one block, all within 32-bit offsets of its first (the tree kernel
     // finds every token's place for itself, so it has the rest: 16 sequences of 8192 tokens of 64 e4m3 values in blocks
     // of 8 take 39 us with it, 2021 with the plain kernel)
-    const int tpl = 1024 / (a.D * item);
+    // a row of 64 values in 4 bits is 32 bytes, half of what the stream kernel's lane groups take
+    const int tpl = (int)(1024 / bytes(a.D));
     const bool fits = a.B % tpl == 0 && a.cache.token_stride <= (1 << 24) &&
-                      a.B * a.cache.token_stride * item <= 0x7FFFFFFF;
+                      bytes(a.B * a.cache.token_stride) <= 0x7FFFFFFF && !(held == FP4 && a.D == 64);
     return fits && queries_of(a) <= kStreamQueries ? Kind::Stream : Kind::Tree;
 }
 
@@ -1657,14 +1733,15 @@ size_t plan_bytes(const AttendArgs& a, const Plan& pl) {
     return may_split(a, pl) ? (size_t)(share_bytes(a.S) + most_items(a, pl) * pl.rows * (a.D + 2) * (int64_t)sizeof(float)) : 0;
 }
 
-template <int D, bool FP8>
+template <int D, Held HELD>
 void launch_fast(const AttendArgs& a, Kind kind, const Plan& pl, uint32_t grid, hipStream_t stream) {
     const BlockSize bs = block_size(a.B);
-    if (kind == Kind::Stream) attend_stream_kernel<D, FP8><<<grid, 256, 0, stream>>>(a, pl, bs);
-    else if (!a.block_lse) attend_tree_kernel<D, FP8, 0><<<grid, 256, 0, stream>>>(a, pl, bs);
-    else if (a.B == 8) attend_tree_kernel<D, FP8, 4><<<grid, 256, 0, stream>>>(a, pl, bs);
-    else if (a.B == 16) attend_tree_kernel<D, FP8, 2><<<grid, 256, 0, stream>>>(a, pl, bs);
-    else attend_tree_kernel<D, FP8, 1><<<grid, 256, 0, stream>>>(a, pl, bs);
+    if (kind == Kind::Stream) {
+        if constexpr (HELD != FP4 || D == 128) attend_stream_kernel<D, HELD><<<grid, 256, 0, stream>>>(a, pl, bs);
+    } else if (!a.block_lse) attend_tree_kernel<D, HELD, 0><<<grid, 256, 0, stream>>>(a, pl, bs);
+    else if (a.B == 8) attend_tree_kernel<D, HELD, 4><<<grid, 256, 0, stream>>>(a, pl, bs);
+    else if (a.B == 16) attend_tree_kernel<D, HELD, 2><<<grid, 256, 0, stream>>>(a, pl, bs);
+    else attend_tree_kernel<D, HELD, 1><<<grid, 256, 0, stream>>>(a, pl, bs);
 }
 
 // A workgroup for a row where a sequence has runs enough for its four waves,
@@ -1699,8 +1776,10 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     const uint32_t row_grid = (uint32_t)(rows * a.Hq);
     const Kind kind = kind_of(a);
     if (kind == Kind::Plain) {
-        if (a.cache.fp8) attend_plain_kernel<true><<<row_grid, 256, 0, stream>>>(a);
-        else attend_plain_kernel<false><<<row_grid, 256, 0, stream>>>(a);
+        const Held held = held_of(a.cache);
+        if (held == FP4) attend_plain_kernel<FP4><<<row_grid, 256, 0, stream>>>(a);
+        else if (held == FP8) attend_plain_kernel<FP8><<<row_grid, 256, 0, stream>>>(a);
+        else attend_plain_kernel<BF16><<<row_grid, 256, 0, stream>>>(a);
         return hipGetLastError();
     }
     const Plan pl = plan_of(a, kind == Kind::Tree);
@@ -1710,10 +1789,14 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     // an XCD's items are numbered from the whole's eighth, rounded up
     const int64_t grid = (most_items(a, pl) + 7) / 8 * 8;
     if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
-    if (a.D == 64 && a.cache.fp8) launch_fast<64, true>(b, kind, pl, (uint32_t)grid, stream);
-    else if (a.D == 64) launch_fast<64, false>(b, kind, pl, (uint32_t)grid, stream);
-    else if (a.cache.fp8) launch_fast<128, true>(b, kind, pl, (uint32_t)grid, stream);
-    else launch_fast<128, false>(b, kind, pl, (uint32_t)grid, stream);
+    auto launch = [&](auto held) {
+        if (a.D == 64) launch_fast<64, decltype(held)::value>(b, kind, pl, (uint32_t)grid, stream);
+        else launch_fast<128, decltype(held)::value>(b, kind, pl, (uint32_t)grid, stream);
+    };
+    const Held held = held_of(a.cache);
+    if (held == FP4) launch(std::integral_constant<Held, FP4>());
+    else if (held == FP8) launch(std::integral_constant<Held, FP8>());
+    else launch(std::integral_constant<Held, BF16>());
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !split) return e;
     if (a.D == 64) launch_join<64>(b, pl, row_grid, stream);

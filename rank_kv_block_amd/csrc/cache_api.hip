@@ -28,9 +28,21 @@ int check_handle(pred_t* p, const char* what) {
 
 int check_cache(pred_t* p, const pred_kv_cache* c, pred::CacheView* out, const char* what) {
     if (!c || !c->k || !c->v) return fail(PRED_ERR_NULL_ARG, "%s: cache, its k or its v is NULL", what);
-    if (c->dtype != PRED_KV_BF16 && c->dtype != PRED_KV_FP8)
-        return fail(PRED_ERR_UNSUPPORTED, "%s: cache dtype %d is not PRED_KV_BF16 or PRED_KV_FP8", what, c->dtype);
+    if (c->dtype != PRED_KV_BF16 && c->dtype != PRED_KV_FP8 && c->dtype != PRED_KV_FP4)
+        return fail(PRED_ERR_UNSUPPORTED, "%s: cache dtype %d is not PRED_KV_BF16, PRED_KV_FP8 or PRED_KV_FP4", what,
+                    c->dtype);
     const pred_dims& d = p->d;
+    const bool fp4 = c->dtype == PRED_KV_FP4;
+    if (fp4 && (!c->k_scales || !c->v_scales))
+        return fail(PRED_ERR_NULL_ARG, "%s: a 4-bit cache's k_scales or v_scales is NULL", what);
+    if (fp4 && d.head_dim % 32 != 0)
+        return fail(PRED_ERR_UNSUPPORTED, "%s: a 4-bit cache needs a head_dim (%d) that is a multiple of 32", what,
+                    d.head_dim);
+    if (fp4 && ((c->block_stride | c->token_stride | c->head_stride) & 31 || !pred::aligned16(c->k) ||
+                !pred::aligned16(c->v)))
+        return fail(PRED_ERR_UNSUPPORTED, "%s: a 4-bit cache's strides (%lld, %lld, %lld) must be multiples of 32 "
+                    "elements and its k, v 16-byte aligned", what, (long long)c->block_stride,
+                    (long long)c->token_stride, (long long)c->head_stride);
     const int64_t bs = c->block_stride, ts = c->token_stride, hs = c->head_stride;
     if ((bs | ts | hs) & 7 || !pred::aligned_to(c->k, c->dtype == PRED_KV_FP8 ? 8 : 16) ||
         !pred::aligned_to(c->v, c->dtype == PRED_KV_FP8 ? 8 : 16))
@@ -51,9 +63,10 @@ int check_cache(pred_t* p, const pred_kv_cache* c, pred::CacheView* out, const c
                     "overlap", what, (long long)ts, (long long)hs);
     if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f) || std::isinf(c->k_scale) || std::isinf(c->v_scale))
         return fail(PRED_ERR_OUT_OF_RANGE, "%s: cache scales must be positive and finite", what);
-    if (c->dtype == PRED_KV_BF16 && (c->k_scale != 1.f || c->v_scale != 1.f))
-        return fail(PRED_ERR_UNSUPPORTED, "%s: a bf16 cache has scales of 1", what);
-    *out = pred::CacheView{c->k, c->v, bs, ts, hs, c->dtype == PRED_KV_FP8, c->k_scale, c->v_scale};
+    if (c->dtype != PRED_KV_FP8 && (c->k_scale != 1.f || c->v_scale != 1.f))
+        return fail(PRED_ERR_UNSUPPORTED, "%s: a bf16 or 4-bit cache has k_scale and v_scale of 1", what);
+    *out = pred::CacheView{c->k, c->v, bs, ts, hs, c->dtype == PRED_KV_FP8, c->k_scale, c->v_scale, fp4,
+                           fp4 ? c->k_scales : nullptr, fp4 ? c->v_scales : nullptr};
     return PRED_OK;
 }
 
@@ -79,20 +92,52 @@ int check_rows(pred_t* p, const void* x, int64_t stride, int64_t heads, const ch
     return PRED_OK;
 }
 
+// r NULL: nothing turns.
 pred::RopeArgs rope_args(pred_t* p, const pred_rope* r, const int32_t* positions, int64_t n_tokens) {
     pred::RopeArgs a{};
-    a.turns = r->turns;
-    a.rot = r->rot_dim;
-    a.interleaved = r->interleaved != 0;
-    a.backward = r->backward != 0;
-    a.mscale = r->mscale;
-    a.positions = positions;
+    if (r) {
+        a.turns = r->turns;
+        a.rot = r->rot_dim;
+        a.interleaved = r->interleaved != 0;
+        a.backward = r->backward != 0;
+        a.mscale = r->mscale;
+        a.positions = positions;
+    }
     a.n_tokens = n_tokens;
     a.D = p->d.head_dim;
     a.N = p->d.max_blocks;
     a.B = p->d.block_size;
     a.err = p->err_dev;
     return a;
+}
+
+// A cache that a call writes: k and v, and their scales, at places of their own.
+int check_store(const pred_kv_cache* c, const char* what) {
+    if (c->k == c->v) return fail(PRED_ERR_OUT_OF_RANGE, "%s: the cache's k and v are one", what);
+    if (c->dtype == PRED_KV_FP4 && c->k_scales == c->v_scales)
+        return fail(PRED_ERR_OUT_OF_RANGE, "%s: the cache's k_scales and v_scales are one", what);
+    return PRED_OK;
+}
+
+// n NULL: no norm.
+int check_norm(pred_t* p, const pred_norm* n, pred::HeadNorm* out, const char* what) {
+    *out = pred::HeadNorm{};
+    if (p->d.head_dim > 512) return fail(PRED_ERR_UNSUPPORTED, "%s: head_dim (%d) above 512", what, p->d.head_dim);
+    if (!n) return PRED_OK;
+    if (!(n->eps > 0.f) || std::isinf(n->eps) || !std::isfinite(n->offset))
+        return fail(PRED_ERR_OUT_OF_RANGE, "%s: a norm's eps must be above 0 and finite, its offset finite", what);
+    if (!pred::aligned16(n->weight))
+        return fail(PRED_ERR_UNSUPPORTED, "%s: a norm's weight must be 16-byte aligned", what);
+    *out = pred::HeadNorm{n->weight, 1, n->eps, n->offset};
+    return PRED_OK;
+}
+
+// A rotation of the calls that may do without (NULL) and run forwards only.
+int check_forward_rope(pred_t* p, const pred_rope* r, const char* what) {
+    if (!r) return PRED_OK;
+    const int rc = check_rope(p, r, what);
+    if (rc == 0 && r->backward) return fail(PRED_ERR_UNSUPPORTED, "%s: rope->backward must be 0", what);
+    return rc;
 }
 
 // Tokens of a sequence: with 2^29 no sum of lengths, runs and tiles passes 32 bits.
@@ -137,6 +182,66 @@ pred::AttendArgs attend_shape(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t
 bool attend_counts_ok(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_blocks) {
     return n_seqs >= 1 && n_rows >= 1 && n_rows <= 64 && n_blocks >= 1 &&
            n_blocks <= kMostTokens / p->d.block_size;
+}
+
+int check_heads(int64_t n_tokens, int32_t n_heads, const char* what) {
+    if (n_tokens < 0 || n_heads < 0 || n_heads > 65536)
+        return fail(PRED_ERR_OUT_OF_RANGE, "%s: n_tokens (%lld) < 0 or n_heads (%d) outside [0, 65536]", what,
+                    (long long)n_tokens, n_heads);
+    return PRED_OK;
+}
+
+int check_in_place(const void* x, int64_t x_stride, const void* out, int64_t out_stride, const char* what,
+                   const char* x_name, const char* out_name) {
+    if (x == out && x_stride != out_stride)
+        return fail(PRED_ERR_OUT_OF_RANGE, "%s: in place, %s and %s need one stride (%lld, %lld)", what, x_name,
+                    out_name, (long long)x_stride, (long long)out_stride);
+    return PRED_OK;
+}
+
+// New tokens into a cache: queries (unless `queries` is false) and keys normed
+// where a norm is on, turned where rope is not NULL.
+int store_rows(pred_t* p, const pred::HeadNorm& q_norm, const pred::HeadNorm& k_norm, const pred_rope* rope,
+               const pred_bf16* q, int64_t q_stride, const pred_bf16* k, int64_t k_stride, const pred_bf16* v,
+               int64_t v_stride, int64_t n_tokens, const int32_t* positions, const int64_t* slots,
+               const pred_kv_cache* cache, pred_bf16* q_out, void* stream, bool queries, const char* what) {
+    pred::CacheView view;
+    int rc = check_cache(p, cache, &view, what);
+    if (rc == 0) rc = check_store(cache, what);
+    if (rc) return rc;
+    if (n_tokens < 0) return fail(PRED_ERR_OUT_OF_RANGE, "%s: n_tokens (%lld) < 0", what, (long long)n_tokens);
+    if (n_tokens == 0) return ok();
+    if ((rope && !positions) || !slots) return fail(PRED_ERR_NULL_ARG, "%s: positions or slots is NULL", what);
+    const pred_dims& d = p->d;
+    const int64_t out_stride = (int64_t)d.num_q_heads * d.head_dim;
+    if (queries && (rc = check_rows(p, q, q_stride, d.num_q_heads, what, "q"))) return rc;
+    if ((rc = check_rows(p, k, k_stride, d.num_kv_heads, what, "k"))) return rc;
+    if ((rc = check_rows(p, v, v_stride, d.num_kv_heads, what, "v"))) return rc;
+    if (queries && (rc = check_rows(p, q_out, out_stride, d.num_q_heads, what, "q_out"))) return rc;
+    if (queries && q == q_out && q_stride != out_stride)
+        return fail(PRED_ERR_OUT_OF_RANGE, "%s: in place, q's stride (%lld) must be %lld", what, (long long)q_stride,
+                    (long long)out_stride);
+    if (d.num_q_heads > 65536 || d.num_kv_heads > 65536)
+        return fail(PRED_ERR_UNSUPPORTED, "%s: more than 65536 heads", what);
+    pred::NormArgs a{rope_args(p, rope, positions, n_tokens), q_norm, k_norm};
+    a.rows.q = q;
+    a.rows.k = k;
+    a.rows.v = v;
+    a.rows.out = q_out;
+    a.rows.q_stride = q_stride;
+    a.rows.k_stride = k_stride;
+    a.rows.v_stride = v_stride;
+    a.rows.out_stride = out_stride;
+    a.rows.Hq = queries ? d.num_q_heads : 0;
+    a.rows.Hk = d.num_kv_heads;
+    a.rows.slots = slots;
+    a.rows.cache = view;
+    // rope.hip's kernels turn two pieces a lane and keep a cosine for both; they have no norms and no 4-bit rows
+    const bool plain = rope && !q_norm.on && !k_norm.on && !view.fp4;
+    const hipError_t e = plain ? pred::launch_rotate(a.rows, (hipStream_t)stream)
+                               : pred::launch_norm_rotate(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, what);
+    return ok();
 }
 
 }  // namespace
@@ -200,16 +305,12 @@ int pred_rotate(pred_t* p, const pred_rope* rope, const pred_bf16* x, int64_t x_
     int rc = check_handle(p, "rotate");
     if (rc == 0) rc = check_rope(p, rope, "rotate");
     if (rc) return rc;
-    if (n_tokens < 0 || n_heads < 0 || n_heads > 65536)
-        return fail(PRED_ERR_OUT_OF_RANGE, "rotate: n_tokens (%lld) < 0 or n_heads (%d) outside [0, 65536]",
-                    (long long)n_tokens, n_heads);
+    if ((rc = check_heads(n_tokens, n_heads, "rotate"))) return rc;
     if (n_tokens == 0 || n_heads == 0) return ok();
     if (!positions) return fail(PRED_ERR_NULL_ARG, "rotate: positions is NULL");
     if ((rc = check_rows(p, x, x_stride, n_heads, "rotate", "x"))) return rc;
     if ((rc = check_rows(p, out, out_stride, n_heads, "rotate", "out"))) return rc;
-    if (x == out && x_stride != out_stride)
-        return fail(PRED_ERR_OUT_OF_RANGE, "rotate: in place, x and out need one stride (%lld, %lld)",
-                    (long long)x_stride, (long long)out_stride);
+    if ((rc = check_in_place(x, x_stride, out, out_stride, "rotate", "x", "out"))) return rc;
     pred::RopeArgs a = rope_args(p, rope, positions, n_tokens);
     a.q = x;
     a.out = out;
@@ -229,38 +330,139 @@ int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int6
     if (rc == 0) rc = check_rope(p, rope, "rotate_store");
     if (rc) return rc;
     if (rope->backward) return fail(PRED_ERR_UNSUPPORTED, "rotate_store: rope->backward must be 0");
+    return store_rows(p, pred::HeadNorm{}, pred::HeadNorm{}, rope, q, q_stride, k, k_stride, v, v_stride, n_tokens,
+                      positions, slots, cache, q_out, stream, true, "rotate_store");
+}
+
+int pred_norm_rotate_store(pred_t* p, const pred_norm* q_norm, const pred_norm* k_norm, const pred_rope* rope,
+                           const pred_bf16* q, int64_t q_stride, const pred_bf16* k, int64_t k_stride,
+                           const pred_bf16* v, int64_t v_stride, int64_t n_tokens, const int32_t* positions,
+                           const int64_t* slots, const pred_kv_cache* cache, pred_bf16* q_out, void* stream) {
+    const char* const what = "norm_rotate_store";
+    pred::HeadNorm qn, kn;
+    int rc = check_handle(p, what);
+    if (rc == 0) rc = check_norm(p, q_norm, &qn, what);
+    if (rc == 0) rc = check_norm(p, k_norm, &kn, what);
+    if (rc == 0) rc = check_forward_rope(p, rope, what);
+    if (rc) return rc;
+    return store_rows(p, qn, kn, rope, q, q_stride, k, k_stride, v, v_stride, n_tokens, positions, slots, cache, q_out,
+                      stream, true, what);
+}
+
+int pred_store(pred_t* p, const pred_bf16* k, int64_t k_stride, const pred_bf16* v, int64_t v_stride, int64_t n_tokens,
+               const int64_t* slots, const pred_kv_cache* cache, void* stream) {
+    pred::HeadNorm none;
+    int rc = check_handle(p, "store");
+    if (rc == 0) rc = check_norm(p, nullptr, &none, "store");
+    if (rc) return rc;
+    return store_rows(p, none, none, nullptr, nullptr, 0, k, k_stride, v, v_stride, n_tokens, nullptr, slots, cache,
+                      nullptr, stream, false, "store");
+}
+
+int pred_load(pred_t* p, const pred_kv_cache* cache, int64_t n_tokens, const int64_t* slots, pred_bf16* k_out,
+              pred_bf16* v_out, void* stream) {
+    int rc = check_handle(p, "load");
+    if (rc) return rc;
     pred::CacheView view;
-    if ((rc = check_cache(p, cache, &view, "rotate_store"))) return rc;
-    if (cache->k == cache->v) return fail(PRED_ERR_OUT_OF_RANGE, "rotate_store: the cache's k and v are one");
-    if (n_tokens < 0) return fail(PRED_ERR_OUT_OF_RANGE, "rotate_store: n_tokens (%lld) < 0", (long long)n_tokens);
+    if ((rc = check_cache(p, cache, &view, "load"))) return rc;
+    if (n_tokens < 0) return fail(PRED_ERR_OUT_OF_RANGE, "load: n_tokens (%lld) < 0", (long long)n_tokens);
     if (n_tokens == 0) return ok();
-    if (!positions || !slots) return fail(PRED_ERR_NULL_ARG, "rotate_store: positions or slots is NULL");
+    if (!slots) return fail(PRED_ERR_NULL_ARG, "load: slots is NULL");
     const pred_dims& d = p->d;
-    const int64_t out_stride = (int64_t)d.num_q_heads * d.head_dim;
-    if ((rc = check_rows(p, q, q_stride, d.num_q_heads, "rotate_store", "q"))) return rc;
-    if ((rc = check_rows(p, k, k_stride, d.num_kv_heads, "rotate_store", "k"))) return rc;
-    if ((rc = check_rows(p, v, v_stride, d.num_kv_heads, "rotate_store", "v"))) return rc;
-    if ((rc = check_rows(p, q_out, out_stride, d.num_q_heads, "rotate_store", "q_out"))) return rc;
-    if (q == q_out && q_stride != out_stride)
-        return fail(PRED_ERR_OUT_OF_RANGE, "rotate_store: in place, q's stride (%lld) must be %lld",
-                    (long long)q_stride, (long long)out_stride);
-    if (d.num_q_heads > 65536 || d.num_kv_heads > 65536)
-        return fail(PRED_ERR_UNSUPPORTED, "rotate_store: more than 65536 heads");
-    pred::RopeArgs a = rope_args(p, rope, positions, n_tokens);
-    a.q = q;
-    a.k = k;
-    a.v = v;
-    a.out = q_out;
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.out_stride = out_stride;
-    a.Hq = d.num_q_heads;
-    a.Hk = d.num_kv_heads;
-    a.slots = slots;
+    const int64_t out_stride = (int64_t)d.num_kv_heads * d.head_dim;
+    if ((rc = check_rows(p, k_out, out_stride, d.num_kv_heads, "load", "k_out"))) return rc;
+    if ((rc = check_rows(p, v_out, out_stride, d.num_kv_heads, "load", "v_out"))) return rc;
+    pred::LoadArgs a{};
     a.cache = view;
-    const hipError_t e = pred::launch_rotate(a, (hipStream_t)stream);
-    if (e != hipSuccess) return hip_fail(e, "rotate_store launch");
+    a.slots = slots;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.err = p->err_dev;
+    a.n_tokens = n_tokens;
+    a.N = d.max_blocks;
+    a.Hk = d.num_kv_heads;
+    a.D = d.head_dim;
+    a.B = d.block_size;
+    const hipError_t e = pred::launch_load(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "load launch");
+    return ok();
+}
+
+int pred_norm_rotate(pred_t* p, const pred_norm* norm, const pred_rope* rope, const pred_bf16* x, int64_t x_stride,
+                     int64_t n_tokens, int32_t n_heads, const int32_t* positions, pred_bf16* out, int64_t out_stride,
+                     void* stream) {
+    const char* const what = "norm_rotate";
+    pred::NormArgs a{};
+    int rc = check_handle(p, what);
+    if (rc == 0 && !norm) rc = fail(PRED_ERR_NULL_ARG, "%s: norm is NULL", what);
+    if (rc == 0) rc = check_norm(p, norm, &a.q, what);
+    if (rc == 0) rc = check_forward_rope(p, rope, what);
+    if (rc == 0) rc = check_heads(n_tokens, n_heads, what);
+    if (rc) return rc;
+    if (n_tokens == 0 || n_heads == 0) return ok();
+    if (rope && !positions) return fail(PRED_ERR_NULL_ARG, "%s: positions is NULL", what);
+    if ((rc = check_rows(p, x, x_stride, n_heads, what, "x")) ||
+        (rc = check_rows(p, out, out_stride, n_heads, what, "out")) ||
+        (rc = check_in_place(x, x_stride, out, out_stride, what, "x", "out")))
+        return rc;
+    a.rows = rope_args(p, rope, positions, n_tokens);
+    a.rows.q = x;
+    a.rows.out = out;
+    a.rows.q_stride = x_stride;
+    a.rows.out_stride = out_stride;
+    a.rows.Hq = n_heads;
+    const hipError_t e = pred::launch_norm_rotate(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "norm_rotate launch");
+    return ok();
+}
+
+size_t pred_norm_rotate_workspace_bytes(pred_t* p, int64_t n_tokens, int32_t n_heads) {
+    if (!p || n_tokens < 1 || n_heads < 1 || n_heads > 65536 || p->d.head_dim > 512) return 0;
+    return (size_t)pred::norm_grad_parts(n_tokens, n_heads, p->d.head_dim) * p->d.head_dim * sizeof(float);
+}
+
+int pred_norm_rotate_backward(pred_t* p, const pred_norm* norm, const pred_rope* rope, const pred_bf16* x,
+                              int64_t x_stride, int64_t n_tokens, int32_t n_heads, const int32_t* positions,
+                              const pred_bf16* dy, int64_t dy_stride, pred_bf16* dx, int64_t dx_stride, float* dweight,
+                              void* workspace, size_t ws_bytes, void* stream) {
+    const char* const what = "norm_rotate_backward";
+    pred::NormGradArgs a{};
+    int rc = check_handle(p, what);
+    if (rc == 0 && !norm) rc = fail(PRED_ERR_NULL_ARG, "%s: norm is NULL", what);
+    if (rc == 0) rc = check_norm(p, norm, &a.norm, what);
+    if (rc == 0) rc = check_forward_rope(p, rope, what);
+    if (rc == 0) rc = check_heads(n_tokens, n_heads, what);
+    if (rc) return rc;
+    const bool none = n_tokens == 0 || n_heads == 0;
+    if (none && !dweight) return ok();
+    if (!none) {
+        if (rope && !positions) return fail(PRED_ERR_NULL_ARG, "%s: positions is NULL", what);
+        if ((rc = check_rows(p, x, x_stride, n_heads, what, "x")) ||
+            (rc = check_rows(p, dy, dy_stride, n_heads, what, "dy")) ||
+            (rc = check_rows(p, dx, dx_stride, n_heads, what, "dx")) ||
+            (rc = check_in_place(x, x_stride, dx, dx_stride, what, "x", "dx")) ||
+            (rc = check_in_place(dy, dy_stride, dx, dx_stride, what, "dy", "dx")))
+            return rc;
+        const size_t need = dweight ? pred_norm_rotate_workspace_bytes(p, n_tokens, n_heads) : 0;
+        if (need > 0 && (!workspace || ws_bytes < need))
+            return fail(PRED_ERR_WORKSPACE, "%s needs a %zu-byte workspace (%zu given)", what, need,
+                        workspace ? ws_bytes : (size_t)0);
+        if (need > 0 && !pred::aligned16(workspace))
+            return fail(PRED_ERR_WORKSPACE, "%s: the workspace must be 16-byte aligned", what);
+    }
+    a.rows = rope_args(p, rope, positions, none ? 0 : n_tokens);
+    a.rows.backward = 1;
+    a.rows.q = x;
+    a.rows.q_stride = x_stride;
+    a.rows.out = dx;
+    a.rows.out_stride = dx_stride;
+    a.rows.Hq = n_heads;
+    a.dy = dy;
+    a.dy_stride = dy_stride;
+    a.dweight = dweight;
+    a.part = static_cast<float*>(workspace);
+    const hipError_t e = pred::launch_norm_rotate_backward(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "norm_rotate_backward launch");
     return ok();
 }
 

@@ -120,13 +120,18 @@ hipError_t launch_rank(const float* scores, int64_t n, int64_t n_seg, int64_t k,
                        void* ws, hipStream_t stream);
 
 // ---- the paged KV cache (rope.hip, attend.hip, evict.hip) -------------------
-// One layer's cache: element strides; fp8 is 8-bit e4m3 (else bf16).
+// One layer's cache: element strides; 8-bit e4m3 if fp8, 4-bit e2m1 if fp4 (the
+// element at offset x is nibble x % 2 of byte x / 2, its scale byte x / 32 of the
+// scales), else bf16.
 struct CacheView {
     void* k;
     void* v;
     int64_t block_stride, token_stride, head_stride;
     int fp8;
     float k_scale, v_scale;
+    int fp4;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
 };
 
 // A rotation: turns[i] = turns per position of pair i as a 64-bit fraction.
@@ -155,6 +160,43 @@ struct RopeArgs {
     uint32_t* err;
 };
 hipError_t launch_rotate(const RopeArgs& a, hipStream_t stream);
+
+// Rows normed, turned and stored (norm.hip).  rows.rot 0: nothing turns; rows.Hq
+// 0: no queries; rows.Hk 0: no keys and values.
+struct HeadNorm {
+    const uint16_t* weight;     // [D] or null (ones)
+    int on;
+    float eps, offset;
+};
+struct NormArgs {
+    RopeArgs rows;
+    HeadNorm q, k;
+};
+hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t stream);
+
+// The gradient: dy of `rows.q` normed and turned -> dx, and dweight [D] or null.
+struct NormGradArgs {
+    RopeArgs rows;              // q: x; out: dx; backward set
+    HeadNorm norm;
+    const uint16_t* dy;
+    int64_t dy_stride;
+    float* dweight;
+    float* part;                // [norm_grad_parts, D]
+};
+int64_t norm_grad_parts(int64_t n_tokens, int n_heads, int D);
+hipError_t launch_norm_rotate_backward(const NormGradArgs& a, hipStream_t stream);
+
+// Cached tokens back to bf16 [n_tokens, Hk, D].
+struct LoadArgs {
+    CacheView cache;
+    const int64_t* slots;
+    uint16_t* k_out;
+    uint16_t* v_out;
+    uint32_t* err;
+    int64_t n_tokens, N;
+    int Hk, D, B;
+};
+hipError_t launch_load(const LoadArgs& a, hipStream_t stream);
 
 struct AttendArgs {
     CacheView cache;
