@@ -563,6 +563,36 @@ size_t pred_attend_workspace_bytes(pred_t* p, int32_t n_seqs, int32_t n_rows, in
  * pred_attend refuses. */
 const char* pred_attend_kernel_name(pred_t* p, const pred_kv_cache* cache, int32_t n_rows, int32_t with_block_lse);
 
+/* Attention of each sequence's newest tokens with a sliding window: any number
+ * of rows (a decode step's, a chain of drafted tokens, a prompt chunk, a whole
+ * prompt).  With d = row_len, row i < d is token p = kv_len - d + i and sees the
+ * `window` newest tokens up to itself, p - window + 1 .. p, and the sequence's first
+ * n_sinks up to itself; window INT32_MAX hides nothing.
+ *   n_rows    [1, 2^24]
+ *   row_len   device, [n_seqs] int32 in [0, min(n_rows, kv_len)], or NULL for that upper limit
+ *   window    >= 1;  n_sinks >= 0
+ * The other arguments, and what is said of rows past row_len, of masked tokens,
+ * of values that are not finite and of lengths and entries out of range, are
+ * pred_attend's.  Entries of blocks of which no row sees a token need not be
+ * valid: those blocks may have been given back.  With more than 16 queries per
+ * kv head (n_rows * num_q_heads / num_kv_heads) a weight enters its product with
+ * a value as one bf16 term. */
+int pred_attend_window(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32_t n_rows,
+                       const int32_t* block_tables, int64_t n_blocks, int32_t n_seqs, const int32_t* kv_len,
+                       const int32_t* row_len, int32_t window, int32_t n_sinks, float scale, pred_bf16* out, float* lse,
+                       void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace of pred_attend_window for this shape on this handle; 0 for a NULL
+ * handle or arguments that the call refuses.  Calls that may run at the same time
+ * need workspaces of their own. */
+size_t pred_attend_window_workspace_bytes(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_blocks, int32_t window,
+                                          int32_t n_sinks);
+
+/* As pred_attend_kernel_name: "attend_stream_kernel" (up to 16 queries per kv
+ * head, the caches it takes there), "attend_chunk_kernel" (the others, head sizes
+ * 64 and 128) or "attend_plain_kernel". */
+const char* pred_attend_window_kernel_name(pred_t* p, const pred_kv_cache* cache, int32_t n_rows);
+
 /* Accumulated attention weight of each block, from pred_attend's lse and
  * block_lse:
  *   mass_out[s, b] = decay * mass[s, b] + sum over accepted rows i, heads h of

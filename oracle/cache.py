@@ -215,6 +215,6 @@ def seen_in_window(rows, length, count, window, sinks):
     see = np.zeros((rows, length), bool)
     for i in range(min(rows, count)):
         pos = length - count + i
-        for t in range(pos + 1):
-            see[i, t] = pos - t < window or t < sinks
+        see[i, max(0, pos - window + 1):pos + 1] = True
+        see[i, :min(sinks, pos + 1)] = True
     return see

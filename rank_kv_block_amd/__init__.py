@@ -324,6 +324,7 @@ def pred_decode_step(h, layer0, k_new, new_table, q, q_proj, block_tables, last_
 # ------------------------------------------------------------------ the paged KV cache
 
 from .cache import (KVCache, Norm, Rope, pred_accumulate_weight, pred_attend, pred_attend_kernel_name,  # noqa: E402,F401
+                    pred_attend_window, pred_attend_window_kernel_name, pred_attend_window_workspace_bytes,
                     pred_attend_workspace_bytes, pred_evict_blocks, pred_evict_workspace_bytes, pred_load,
                     pred_norm_rotate, pred_norm_rotate_backward, pred_norm_rotate_store,
                     pred_norm_rotate_workspace_bytes, pred_rope_turns, pred_rotate, pred_rotate_store, pred_store)

@@ -162,6 +162,10 @@ SIGNATURES = {
     "pred_load": (ctypes.c_int, [_vp, _PC, _i64, _vp, _vp, _vp, _vp]),
     "pred_attend": (ctypes.c_int, [_vp, _PC, _vp, _i32, _vp, _vp, _i64, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _sz,
                                    _vp]),
+    "pred_attend_window": (ctypes.c_int, [_vp, _PC, _vp, _i32, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _f32, _vp, _vp, _vp,
+                                          _sz, _vp]),
+    "pred_attend_window_workspace_bytes": (_sz, [_vp, _i32, _i32, _i64, _i32, _i32]),
+    "pred_attend_window_kernel_name": (ctypes.c_char_p, [_vp, _PC, _i32]),
     "pred_attend_workspace_bytes": (_sz, [_vp, _i32, _i32, _i64]),
     "pred_attend_kernel_name": (ctypes.c_char_p, [_vp, _PC, _i32, _i32]),
     "pred_accumulate_weight": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _i64, _i32, _f32, _vp, _vp, _vp]),

@@ -21,7 +21,7 @@ COMMON = [
     "-I", INCLUDE, "-I", CSRC,
 ]
 SOURCES = ["pred_api.hip", "proj.hip", "score_decode.hip", "score_prefill.hip", "score_rows.hip", "rank.hip",
-           "cache_api.hip", "rope.hip", "norm.hip", "attend.hip", "evict.hip", "prng.cpp"]
+           "cache_api.hip", "rope.hip", "norm.hip", "attend.hip", "window.hip", "evict.hip", "prng.cpp"]
 # the projection generator must be plain IEEE float64 arithmetic, one operation at a time
 EXTRA = {
     "prng.cpp": ["-ffp-contract=off", "-fno-fast-math"],
@@ -76,6 +76,7 @@ _SAN = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefine
 def _newest_input(src):
     paths = [os.path.join(CSRC, src), os.path.join(INCLUDE, "pred.h"), os.path.join(CSRC, "common.h"),
              os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "handle.h"), os.path.join(CSRC, "rope.h"),
+             os.path.join(CSRC, "attend.h"),
              os.path.abspath(__file__)]
     return max(os.path.getmtime(q) for q in paths)
 

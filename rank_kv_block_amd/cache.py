@@ -345,7 +345,10 @@ def pred_attend_workspace_bytes(h, n_seqs, n_rows, n_blocks):
 
 def pred_attend_kernel_name(h, cache, n_rows=1, with_block_lse=False):
     """The kernel pred_attend runs for this handle, cache and rows per sequence."""
-    name = _lib.load().pred_attend_kernel_name(h, cache._ref, n_rows, bool(with_block_lse))
+    return _name(h, _lib.load().pred_attend_kernel_name(h, cache._ref, n_rows, bool(with_block_lse)))
+
+
+def _name(h, name):
     if name is None:
         rk = _pkg()
         raise rk.PredError(rk.PRED_ERR_NULL_ARG if not h else rk.PRED_ERR_OUT_OF_RANGE, rk.pred_last_error())
@@ -362,14 +365,7 @@ def pred_attend(h, cache, q, tree, block_tables, kv_len, draft_len, scale, out, 
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise TypeError("q: expected a tensor [n_seqs, n_rows, num_q_heads, head_dim]")
     S, M = q.shape[0], q.shape[1]
-    if block_tables is not None:
-        if not isinstance(block_tables, torch.Tensor):
-            raise TypeError("block_tables: expected a torch.Tensor")
-        if block_tables.dim() != 2:
-            raise ValueError("block_tables must be [n_seqs, n_blocks]")
-        n_blocks = block_tables.shape[1]
-    elif n_blocks is None:
-        n_blocks = d.max_blocks
+    n_blocks = _blocks_of(d, block_tables, n_blocks)
     shape = (S, M, d.num_q_heads, d.head_dim)
     ws, ws_bytes = a.buffer(workspace, "workspace")
     _check(_lib.load().pred_attend(
@@ -378,6 +374,44 @@ def pred_attend(h, cache, q, tree, block_tables, kv_len, draft_len, scale, out, 
         a.ptr(draft_len, "draft_len", _I32, (S,)), scale, a.ptr(out, "out", _BF16, shape),
         a.ptr(lse, "lse", _F32, shape[:3]), a.ptr(block_lse, "block_lse", _F32, (S, n_blocks, M, d.num_q_heads)),
         ws, ws_bytes, _raw_stream(stream, a.device)))
+
+
+def _blocks_of(d, block_tables, n_blocks):
+    """The blocks of a sequence: the table's, or those asked for (default: all of the cache's)."""
+    if block_tables is None:
+        return d.max_blocks if n_blocks is None else n_blocks
+    if not isinstance(block_tables, torch.Tensor):
+        raise TypeError("block_tables: expected a torch.Tensor")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [n_seqs, n_blocks]")
+    return block_tables.shape[1]
+
+
+def pred_attend_window_workspace_bytes(h, n_seqs, n_rows, n_blocks, window, n_sinks):
+    return _lib.load().pred_attend_window_workspace_bytes(h, n_seqs, n_rows, n_blocks, window, n_sinks)
+
+
+def pred_attend_window_kernel_name(h, cache, n_rows=1):
+    """The kernel pred_attend_window runs for this handle, cache and rows per sequence."""
+    return _name(h, _lib.load().pred_attend_window_kernel_name(h, cache._ref, n_rows))
+
+
+def pred_attend_window(h, cache, q, block_tables, kv_len, row_len, window, n_sinks, scale, out, lse=None, workspace=None,
+                       n_blocks=None, stream=None):
+    """Attention of each sequence's newest tokens, any number of them, over the `window` newest tokens up to each and the
+    first n_sinks: q [n_seqs, n_rows, num_q_heads, head_dim] bf16 -> out alike; kv_len, row_len [n_seqs] int32 or None;
+    lse [n_seqs, n_rows, num_q_heads] float32 or None; the others as for pred_attend."""
+    d, a = _dims(h), _Args()
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise TypeError("q: expected a tensor [n_seqs, n_rows, num_q_heads, head_dim]")
+    S, M = q.shape[0], q.shape[1]
+    n_blocks = _blocks_of(d, block_tables, n_blocks)
+    shape = (S, M, d.num_q_heads, d.head_dim)
+    ws, ws_bytes = a.buffer(workspace, "workspace")
+    _check(_lib.load().pred_attend_window(
+        h, cache._of(d, a), a.ptr(q, "q", _BF16, shape), M, a.ptr(block_tables, "block_tables", _I32, (S, n_blocks)), n_blocks,
+        S, a.ptr(kv_len, "kv_len", _I32, (S,)), a.ptr(row_len, "row_len", _I32, (S,)), window, n_sinks, scale,
+        a.ptr(out, "out", _BF16, shape), a.ptr(lse, "lse", _F32, shape[:3]), ws, ws_bytes, _raw_stream(stream, a.device)))
 
 
 def pred_accumulate_weight(h, lse, block_lse, accepted, kv_len, decay, mass, mass_out=None, stream=None):

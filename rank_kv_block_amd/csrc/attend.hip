@@ -2,66 +2,13 @@
 // its paged cache.
 #include <type_traits>
 
+#include "attend.h"
 #include "common.h"
 #include "kernels.h"
 
 namespace pred {
+namespace attend {
 namespace {
-
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-// Start of a running maximum: finite, so that exp2(-inf - max) is 0 and not NaN
-// for a masked score before the first real one.
-constexpr float kLowest = -3.402823466e38f;
-
-// How a cache holds its values.
-enum Held : int { BF16, FP8, FP4 };
-// bytes of x values (or of a stride of x)
-template <Held HELD>
-__host__ __device__ inline int64_t bytes_of(int64_t x) {
-    return HELD == FP4 ? x / 2 : (HELD == FP8 ? x : 2 * x);
-}
-inline Held held_of(const CacheView& c) { return c.fp4 ? FP4 : (c.fp8 ? FP8 : BF16); }
-
-__device__ inline float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ inline float log2_of(float x) { return __builtin_amdgcn_logf(x); }
-
-// Which drafted tokens row i sees, a bit each.
-__device__ inline uint64_t tree_word(const AttendArgs& a, int s, int i) {
-    return a.tree ? a.tree[(int64_t)s * a.M + i] : ~0ull >> (63 - i);
-}
-
-// The lengths given for sequence s, checked once per sequence.
-__device__ inline void check_lengths(const AttendArgs& a, int s, int len, int drafted) {
-    if ((a.kv_len && a.kv_len[s] != len) || (a.draft && a.draft[s] != drafted)) atomicOr(a.err, DEVERR_LEN);
-}
-
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-__device__ inline uint32_t bf16_pair(float lo, float hi) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){lo, hi}, bf16x2_t));
-}
-
-__device__ inline uint16_t to_bf16(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
-
-__device__ inline float fp8_value(uint32_t byte) { return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0); }
-
-// Values that are not finite.  A softmax weight is positive, so an infinite
-// value that a row sees makes that element of its output the infinity, and two
-// of opposite signs or a NaN make it NaN.  Sums of products give that only while
-// the weight is held: one that underflows, or a matrix product's second term
-// (which may be 0 or negative), turns the infinity into NaN.  So where a sum
-// ends up not finite it becomes the sum of the values that are not, without
-// weights; and sums are joined by joined().
-
-// 0 for a number, else itself
-__device__ inline float not_finite(float x) { return fabsf(x) < INFINITY ? 0.f : x; }
-
-// a fa + b fb for factors in [0, 1]: an infinity stays one whatever its factor
-__device__ inline float joined(float a, float fa, float b, float fb) {
-    const float x = a * fa + b * fb;
-    return x != x ? a + b : x;
-}
 
 // ---------------------------------------------------------------- plain kernel
 //
@@ -88,7 +35,7 @@ __device__ inline float cache_value(const void* p, const uint8_t* scales, int64_
 
 constexpr int kPlainHead = 256;     // largest head size
 
-template <Held HELD>
+template <Held HELD, bool WINDOW>
 __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
     __shared__ float q_row[kPlainHead];
     __shared__ float part[4][kPlainHead];
@@ -99,7 +46,12 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
     if (h == 0 && i == 0 && threadIdx.x == 0) check_lengths(a, s, len, drafted);
     const int ctx = len - drafted;
     const bool live = i < drafted;
-    const uint64_t seen = tree_word(a, s, i);
+    const uint64_t seen = WINDOW ? 0 : tree_word(a, s, i);
+    const int pos = ctx + i, first = pos - a.window + 1;       // with a window
+    auto sees_token = [&](int t) {
+        if constexpr (WINDOW) return t <= pos && (t >= first || t < a.sinks);
+        else return t < ctx || ((seen >> (t - ctx)) & 1);
+    };
     const int64_t q_at = (((int64_t)s * a.M + i) * a.Hq + h) * a.D;
     const float scale = a.scale * a.cache.k_scale * kLog2e;
     for (int d = threadIdx.x; d < a.D; d += 256) q_row[d] = bf16_lo(a.q[q_at + d]);
@@ -111,11 +63,12 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
     for (int b = wave; b < used; b += 4) {
         const int64_t slot = a.tables ? a.tables[(int64_t)s * a.n + b] : b;
         const bool good = slot >= 0 && slot < a.N;
+        if (WINDOW && (b * a.B > pos || (b * a.B >= a.sinks && (b + 1) * a.B <= first))) continue;     // no token of it seen
         if (!good && lane == 0) atomicOr(a.err, DEVERR_TABLE);
         float bm = kLowest, bl = 0.f;
         for (int t0 = 0; good && live && t0 < a.B && b * a.B + t0 < len; t0 += 64) {
             const int t = b * a.B + t0 + lane;
-            const bool sees = t0 + lane < a.B && t < len && (t < ctx || ((seen >> (t - ctx)) & 1));
+            const bool sees = t0 + lane < a.B && t < len && sees_token(t);
             const int64_t base = slot * a.cache.block_stride + t0 * a.cache.token_stride + head_off;
             float x = 0.f;
             if (sees) {
@@ -161,7 +114,7 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
                 if (slot < 0 || slot >= a.N) continue;
                 for (int t0 = 0; t0 < a.B && b * a.B + t0 < len; ++t0) {
                     const int t = b * a.B + t0;
-                    if (t >= ctx && !((seen >> (t - ctx)) & 1)) continue;
+                    if (!sees_token(t)) continue;
                     const int64_t at = slot * a.cache.block_stride + t0 * a.cache.token_stride + head_off;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -195,159 +148,6 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
         a.lse[((int64_t)s * a.M + i) * a.Hq + h] = none ? -INFINITY : (top + log2_of(total)) * kLn2;
 }
 
-// ---------------------------------------------------------------- splitting the work
-//
-// A workgroup takes an item: one group of `rows` queries of one kv head over
-// one run of a sequence's tokens.  The lengths are on the device, so every
-// workgroup works the split out for itself from all of them: with w_s = tokens
-// of sequence s times its groups that have a live row, a run is about the sum
-// of w_s over the items wanted, so the items are alike however uneven the
-// sequences are.  A sequence of one run gets its result written by its items;
-// of one with more the items write unnormalised sums, maximum and total, and
-// a second launch joins them.
-struct Plan {
-    int slots;      // workgroups the chip holds at once
-    int rounds;     // at most this many times as many items; the runs' rounding adds at most one per sequence, head and
-                    // group
-    int run;        // shorter runs than this are not worth a round more: an item's start and its partial results
-    int unit;       // a run is a multiple of this many tokens
-    int rows;       // queries of a group
-    int groups;     // groups of a kv head's queries
-};
-
-// One sequence's share: `first` items (counting one kv head) before its own.
-struct Share {
-    int len, groups, run, runs, first;
-};
-
-struct Item {
-    int s, kvh, group, split;
-    Share share;
-    int slot;       // index of its partial results; -1: no item
-    bool last;      // the last group: it also writes what the rows of dead groups get
-};
-
-__device__ inline int runs_of(int len, int run) { return len > run ? (len + run - 1) / run : 1; }
-
-// Workgroup b of the grid, worked out by every wave alike.  Item f = ((first_s +
-// split * groups) * Hk ..): an XCD (b % 8) takes consecutive items, so the
-// groups that read the same bytes, and the heads whose bytes lie side by side,
-// meet in one L2.
-__device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b) {
-    const int lane = threadIdx.x & 63, g = a.Hq / a.Hk;
-    const int64_t most = (int64_t)a.n * a.B;
-    auto read = [&](int s, int& len, int& groups) {
-        len = 0;
-        groups = 0;
-        if (s < a.S) {
-            len = kv_len_of(a.kv_len, s, most);
-            groups = (draft_len_of(a, s, len) * g + pl.rows - 1) / pl.rows;
-            groups = groups < 1 ? 1 : groups;
-        }
-    };
-    int len0, groups0;      // the first 64 sequences' stay in registers
-    read(lane, len0, groups0);
-    auto sequence = [&](int s0, int& len, int& groups) {
-        if (s0 == 0) {
-            len = len0;
-            groups = groups0;
-        } else {
-            read(s0 + lane, len, groups);
-        }
-    };
-    int64_t total = 0;
-    for (int s0 = 0; s0 < a.S; s0 += 64) {
-        int len, groups;
-        sequence(s0, len, groups);
-        total += (int64_t)len * groups;
-    }
-    if (a.S > 1)
-        for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o);
-    // (lane 0 has a single sequence's) the same in every lane from here on, in scalar registers
-    total = ((int64_t)__builtin_amdgcn_readfirstlane((int)(total >> 32)) << 32 |
-             (uint32_t)__builtin_amdgcn_readfirstlane((int)total)) * a.Hk;
-    const int64_t per_slot = total / pl.slots, rounds = per_slot / pl.run;
-    const int64_t items = (int64_t)pl.slots * (rounds < 1 ? 1 : (rounds < pl.rounds ? rounds : pl.rounds));
-    const int64_t wanted = ((total + items - 1) / items + pl.unit - 1) / pl.unit * pl.unit;
-    auto items_of = [&](int run) {
-        int count = 0;      // of one kv head
-        for (int s0 = 0; s0 < a.S; s0 += 64) {
-            int len, groups;
-            sequence(s0, len, groups);
-            count += groups * runs_of(len, run);
-        }
-        if (a.S > 1)
-            for (int o = 32; o >= 1; o >>= 1) count += __shfl_xor(count, o);
-        return (uint32_t)__builtin_amdgcn_readfirstlane(count) * a.Hk;
-    };
-    int run = (int)(wanted < pl.unit ? pl.unit : (wanted < 0x7FFFFFFF ? wanted : 0x7FFFFFFF));
-    uint32_t all = items_of(run);
-    // Every sequence's last run is a part of one, so the items are a few more than wanted.  Where they pass one round
-    // by up to a quarter, runs a little longer do without the second, nearly empty one (8 sequences of 5k tokens, 13
-    // rows: 78 us without, 70 with; with more rounds there is nothing to gain).
-    const uint32_t one = (uint32_t)pl.slots;
-    int longer = run;
-    for (uint32_t tries = 0, now = all; tries < 2 && all > one && all - one <= one / 4; ++tries) {
-        longer = (int)(((int64_t)longer * now / one + pl.unit) / pl.unit * pl.unit);
-        now = items_of(longer);
-        if (now <= one) {
-            run = longer;
-            all = now;
-        }
-    }
-    const uint32_t each = (all + 7) / 8, f = b % 8 * each + b / 8;
-    Item it{};
-    it.slot = -1;
-    if (b / 8 >= each || f >= all) return it;
-    int before = 0;
-    for (int s0 = 0; s0 < a.S; s0 += 64) {
-        int len, groups;
-        sequence(s0, len, groups);
-        const int own = groups * runs_of(len, run);
-        int upto = own;
-        for (int o = 1; o < 64; o <<= 1) {
-            const int x = __shfl_up(upto, o);
-            if (lane >= o) upto += x;
-        }
-        const uint64_t past = __ballot((uint32_t)(before + upto) * a.Hk > f);
-        if (past) {
-            const int at = __builtin_ctzll(past);
-            it.s = s0 + at;
-            it.share.first = __builtin_amdgcn_readlane(before + upto - own, at);
-            it.share.len = __builtin_amdgcn_readlane(len, at);
-            it.share.groups = __builtin_amdgcn_readlane(groups, at);
-            break;
-        }
-        before += __builtin_amdgcn_readlane(upto, 63);
-    }
-    it.share.runs = runs_of(it.share.len, run);
-    // the sequence's runs, evened out
-    const int even_run = (it.share.len + it.share.runs - 1) / it.share.runs;
-    it.share.run = it.share.runs == 1 ? run : (even_run + pl.unit - 1) / pl.unit * pl.unit;
-    uint32_t in = f - (uint32_t)it.share.first * a.Hk;
-    it.slot = (int)f;
-    it.group = (int)(in % it.share.groups);
-    in /= it.share.groups;
-    it.kvh = (int)(in % a.Hk);
-    it.split = (int)(in / a.Hk);
-    it.last = it.group == it.share.groups - 1;
-    return it;
-}
-
-// Workspace: each sequence's share, then [items, rows, D] sums, then [items,
-// rows] (maximum, total).
-__device__ inline Share* shares_of(const AttendArgs& a) { return static_cast<Share*>(a.ws); }
-__host__ __device__ inline int64_t share_bytes(int64_t S) { return (S * (int64_t)sizeof(Share) + 15) / 16 * 16; }
-__device__ inline float* part_sums(const AttendArgs& a, const Plan& pl, int64_t slot) {
-    return reinterpret_cast<float*>(static_cast<char*>(a.ws) + share_bytes(a.S)) + slot * pl.rows * a.D;
-}
-__host__ __device__ inline int64_t most_items(const AttendArgs& a, const Plan& pl) {
-    return (int64_t)pl.slots * pl.rounds + (int64_t)a.S * a.Hk * pl.groups;
-}
-__device__ inline float2* part_stats(const AttendArgs& a, const Plan& pl, int64_t slot) {
-    return reinterpret_cast<float2*>(part_sums(a, pl, most_items(a, pl))) + slot * pl.rows;
-}
-
 // Joins a row's runs: out = sum_r 2^(m_r - m) o_r / sum_r 2^(m_r - m) l_r, for a
 // row (sequence, drafted row, query head) that has more than one.  Bound: the
 // partial sums, and a launch's latency for few rows.
@@ -362,9 +162,11 @@ __device__ inline JoinRow join_row(const AttendArgs& a, const Plan& pl, uint32_t
     const int i = (int)(row / (uint32_t)a.Hq % (uint32_t)a.M);
     j.s = (int)(row / (uint32_t)a.Hq / (uint32_t)a.M);
     const Share share = shares_of(a)[j.s];
-    j.wanted = share.runs > 1;
-    const int g = a.Hq / a.Hk, r = i * g + j.h % g;
-    j.runs = j.wanted && i < draft_len_of(a, j.s, share.len) ? share.runs : 0;
+    const int g = a.Hq / a.Hk, r = i * g + j.h % g, drafted = draft_len_of(a, j.s, share.len);
+    int runs = share.runs;
+    if (pl.chunk) runs = chunk_runs(chunk_span(a, pl, share.len, drafted, r / pl.rows), share.run);
+    j.wanted = runs > 1;
+    j.runs = j.wanted && i < drafted ? runs : 0;
     j.in_group = r % pl.rows;
     j.step = (int64_t)a.Hk * share.groups;
     j.slot = (int64_t)share.first * a.Hk + (int64_t)(j.h / g) * share.groups + r / pl.rows;
@@ -572,54 +374,6 @@ __device__ inline float sum_over_c(float x) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// Turns a product q k into units of log2: above 0, so that a masked -inf stays
-// one (the queries carry a negative scale's sign).  A scale of 0, which weighs
-// every token alike, is 2^-120 here: products below 2^96 differ by less than
-// 2^-24 then.
-__device__ inline float log2_scale(const AttendArgs& a) {
-    return fmaxf(fabsf(a.scale) * a.cache.k_scale * kLog2e, 0x1p-120f);
-}
-
-// x, or -x where scale is negative
-__device__ inline bf16x8_t signed_by(float scale, bf16x8_t x) {
-    const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;
-    return __builtin_bit_cast(bf16x8_t, __builtin_bit_cast(u32x4_t, x) ^ (u32x4_t){flip, flip, flip, flip});
-}
-
-// two e4m3 values (bytes 0, 1 or 2, 3 of w) as two bf16, exact
-template <bool HI>
-__device__ inline uint32_t fp8x2_to_bf16(uint32_t w) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI));
-}
-
-// eight e2m1 values as eight bf16 times the power of two of a scale byte, exact
-__device__ inline u32x4_t fp4x8_to_bf16(uint32_t w, uint32_t scale_byte) {
-    const float scale = __uint_as_float(scale_byte << 23);
-    return u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3))};
-}
-
-// Division of a token's index by the block size: one 64-bit product.  With
-// 2^(s-1) < B <= 2^s and magic = ceil(2^(31+s) / B), magic * B - 2^(31+s) < B <=
-// 2^s, so t * magic >> (31 + s) is t / B for every t < 2^31.
-struct BlockSize {
-    int B, shift;           // shift = 31 + s
-    uint32_t magic;
-    __host__ __device__ inline int block(int t) const { return (int)((uint64_t)(uint32_t)t * magic >> shift); }
-};
-
-inline BlockSize block_size(int B) {
-    int s = 0;
-    while (s < 31 && (1u << s) < (uint32_t)B) ++s;
-    const uint64_t one = 1ull << (31 + s);
-    return BlockSize{B, 31 + s, (uint32_t)((one + B - 1) / B)};
-}
-
-// The larger of three, one instruction where `a` is known to be a number.
-__device__ inline float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
-
 // x less its bf16 value, half HI of `pair`: exact, as one dot product.  The
 // factor -1 is kept in a register: as an operand (-1, 0) the compiler writes
 // the inline constant -1.0, which the instruction takes for (0, -1).
@@ -631,67 +385,17 @@ __device__ inline float rest_of(float x, uint32_t pair) {
                                            false);
 }
 
-// w with its halves that are not finite set to 0
-__device__ inline uint32_t finite_only(uint32_t w) {
-    return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u);
-}
-
-// the same for four e4m3 values, whose only such pattern is NaN (0x7F, 0xFF)
-__device__ inline uint32_t finite_only_fp8(uint32_t w) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        if (((w >> i) & 0x7Fu) == 0x7Fu) w &= ~(0xFFu << i);
-    return w;
-}
-
-// A masked weight is 0, and 0 times a value that is not finite would be NaN in
-// the matrix cores.  So drafted tokens' values enter the products with 0 in the
-// place of what is not finite.  A run that holds any, or whose sums are not
-// finite (every row sees the whole context), walks its tokens once more and
-// takes what is not finite from there.  (e4m3 and a 4-bit cache have no
-// infinities, and a NaN of the context needs no walk.)
-
-// Adds what is not finite among the 4 values from d on of a token's head, `row` from value_row.
-template <Held HELD>
-__device__ inline void add_not_finite(float* sum, const char* row, int d) {
-    if constexpr (HELD == FP4) {
-        if ((uint8_t)row[d / 32] == 255u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] = NAN;
-    } else if constexpr (HELD == FP8) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(row + d);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (((w >> (8 * e)) & 0x7Fu) == 0x7Fu) sum[e] = NAN;
-    } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(row + 2 * d);
-        sum[0] += not_finite(bf16_lo(w.x));
-        sum[1] += not_finite(bf16_hi(w.x));
-        sum[2] += not_finite(bf16_lo(w.y));
-        sum[3] += not_finite(bf16_hi(w.y));
-    }
-}
-// The values of a token's head (of a 4-bit cache their scales), null where its block has an invalid entry.
-template <Held HELD>
-__device__ inline const char* value_row(const AttendArgs& a, const BlockSize& bs, int s, int kvh, int tok) {
-    const int b = bs.block(tok);
-    const int64_t slot = a.tables ? a.tables[(int64_t)s * a.n + b] : b;
-    if (slot < 0 || slot >= a.N) return nullptr;
-    const int64_t at = slot * a.cache.block_stride + (int64_t)(tok - b * bs.B) * a.cache.token_stride +
-                       (int64_t)kvh * a.cache.head_stride;
-    if constexpr (HELD == FP4) return reinterpret_cast<const char*>(a.cache.v_scales) + at / 32;
-    return static_cast<const char*>(a.cache.v) + bytes_of<HELD>(at);
-}
-
 // The blocks of one sequence as a wave walks it: 64 blocks at a time, a lane
 // each holding where its block lies (bytes from the head's start of the cache).
 // Entries that are invalid, or of blocks the sequence does not use, stand for
 // block 0: every address is inside the cache, and what is loaded there is masked.
+template <bool WINDOW>
 struct TableWindow {
     const int32_t* row;     // null: the identity
     int used, first;
     uint32_t lo, hi;
     uint64_t bad;           // used blocks with an invalid entry
+    int unseen, unseen_end; // blocks that a window leaves out, whose entries may be anything
 
     __device__ inline void load(const AttendArgs& a, int block, int64_t block_bytes, int lane) {
         first = block;
@@ -699,7 +403,9 @@ struct TableWindow {
         if (block + lane < used) e = row ? row[block + lane] : block + lane;
         const bool invalid = e < 0 || e >= a.N;
         bad = __ballot(invalid);
-        if (bad && lane == 0) atomicOr(a.err, DEVERR_TABLE);
+        if (WINDOW ? __ballot(invalid && !(block + lane >= unseen && block + lane < unseen_end)) != 0 && lane == 0
+                   : bad && lane == 0)
+            atomicOr(a.err, DEVERR_TABLE);
         const int64_t at = invalid ? 0 : e * block_bytes;
         lo = (uint32_t)at;
         hi = (uint32_t)(at >> 32);
@@ -755,7 +461,17 @@ __device__ inline void stream_load(uint32_t* dst, const char* base, uint32_t off
     }
 }
 
-template <int D, Held HELD>
+// A sequence's work where a window limits it.
+struct WindowWork {
+    const AttendArgs& a;
+    __device__ inline void operator()(int s, int& len, int& groups) const {
+        const int tokens = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B), drafted = draft_len_of(a, s, tokens);
+        len = span_of(a, tokens, drafted, 0, drafted - 1, 32).end;
+        groups = 1;
+    }
+};
+
+template <int D, Held HELD, bool WINDOW>
 __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Plan pl, BlockSize bs) {
     using L = StreamLayout<D, HELD>;
     constexpr int NK = L::NK, W = L::W, H = L::H, KP = L::KP, J = L::J, TPL = L::TPL, VW = L::VW;
@@ -763,23 +479,35 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, c = lane >> 4;
-    const Item it = item_of(a, pl, blockIdx.x);
+    Item it;
+    if constexpr (WINDOW) it = item_of(a, pl, blockIdx.x, WindowWork{a});
+    else it = item_of(a, pl, blockIdx.x, DraftWork{a, pl});
     if (it.slot < 0) return;
+    if constexpr (WINDOW) it.share.len = kv_len_of(a.kv_len, it.s, (int64_t)a.n * a.B);
     const int s = it.s, kvh = it.kvh, len = it.share.len, drafted = draft_len_of(a, s, len);
+    // t0, t1 and what counts tiles are places of the walk, which with a window leaves tokens out
+    const Span span = WINDOW ? span_of(a, len, drafted, 0, drafted - 1, 32) : Span{len, 0, len};
     if (kvh == 0 && it.group == 0 && it.split == 0 && threadIdx.x == 0) {
         check_lengths(a, s, len, drafted);
         if (a.ws) shares_of(a)[s] = it.share;
     }
     const int ctx = len - drafted, t0 = it.split * it.share.run;
-    const int t1 = t0 + it.share.run < len ? t0 + it.share.run : len;
+    const int t1 = t0 + it.share.run < span.end ? t0 + it.share.run : span.end;
+    const int end = WINDOW ? span.real_end(t1) : t1;
+    auto real = [&](int v) { return WINDOW ? span.real(v) : v; };
     const int g = a.Hq / a.Hk, R = a.M * g;
 
-    if (it.last) write_dead_rows(a, it, bs, 16 * (it.group + 1), t0, t1);
+    if (!WINDOW && it.last) write_dead_rows(a, it, bs, 16 * (it.group + 1), t0, t1);
 
     // the lane's row, and the queries as second operands
     const int r = 16 * it.group + n, i = r / g;
     const bool live = r < R && i < drafted;
-    const uint64_t seen = live ? tree_word(a, s, i) : 0;
+    const uint64_t seen = live && !WINDOW ? tree_word(a, s, i) : 0;
+    const int pos = ctx + i, first = pos - a.window + 1;       // with a window
+    auto sees_token = [&](int tok) {
+        if constexpr (WINDOW) return tok <= pos && (tok >= first || tok < a.sinks);
+        else return tok < ctx || ((seen >> ((tok - ctx) & 63)) & 1);
+    };
     const int64_t row = ((int64_t)s * a.M + i) * a.Hq + kvh * g + r % g;
     const int64_t block_step = (int64_t)a.M * a.Hq;
     // where lane group c writes the c-th block of a tile that starts with block 0
@@ -807,9 +535,15 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
     const uint8_t* const ksp = HELD == FP4 ? a.cache.k_scales + head_off / 16 : nullptr;
     const uint8_t* const vsp = HELD == FP4 ? a.cache.v_scales + head_off / 16 : nullptr;
 
-    TableWindow table;
+    TableWindow<WINDOW> table;
     table.row = a.tables ? a.tables + (int64_t)s * a.n : nullptr;
-    table.used = t1 > 0 ? bs.block(t1 - 1) + 1 : 0;
+    table.used = end > 0 ? bs.block(end - 1) + 1 : 0;
+    table.unseen = table.unseen_end = 0;
+    if constexpr (WINDOW) {
+        const int lowest = ctx - a.window + 1;      // the first row's window
+        table.unseen = bs.block(a.sinks + bs.B - 1);
+        table.unseen_end = lowest > 0 ? bs.block(lowest) : 0;
+    }
 
     // this wave's tiles: groups of `per` consecutive ones, every fourth group
     const int per = pl.unit / 128;
@@ -820,7 +554,7 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
     uint32_t kr[NK][4], vr[8][VW];
     uint32_t k_sc[NK], v_sc[8];     // their scale bytes
     auto places = [&](int t) {
-        const int b = bs.block(t), last = bs.block(t + 31 < t1 ? t + 31 : t1 - 1);
+        const int b = bs.block(t), last = bs.block(t + 31 < end ? t + 31 : end - 1);
         if (last >= table.first + 64) table.load(a, b, block_bytes, lane);
         int index = b - table.first, off = (t - b * bs.B) * ts;
 #pragma unroll
@@ -857,15 +591,15 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
     const float scale = log2_scale(a);      // the queries carry its sign
 
     bool odd = false;       // a drafted token's value is not finite
-    int t = tile_of(0);
-    if (t < t1) {
+    int at_tile = tile_of(0), t = real(at_tile);
+    if (at_tile < t1) {
         table.load(a, bs.block(t), block_bytes, lane);
         places(t);
         load_k();
         load_v();
     }
-    for (int k = 0; t < t1; ++k) {
-        const int next = tile_of(k + 1);
+    for (int k = 0; at_tile < t1; ++k) {
+        const int next_tile = tile_of(k + 1), next = real(next_tile);
         // scores of this tile's 32 tokens
         float x[8];
 #pragma unroll
@@ -905,8 +639,9 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
             for (int u = 0; u < NK; ++u)
                 dead |= (uint32_t)((table.bad >> ((bs.block(t + TPL * u) - table.first) & 63)) & 1) << u;
         }
-        const bool masked = t + 32 > ctx || t + 32 > t1 || dead != 0;
-        if (next < t1) {
+        // (the last row's window begins at len - window)
+        const bool masked = t + 32 > ctx || t + 32 > end || dead != 0 || (WINDOW && t < len - a.window && t + 32 > a.sinks);
+        if (next_tile < t1) {
             places(next);
             load_k();
         }
@@ -915,20 +650,20 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int u = e / W, tok = t + TPL * u + W * c + e % W;
-                const bool there = tok < t1 && !((dead >> u) & 1);
-                const int at = tok - ctx;
-                const bool sees = there && (at < 0 || ((seen >> (at & 63)) & 1));
+                const bool there = tok < end && !((dead >> u) & 1);
+                const bool some = WINDOW || tok >= ctx;         // perhaps not every row sees it
+                const bool sees = there && sees_token(tok);
                 x[e] = sees ? x[e] : -INFINITY;
                 if constexpr (HELD == FP4) {
                     const bool bad = v_sc[e] == 255u;
-                    odd |= bad && there && at >= 0;
-                    if (!there || (bad && at >= 0)) vr[e][0] = v_sc[e] = 0u;
+                    odd |= bad && there && some;
+                    if (!there || (bad && some)) vr[e][0] = v_sc[e] = 0u;
                 } else {
 #pragma unroll
                     for (int y = 0; y < VW; ++y) {
                         vr[e][y] = there ? vr[e][y] : 0u;       // no value there at all
                         const uint32_t finite = HELD == FP8 ? finite_only_fp8(vr[e][y]) : finite_only(vr[e][y]);
-                        if (at >= 0 && finite != vr[e][y]) {
+                        if (some && finite != vr[e][y]) {
                             vr[e][y] = finite;
                             odd = true;
                         }
@@ -950,7 +685,7 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 #pragma unroll
             for (int j = 0; j < J; ++j) o[j] *= alpha;
         }
-        if (a.block_lse) {
+        if (!WINDOW && a.block_lse) {
             // Blocks of 8 or 16 tokens lie side by side in a tile, in 2 or 4 of a lane's 8 places; one of 32 or more
             // fills it.  Their sums are those of the weights, brought back by the maximum, unless one lies so far
             // below it that its weights are lost: then the sums are taken against each block's own maximum.
@@ -1063,7 +798,8 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
             o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, hi, o[j], 0, 0, 0);
             o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(val, lo, o[j], 0, 0, 0);
         }
-        if (next < t1) load_v();
+        if (next_tile < t1) load_v();
+        at_tile = next_tile;
         t = next;
     }
 
@@ -1084,10 +820,11 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
         for (int v = 0; v < 4; ++v)
 #pragma unroll
             for (int j = 0; j < J; ++j) sum[v][j] = 0.f;
-        for (int tok = all || ctx < t0 ? t0 : ctx; tok < t1; ++tok) {
-            if ((tok - t0) / 32 / per % 4 != wave) continue;        // another wave's
+        for (int v = all || WINDOW || ctx < t0 ? t0 : ctx; v < t1; ++v) {
+            if ((v - t0) / 32 / per % 4 != wave) continue;          // another wave's
+            const int tok = real(v);
             const char* const from = value_row<HELD>(a, bs, s, kvh, tok);
-            if (from && (tok < ctx || ((seen >> ((tok - ctx) & 63)) & 1))) {
+            if (from && sees_token(tok)) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
 #pragma unroll
@@ -1187,33 +924,6 @@ __global__ __launch_bounds__(256, 2) void attend_stream_kernel(AttendArgs a, Pla
 // cores busy in 46% of the SIMDs' cycles; with block sums and lengths and drafts
 // that vary 484 us (458 from an e4m3 cache), 24%.  13 rows over 8 sequences of 5k
 // tokens: 58 us (50), 16%: an item's start and a chain of 10 to 12 tiles.
-template <int D>
-struct TreeLds {
-    static constexpr int kRow = 2 * D;              // bytes of a row
-    static constexpr int kPieces = kRow / 16;
-    static constexpr int kTile = 64 * kRow;
-    // byte offset of 16-byte piece `piece` of row `row`
-    __device__ static inline int key(int row, int piece) {
-        return row * kRow + 16 * (piece ^ (D == 128 ? row & 15 : (row >> 1) & 7));
-    }
-    __device__ static inline int value(int row, int piece) {
-        return row * kRow + 16 * (piece ^ (D == 128 ? (row & 3) * 4 : ((row >> 1) & 1) * 4));
-    }
-};
-
-// max / sum over the two lanes of a query
-__device__ inline float max_over_f(float x) {
-    auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-}
-__device__ inline float sum_over_f(float x) {
-    auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
-}
-
-typedef short i16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
-
 // BLOCKS: block sums a half tile has: 0 without block_lse, 1 for blocks of 32
 // tokens or more, 2 for 16, 4 for 8.
 template <int D, Held HELD, int BLOCKS>
@@ -1227,7 +937,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
     __shared__ __attribute__((aligned(16))) char lds[4 * T::kTile];     // keys 0, keys 1, values 0, values 1
     __shared__ int any_odd;         // a drafted token's value is not finite
 
-    const Item it = item_of(a, pl, blockIdx.x);
+    const Item it = item_of(a, pl, blockIdx.x, DraftWork{a, pl});
     if (it.slot < 0) return;
     const int s = it.s, kvh = it.kvh, len = it.share.len, drafted = draft_len_of(a, s, len);
     if (kvh == 0 && it.group == 0 && it.split == 0 && threadIdx.x == 0) {
@@ -1676,7 +1386,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
 
 // ---------------------------------------------------------------- choice of a kernel
 
-enum class Kind { Stream, Tree, Plain };
+enum class Kind { Stream, Tree, Plain, Chunk };
 
 int queries_of(const AttendArgs& a) { return a.M * (a.Hq / a.Hk); }
 
@@ -1684,6 +1394,8 @@ constexpr int kRounds = 8;              // most workgroups a CU's places get one
 // Queries per kv head of the stream kernel.  Two groups of 16 read most bytes twice: over 131072 tokens of one sequence
 // 32 queries take 142 us with it, and 40 take 111 with the tree kernel; where they cross below 32 has not been measured.
 constexpr int kStreamQueries = 32;
+// and with a window: one group
+constexpr int kWindowQueries = 16;
 
 Kind kind_of(const AttendArgs& a) {
     const Held held = held_of(a.cache);
@@ -1702,12 +1414,23 @@ Kind kind_of(const AttendArgs& a) {
     const int tpl = (int)(1024 / bytes(a.D));
     const bool fits = a.B % tpl == 0 && a.cache.token_stride <= (1 << 24) &&
                       bytes(a.B * a.cache.token_stride) <= 0x7FFFFFFF && !(held == FP4 && a.D == 64);
+    if (a.window) return fits && queries_of(a) <= kWindowQueries ? Kind::Stream : Kind::Chunk;
     return fits && queries_of(a) <= kStreamQueries ? Kind::Stream : Kind::Tree;
 }
 
-Plan plan_of(const AttendArgs& a, bool tree) {
+// The most tokens that a group walks: all of them, or what a window leaves (of any run of rows that a group has).
+int64_t most_tokens(const AttendArgs& a, const Plan& pl) {
+    const int64_t all = (int64_t)a.n * a.B;
+    if (!a.window) return all;
+    const int64_t rows = pl.chunk ? pl.rows / (a.Hq / a.Hk) + 2 : a.M, some = (int64_t)a.sinks + a.window + rows + 2 * 64;
+    return some < all ? some : all;
+}
+
+Plan plan_of(const AttendArgs& a, Kind kind) {
+    const bool tree = kind != Kind::Stream;
     const int queries = queries_of(a);
     Plan pl;
+    pl.chunk = kind == Kind::Chunk;
     pl.rows = tree ? 128 : 16;
     pl.groups = (queries + pl.rows - 1) / pl.rows;
     if (pl.rows > queries) pl.rows = queries;       // of one group
@@ -1721,13 +1444,18 @@ Plan plan_of(const AttendArgs& a, bool tree) {
     // tokens, 13 rows: 75 us with 1, 91 with 2, 109 with 4).
     pl.slots = 2 * a.n_cu;
     pl.run = tree ? 2048 : 2560;
-    const double most = (double)a.S * a.n * a.B * pl.groups * a.Hk / pl.slots / pl.run;
+    const double most = (double)a.S * most_tokens(a, pl) * pl.groups * a.Hk / pl.slots / pl.run;
     pl.rounds = most < 1 ? 1 : (most < kRounds ? (int)most : kRounds);
+    if (pl.chunk) {
+        pl.rounds = 1;
+        // groups that fill the chip as they are keep their tokens in one run (unit above any number of tokens)
+        if ((int64_t)a.S * a.Hk * pl.groups >= 4ll * pl.slots) pl.unit = 1 << 30;
+    }
     return pl;
 }
 
 // Whether a sequence can have more than one run, so that there are partial results.
-bool may_split(const AttendArgs& a, const Plan& pl) { return (int64_t)a.n * a.B > pl.unit; }
+bool may_split(const AttendArgs& a, const Plan& pl) { return most_tokens(a, pl) > pl.unit; }
 
 size_t plan_bytes(const AttendArgs& a, const Plan& pl) {
     return may_split(a, pl) ? (size_t)(share_bytes(a.S) + most_items(a, pl) * pl.rows * (a.D + 2) * (int64_t)sizeof(float)) : 0;
@@ -1737,7 +1465,12 @@ template <int D, Held HELD>
 void launch_fast(const AttendArgs& a, Kind kind, const Plan& pl, uint32_t grid, hipStream_t stream) {
     const BlockSize bs = block_size(a.B);
     if (kind == Kind::Stream) {
-        if constexpr (HELD != FP4 || D == 128) attend_stream_kernel<D, HELD><<<grid, 256, 0, stream>>>(a, pl, bs);
+        if constexpr (HELD != FP4 || D == 128) {
+            if (a.window) attend_stream_kernel<D, HELD, true><<<grid, 256, 0, stream>>>(a, pl, bs);
+            else attend_stream_kernel<D, HELD, false><<<grid, 256, 0, stream>>>(a, pl, bs);
+        }
+    } else if (kind == Kind::Chunk) {
+        launch_chunk<D, HELD>(a, pl, bs, grid, stream);
     } else if (!a.block_lse) attend_tree_kernel<D, HELD, 0><<<grid, 256, 0, stream>>>(a, pl, bs);
     else if (a.B == 8) attend_tree_kernel<D, HELD, 4><<<grid, 256, 0, stream>>>(a, pl, bs);
     else if (a.B == 16) attend_tree_kernel<D, HELD, 2><<<grid, 256, 0, stream>>>(a, pl, bs);
@@ -1755,19 +1488,26 @@ void launch_join(const AttendArgs& a, const Plan& pl, uint32_t rows, hipStream_t
 }
 
 }  // namespace
+}  // namespace attend
+
+using namespace attend;
 
 size_t attend_workspace_bytes(const AttendArgs& a) {
     if (a.D != 64 && a.D != 128) return 0;
-    // of a call without block_lse, whose runs can be the shorter
-    const size_t tree = plan_bytes(a, plan_of(a, true));
-    const size_t stream = queries_of(a) > kStreamQueries ? 0 : plan_bytes(a, plan_of(a, false));
+    // of a call without block_lse, whose runs can be the shorter; the cache may be of any type and layout
+    const Kind many = a.window ? Kind::Chunk : Kind::Tree;
+    const size_t tree = plan_bytes(a, plan_of(a, many));
+    const size_t stream = queries_of(a) > (a.window ? kWindowQueries : kStreamQueries) ? 0 : plan_bytes(a, plan_of(a, Kind::Stream));
     return tree > stream ? tree : stream;
 }
 
 const char* attend_kernel_name(const AttendArgs& a) {
-    const Kind kind = kind_of(a);
-    return kind == Kind::Stream ? "attend_stream_kernel"
-                                : (kind == Kind::Tree ? "attend_tree_kernel" : "attend_plain_kernel");
+    switch (kind_of(a)) {
+        case Kind::Stream: return "attend_stream_kernel";
+        case Kind::Tree: return "attend_tree_kernel";
+        case Kind::Chunk: return "attend_chunk_kernel";
+        default: return "attend_plain_kernel";
+    }
 }
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
@@ -1777,12 +1517,16 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     const Kind kind = kind_of(a);
     if (kind == Kind::Plain) {
         const Held held = held_of(a.cache);
-        if (held == FP4) attend_plain_kernel<FP4><<<row_grid, 256, 0, stream>>>(a);
-        else if (held == FP8) attend_plain_kernel<FP8><<<row_grid, 256, 0, stream>>>(a);
-        else attend_plain_kernel<BF16><<<row_grid, 256, 0, stream>>>(a);
+        auto launch = [&](auto held) {
+            if (a.window) attend_plain_kernel<decltype(held)::value, true><<<row_grid, 256, 0, stream>>>(a);
+            else attend_plain_kernel<decltype(held)::value, false><<<row_grid, 256, 0, stream>>>(a);
+        };
+        if (held == FP4) launch(std::integral_constant<Held, FP4>());
+        else if (held == FP8) launch(std::integral_constant<Held, FP8>());
+        else launch(std::integral_constant<Held, BF16>());
         return hipGetLastError();
     }
-    const Plan pl = plan_of(a, kind == Kind::Tree);
+    const Plan pl = plan_of(a, kind);
     const bool split = may_split(a, pl);
     AttendArgs b = a;
     if (!split) b.ws = nullptr;

@@ -184,6 +184,63 @@ bool attend_counts_ok(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_block
            n_blocks <= kMostTokens / p->d.block_size;
 }
 
+// Rows of a sequence in a call with a window.
+constexpr int kMostRows = 1 << 24;
+
+int check_window(int32_t n_rows, int32_t window, int32_t n_sinks, const char* what) {
+    if (n_rows < 1 || n_rows > kMostRows)
+        return fail(PRED_ERR_OUT_OF_RANGE, "%s: n_rows (%d) outside [1, 2^24]", what, n_rows);
+    if (window < 1 || n_sinks < 0)
+        return fail(PRED_ERR_OUT_OF_RANGE, "%s: window (%d) must be >= 1 and n_sinks (%d) >= 0", what, window, n_sinks);
+    return PRED_OK;
+}
+
+// No sequence has more than kMostTokens, so a larger window or more sinks hide nothing either.
+void set_window(pred::AttendArgs* a, int32_t window, int32_t n_sinks) {
+    a->window = window < kMostTokens ? window : (int)kMostTokens;
+    a->sinks = n_sinks < kMostTokens ? n_sinks : (int)kMostTokens;
+}
+
+// The checks and the launch of both attention calls; `a` holds the shape and what
+// only one of them has.
+int attend(pred_t* p, pred::AttendArgs& a, const pred_kv_cache* cache, const pred_bf16* q, const int32_t* block_tables,
+           int64_t n_blocks, const int32_t* kv_len, const int32_t* draft_len, float scale, pred_bf16* out, float* lse,
+           void* workspace, size_t ws_bytes, void* stream, const char* what) {
+    int rc;
+    if ((rc = check_cache(p, cache, &a.cache, what)) || (rc = check_counts(p, n_blocks, a.S, what))) return rc;
+    if (p->d.head_dim > kMostHead)
+        return fail(PRED_ERR_UNSUPPORTED, "%s: head_dim (%d) above %d", what, p->d.head_dim, kMostHead);
+    if (!block_tables && n_blocks > p->d.max_blocks)
+        return fail(PRED_ERR_OUT_OF_RANGE, "%s: %lld blocks without a table, max_blocks %lld", what, (long long)n_blocks,
+                    (long long)p->d.max_blocks);
+    if (!std::isfinite(scale)) return fail(PRED_ERR_OUT_OF_RANGE, "%s: scale must be finite", what);
+    if (a.S == 0) return ok();
+    if (!q || !out) return fail(PRED_ERR_NULL_ARG, "%s: q or out is NULL", what);
+    if (!pred::aligned16(q) || !pred::aligned16(out))
+        return fail(PRED_ERR_UNSUPPORTED, "%s: q and out must be 16-byte aligned", what);
+    // a row's queries are read by several workgroups, and its output may be written before the last of them starts
+    const uint64_t bytes = (uint64_t)a.S * a.M * p->d.num_q_heads * p->d.head_dim * 2;
+    const uint64_t from = (uint64_t)(uintptr_t)q, to = (uint64_t)(uintptr_t)out;
+    if (from < to + bytes && to < from + bytes) return fail(PRED_ERR_OUT_OF_RANGE, "%s: out overlaps q", what);
+    const size_t need = n_blocks > 0 ? pred::attend_workspace_bytes(a) : 0;
+    if (need > 0 && (!workspace || ws_bytes < need))
+        return fail(PRED_ERR_WORKSPACE, "%s needs a %zu-byte workspace (%zu given)", what, need,
+                    workspace ? ws_bytes : (size_t)0);
+    if (need > 0 && !pred::aligned16(workspace))
+        return fail(PRED_ERR_WORKSPACE, "%s: the workspace must be 16-byte aligned", what);
+    a.q = q;
+    a.tables = block_tables;
+    a.kv_len = kv_len;
+    a.draft = draft_len;
+    a.out = out;
+    a.lse = lse;
+    a.ws = workspace;
+    a.scale = scale;
+    const hipError_t e = pred::launch_attend(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, what);
+    return ok();
+}
+
 int check_heads(int64_t n_tokens, int32_t n_heads, const char* what) {
     if (n_tokens < 0 || n_heads < 0 || n_heads > 65536)
         return fail(PRED_ERR_OUT_OF_RANGE, "%s: n_tokens (%lld) < 0 or n_heads (%d) outside [0, 65536]", what,
@@ -496,46 +553,55 @@ int pred_attend(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32
                 const int32_t* draft_len, float scale, pred_bf16* out, float* lse, float* block_lse, void* workspace,
                 size_t ws_bytes, void* stream) {
     int rc = check_handle(p, "attend");
+    if (rc == 0) rc = check_n_rows(n_rows, "attend");
     if (rc) return rc;
-    pred::CacheView view;
-    if ((rc = check_cache(p, cache, &view, "attend")) || (rc = check_counts(p, n_blocks, n_seqs, "attend")) ||
-        (rc = check_n_rows(n_rows, "attend")))
-        return rc;
-    if (p->d.head_dim > kMostHead)
-        return fail(PRED_ERR_UNSUPPORTED, "attend: head_dim (%d) above %d", p->d.head_dim, kMostHead);
-    if (!block_tables && n_blocks > p->d.max_blocks)
-        return fail(PRED_ERR_OUT_OF_RANGE, "attend: %lld blocks without a table, max_blocks %lld", (long long)n_blocks,
-                    (long long)p->d.max_blocks);
-    if (!std::isfinite(scale)) return fail(PRED_ERR_OUT_OF_RANGE, "attend: scale must be finite");
-    if (n_seqs == 0) return ok();
-    if (!q || !out) return fail(PRED_ERR_NULL_ARG, "attend: q or out is NULL");
-    if (!pred::aligned16(q) || !pred::aligned16(out))
-        return fail(PRED_ERR_UNSUPPORTED, "attend: q and out must be 16-byte aligned");
-    // a row's queries are read by several workgroups, and its output may be written before the last of them starts
-    const uint64_t bytes = (uint64_t)n_seqs * n_rows * p->d.num_q_heads * p->d.head_dim * 2;
-    const uint64_t from = (uint64_t)(uintptr_t)q, to = (uint64_t)(uintptr_t)out;
-    if (from < to + bytes && to < from + bytes) return fail(PRED_ERR_OUT_OF_RANGE, "attend: out overlaps q");
     pred::AttendArgs a = attend_shape(p, n_seqs, n_rows, n_blocks);
-    const size_t need = n_blocks > 0 ? pred::attend_workspace_bytes(a) : 0;
-    if (need > 0 && (!workspace || ws_bytes < need))
-        return fail(PRED_ERR_WORKSPACE, "attend needs a %zu-byte workspace (%zu given)", need,
-                    workspace ? ws_bytes : (size_t)0);
-    if (need > 0 && !pred::aligned16(workspace))
-        return fail(PRED_ERR_WORKSPACE, "attend: the workspace must be 16-byte aligned");
-    a.cache = view;
-    a.q = q;
     a.tree = tree;
-    a.tables = block_tables;
-    a.kv_len = kv_len;
-    a.draft = draft_len;
-    a.out = out;
-    a.lse = lse;
     a.block_lse = block_lse;
-    a.ws = workspace;
-    a.scale = scale;
-    const hipError_t e = pred::launch_attend(a, (hipStream_t)stream);
-    if (e != hipSuccess) return hip_fail(e, "attend launch");
-    return ok();
+    return attend(p, a, cache, q, block_tables, n_blocks, kv_len, draft_len, scale, out, lse, workspace, ws_bytes, stream,
+                  "attend");
+}
+
+size_t pred_attend_window_workspace_bytes(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_blocks, int32_t window,
+                                          int32_t n_sinks) {
+    if (!p || n_seqs < 1 || n_rows < 1 || n_rows > kMostRows || n_blocks < 1 || n_blocks > kMostTokens / p->d.block_size ||
+        window < 1 || n_sinks < 0)
+        return 0;
+    pred::AttendArgs a = attend_shape(p, n_seqs, n_rows, n_blocks);
+    set_window(&a, window, n_sinks);
+    return pred::attend_workspace_bytes(a);
+}
+
+const char* pred_attend_window_kernel_name(pred_t* p, const pred_kv_cache* cache, int32_t n_rows) {
+    const char* const what = "attend_window_kernel_name";
+    if (!p) {
+        fail(PRED_ERR_NULL_ARG, "%s: predictor is NULL", what);
+        return nullptr;
+    }
+    pred::CacheView view;
+    if (check_cache(p, cache, &view, what) || check_window(n_rows, 1, 0, what)) return nullptr;
+    if (p->d.head_dim > kMostHead) {
+        fail(PRED_ERR_UNSUPPORTED, "%s: head_dim (%d) above %d", what, p->d.head_dim, kMostHead);
+        return nullptr;
+    }
+    pred::AttendArgs a = attend_shape(p, 1, n_rows, 1);
+    a.cache = view;
+    set_window(&a, 1, 0);
+    ok();
+    return pred::attend_kernel_name(a);
+}
+
+int pred_attend_window(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32_t n_rows,
+                       const int32_t* block_tables, int64_t n_blocks, int32_t n_seqs, const int32_t* kv_len,
+                       const int32_t* row_len, int32_t window, int32_t n_sinks, float scale, pred_bf16* out, float* lse,
+                       void* workspace, size_t ws_bytes, void* stream) {
+    int rc = check_handle(p, "attend_window");
+    if (rc == 0) rc = check_window(n_rows, window, n_sinks, "attend_window");
+    if (rc) return rc;
+    pred::AttendArgs a = attend_shape(p, n_seqs, n_rows, n_blocks);
+    set_window(&a, window, n_sinks);
+    return attend(p, a, cache, q, block_tables, n_blocks, kv_len, row_len, scale, out, lse, workspace, ws_bytes, stream,
+                  "attend_window");
 }
 
 int pred_accumulate_weight(pred_t* p, const float* lse, const float* block_lse, int32_t n_rows,

@@ -215,6 +215,7 @@ struct AttendArgs {
     int n;                  // blocks per sequence
     int S, M, Hq, Hk, D, B;
     int n_cu;
+    int window, sinks;      // window 0: every row sees the whole context
 };
 // Tokens in a sequence's cache and how many of them are drafted rows; values
 // outside their range are clamped (attend.hip's check_lengths flags them).

@@ -1,0 +1,442 @@
+// Attention with a sliding window and sinks for more queries than the stream
+// kernel takes: prompt chunks, whole prompts, chains of drafted tokens.
+#include "attend.h"
+#include "common.h"
+#include "kernels.h"
+
+namespace pred {
+namespace attend {
+namespace {
+
+// A sequence's work: the most that a group of it walks, and all groups, those
+// without a live row among them (they write what such rows get).
+struct ChunkWork {
+    const AttendArgs& a;
+    const Plan& pl;
+    __device__ inline void operator()(int s, int& len, int& groups) const {
+        const int tokens = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B);
+        const int some = (a.sinks + 63) / 64 * 64 + a.window + pl.rows / (a.Hq / a.Hk) + 1 + 64;
+        len = draft_len_of(a, s, tokens) == 0 ? 0 : (some < tokens ? some : tokens);
+        groups = pl.groups;
+    }
+};
+
+// ---------------------------------------------------------------- chunk kernel
+//
+// The tree kernel's layout (attend.hip): a workgroup has 128 queries of a kv
+// head, consecutive in (row, query head), and walks tiles of 64 tokens through a
+// double-buffered stage in LDS, each of its four waves with 32 queries, or, where
+// up to 64 are live, two waves with the same 32 and half of each tile each.  Lane
+// (n = lane % 32, f = lane / 32) owns query n.
+//
+// A group walks only the tiles that some row of it sees (Span): the sinks' and
+// from its first row's window on, up to its last row.  A wave skips a tile that
+// none of its rows sees.  Tiles that every row of the group sees whole need no
+// masks, and those of a bf16 cache go straight into LDS; in the others values
+// that are not finite are taken out on the way (the tree kernel's drafted tokens).
+//
+// The weights enter the value product as one bf16 term, 2^-8 of a weight off at
+// most (the stream and tree kernels' two terms would be half as many matrix
+// instructions again, and these are what long chunks are bound by): an output is
+// 2^-8 of the weighted mean of the absolute values off at most.  Where the values
+// are of either sign that is about what the output's own rounding to bf16 adds.
+template <int D, Held HELD>
+__global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan pl, BlockSize bs) {
+    using T = TreeLds<D>;
+    constexpr int RB = (int)(HELD == FP4 ? D / 2 : (HELD == FP8 ? D : 2 * D));      // bytes of a cache row
+    constexpr int CR = RB / 16;                 // 16-byte pieces of it
+    constexpr int NR = (64 * CR + 255) / 256;   // pieces a thread stages, of keys and of values
+    constexpr int SPREAD = 2 * D / RB;          // pieces of an LDS row that one becomes
+    constexpr int KS = D / 16, DT = D / 32;
+    __shared__ __attribute__((aligned(16))) char lds[4 * T::kTile];     // keys 0, keys 1, values 0, values 1
+    __shared__ int any_odd;         // a value of a tile that is not seen whole is not finite
+
+    Item it = item_of(a, pl, blockIdx.x, ChunkWork{a, pl});
+    if (it.slot < 0) return;
+    {   // the longest walks first
+        const int other = it.share.groups - 1 - it.group;
+        it.slot += other - it.group;
+        it.group = other;
+    }
+    it.share.len = kv_len_of(a.kv_len, it.s, (int64_t)a.n * a.B);
+    const int s = it.s, kvh = it.kvh, len = it.share.len, drafted = draft_len_of(a, s, len);
+    if (kvh == 0 && it.group == 0 && it.split == 0 && threadIdx.x == 0) {
+        check_lengths(a, s, len, drafted);
+        if (a.ws) shares_of(a)[s] = it.share;
+    }
+    const Span span = chunk_span(a, pl, len, drafted, it.group);
+    const int runs = chunk_runs(span, it.share.run);
+    if (it.split >= runs) return;
+    // places of the walk
+    const int v0 = it.split * it.share.run, v1 = v0 + it.share.run < span.end ? v0 + it.share.run : span.end;
+    const int end = span.real_end(v1), ctx = len - drafted;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 31, f = lane >> 5;
+    const int g = a.Hq / a.Hk, R = a.M * g;
+    const int64_t group_r0 = (int64_t)pl.rows * it.group;
+    const bool pairs = (int64_t)drafted * g - group_r0 <= 64;
+    const int in_group = (pairs ? wave / 2 : wave) * 32, r0 = (int)group_r0 + in_group, r = r0 + n, i = r / g;
+    const bool live = r < R && in_group + n < pl.rows && i < drafted;
+    const bool wave_live = r0 < R && in_group < pl.rows && r0 / g < drafted;       // rows of a wave die from the end
+    const int64_t row = ((int64_t)s * a.M + i) * a.Hq + kvh * g + r % g;
+    const int pos = ctx + i, first = pos - a.window + 1;
+    // of all live rows of the group, and of the wave
+    auto last_row = [&](int r_last) { return r_last / g < drafted ? r_last / g : drafted - 1; };
+    const int group_pos = ctx + (int)group_r0 / g, group_first = ctx + last_row((int)group_r0 + pl.rows - 1) - a.window + 1;
+    const int wave_pos = ctx + r0 / g, wave_last = ctx + last_row(r0 + 31), wave_first = wave_last - a.window + 1;
+    // every token of the 64 (32) from t on is seen by all rows from position `pos` on whose last window begins at `first`
+    auto whole = [&](int t, int tokens, int lowest_pos, int highest_first) {
+        return t + tokens - 1 <= lowest_pos && (t >= highest_first || t + tokens <= a.sinks);
+    };
+
+    bf16x8_t q[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+        q[k] = bf16x8_t{};
+        if (live) q[k] = signed_by(a.scale, load8(a.q + row * D + 16 * k + 8 * f));
+    }
+
+    const int64_t head_off = bytes_of<HELD>(kvh * a.cache.head_stride);
+    const char* const kp = static_cast<const char*>(a.cache.k) + head_off;
+    const char* const vp = static_cast<const char*>(a.cache.v) + head_off;
+    const int32_t* const table = a.tables ? a.tables + (int64_t)s * a.n : nullptr;
+
+    // Staging, as in the tree kernel; t is a tile's first token.
+    auto entry_of = [&](int t) {
+        const int tok = t + lane;
+        if (tok >= end) return -1;
+        const int b = bs.block(tok);
+        return table ? table[b] : b;
+    };
+    auto offset_of = [&](int t, int slot, uint64_t& nowhere) -> int64_t {
+        const int tok = t + lane;
+        const bool none = tok >= end || slot < 0 || slot >= a.N;
+        nowhere = __ballot(none);
+        return none ? 0 : bytes_of<HELD>(slot * a.cache.block_stride + (int64_t)(tok - bs.block(tok) * bs.B) * a.cache.token_stride);
+    };
+    const int my_tok = threadIdx.x / CR, my_piece = threadIdx.x % CR;     // and tokens 256 / CR further on
+    const bool mine_in = 256 / CR * NR <= 64 || my_tok < 64;     // (64 values in 4 bits: half of the threads have a piece)
+    u32x4_t ks[NR], vs[NR];
+    uint32_t k_sc[NR], v_sc[NR];        // a piece's scale byte
+    auto load_tile = [&](int64_t off) {
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            const int from = my_tok + 256 / CR * x;
+            const int64_t o = ((int64_t)__shfl((int)(off >> 32), from) << 32 | (uint32_t)__shfl((int)off, from)) +
+                              16 * my_piece;
+            ks[x] = *reinterpret_cast<const u32x4_t*>(kp + o);
+            vs[x] = *reinterpret_cast<const u32x4_t*>(vp + o);
+            if constexpr (HELD == FP4) {
+                k_sc[x] = a.cache.k_scales[(head_off + o) >> 4];
+                v_sc[x] = a.cache.v_scales[(head_off + o) >> 4];
+            }
+        }
+    };
+    const int k_to = T::key(my_tok, SPREAD * my_piece), v_to = T::value(my_tok, SPREAD * my_piece);
+    auto store_tile = [&](int buf, int t, uint64_t nowhere) {
+        if (!mine_in) return;
+        if (nowhere != 0 || !whole(t, 64, group_pos, group_first)) {
+            bool odd = false;
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+                const bool none = (nowhere >> (my_tok + 256 / CR * x)) & 1;
+                if constexpr (HELD == FP4) {
+                    const bool bad = v_sc[x] == 255u;
+                    odd |= bad && !none;
+                    if (none || bad) {
+                        vs[x] = u32x4_t{0, 0, 0, 0};
+                        v_sc[x] = 0;
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < 4 && HELD != FP4; ++y) {
+                    const uint32_t w = none ? 0u : vs[x][y];
+                    vs[x][y] = HELD == FP8 ? finite_only_fp8(w) : finite_only(w);
+                    odd |= vs[x][y] != w;
+                }
+            }
+            if (odd) any_odd = 1;
+        }
+        char* const kt = lds + buf * T::kTile;
+        char* const vt = lds + (2 + buf) * T::kTile;
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            constexpr int kStep = 256 / CR * T::kRow;
+            if constexpr (HELD == FP4) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    *reinterpret_cast<u32x4_t*>(kt + (k_to ^ (16 * y)) + x * kStep) = fp4x8_to_bf16(ks[x][y], k_sc[x]);
+                    *reinterpret_cast<u32x4_t*>(vt + (v_to ^ (16 * y)) + x * kStep) = fp4x8_to_bf16(vs[x][y], v_sc[x]);
+                }
+            } else if constexpr (HELD == FP8) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    u32x4_t wk, wv;
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        wk[2 * z] = fp8x2_to_bf16<false>(ks[x][2 * y + z]);
+                        wk[2 * z + 1] = fp8x2_to_bf16<true>(ks[x][2 * y + z]);
+                        wv[2 * z] = fp8x2_to_bf16<false>(vs[x][2 * y + z]);
+                        wv[2 * z + 1] = fp8x2_to_bf16<true>(vs[x][2 * y + z]);
+                    }
+                    *reinterpret_cast<u32x4_t*>(kt + (k_to ^ (16 * y)) + x * kStep) = wk;
+                    *reinterpret_cast<u32x4_t*>(vt + (v_to ^ (16 * y)) + x * kStep) = wv;
+                }
+            } else {
+                *reinterpret_cast<u32x4_t*>(kt + k_to + x * kStep) = ks[x];
+                *reinterpret_cast<u32x4_t*>(vt + v_to + x * kStep) = vs[x];
+            }
+        }
+    };
+    // straight into LDS: a lane fetches the piece that belongs in its place
+    const int k_piece = my_piece ^ (D == 128 ? my_tok & 15 : (my_tok >> 1) & 7);
+    const int v_piece = my_piece ^ (D == 128 ? (my_tok & 3) * 4 : ((my_tok >> 1) & 1) * 4);
+    auto direct_load = [&](char* to, const char* from) {
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)from,
+                                         (__attribute__((address_space(3))) uint32_t*)to, 16, 0, 0);
+    };
+    auto direct_tile = [&](int buf, int64_t off) {
+        int64_t at[NR];
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            const int from = my_tok + 256 / CR * x;
+            at[x] = (int64_t)__shfl((int)(off >> 32), from) << 32 | (uint32_t)__shfl((int)off, from);
+        }
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            char* const to = lds + (wave * (64 / CR) + 256 / CR * x) * T::kRow + buf * T::kTile;
+            direct_load(to, kp + at[x] + 16 * k_piece);
+            direct_load(to + 2 * T::kTile, vp + at[x] + 16 * v_piece);
+        }
+    };
+    const int l16 = lane & 15;
+    const int k_from = T::key(n, f);
+    const int v_from = T::value(4 * f + l16 / 4, 2 * ((lane >> 4) & 1) + l16 % 4 / 2) + 8 * (l16 % 2);
+
+    f32x16_t o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = f32x16_t{};
+    float m = kLowest, l = 0.f;
+    const float scale = log2_scale(a);
+
+    if (threadIdx.x == 0) any_odd = 0;
+    __syncthreads();
+    uint64_t nowhere = 0, nowhere_next = 0;
+    int slot = -1;
+    if (v0 < v1) {
+        slot = entry_of(span.real(v0));
+        load_tile(offset_of(span.real(v0), slot, nowhere));
+        slot = entry_of(span.real(v0 + 64));
+        store_tile(0, span.real(v0), nowhere);
+    }
+    __syncthreads();
+    // HALVES = 2: the whole of every tile; 1: half `mine` of it
+    auto walk = [&](auto halves_, const int mine) {
+        constexpr int HALVES = decltype(halves_)::value;
+        for (int v = v0, buf = 0; v < v1; v += 64, buf ^= 1) {
+            const bool more = v + 64 < v1;
+            const int t = span.real(v), next = span.real(v + 64);
+            bool direct = false;
+            int64_t off = 0;
+            if (more) {
+                off = offset_of(next, slot, nowhere_next);
+                direct = HELD == BF16 && nowhere_next == 0 && whole(next, 64, group_pos, group_first);
+                if (direct) direct_tile(buf ^ 1, off);
+                else if (HELD != BF16) load_tile(off);
+                slot = entry_of(span.real(v + 128));
+            }
+            uint64_t wrong = nowhere;       // invalid entries: tokens past the run's end are none
+            if (t + 64 > end) wrong &= (1ull << (end - t)) - 1;
+            if (wrong) wrong &= __ballot(t + lane < a.sinks || t + lane > group_pos - a.window);     // of tokens that some row sees
+            if (wrong && wave == 0 && lane == 0) atomicOr(a.err, DEVERR_TABLE);
+            const int th = t + 32 * mine;
+            // no row of the wave sees any of it
+            const bool past = th > wave_last || (th + 32 * HALVES <= wave_pos - a.window + 1 && th >= a.sinks);
+            if (wave_live && !past) {
+                float x[HALVES][16];
+                const char* const kt = lds + buf * T::kTile + (HALVES == 1 ? 32 * mine * T::kRow : 0);
+                const char* const vt = kt + 2 * T::kTile;
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    f32x16_t acc = f32x16_t{};
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        const bf16x8_t key = __builtin_bit_cast(
+                            bf16x8_t, *reinterpret_cast<const u32x4_t*>(kt + (k_from ^ (32 * k)) + 32 * h * T::kRow));
+                        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) x[h][y] = acc[y];
+                }
+                if (nowhere != 0 || !whole(th, 32 * HALVES, wave_pos, wave_first)) {
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) {
+                        const uint32_t dead = (uint32_t)(nowhere >> (32 * (h + mine)));
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) {
+                            const int in = y % 4 + 8 * (y / 4) + 4 * f, tok = th + 32 * h + in;
+                            const bool sees = ((dead >> in) & 1) == 0 && tok <= pos && (tok >= first || tok < a.sinks);
+                            x[h][y] = sees ? x[h][y] : -INFINITY;
+                        }
+                    }
+                }
+                float tile_top = kLowest;
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                    for (int y = 0; y < 16; y += 2) tile_top = max3(tile_top, x[h][y], x[h][y + 1]);
+                tile_top *= scale;
+                if (__ballot(tile_top > m + 8.f)) {
+                    const float m_new = fmaxf(m, max_over_f(tile_top));
+                    const float alpha = exp2_of(m - m_new);
+                    m = m_new;
+                    l *= alpha;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) o[d] *= alpha;
+                }
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float* const w = x[h] + 8 * y;
+                        float part_l[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            w[e] = exp2_of(__builtin_fmaf(w[e], scale, -m));
+                            part_l[e / 4] += w[e];
+                        }
+                        l += part_l[0] + part_l[1];
+                        u32x4_t wh;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) wh[e] = bf16_pair(w[2 * e], w[2 * e + 1]);
+                        // 8 tokens' values of one d: two transpose reads
+                        bf16x8_t val[DT];
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) {
+                            struct { i16x4_t p[2]; } both;
+#pragma unroll
+                            for (int z = 0; z < 2; ++z)
+                                both.p[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                    (lds_i16x4_t*)(vt + (v_from ^ (64 * d)) + (32 * h + 16 * y + 8 * z) * T::kRow));
+                            val[d] = __builtin_bit_cast(bf16x8_t, both);
+                        }
+#pragma unroll
+                        for (int d = 0; d < DT; ++d)
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val[d], __builtin_bit_cast(bf16x8_t, wh), o[d], 0, 0, 0);
+                    }
+            }
+            if (direct) {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // in LDS before the barrier
+            } else if (more) {
+                if (HELD == BF16) load_tile(off);
+                store_tile(buf ^ 1, next, nowhere_next);
+            }
+            nowhere = nowhere_next;
+            __syncthreads();
+        }
+    };
+    if (pairs) walk(std::integral_constant<int, 1>(), wave % 2);
+    else walk(std::integral_constant<int, 2>(), 0);
+
+    l = sum_over_f(l);
+    bool lost = false;
+    if constexpr (HELD == BF16) {
+        float x = 0.f;      // NaN where a sum is not finite
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int y = 0; y < 16; ++y) x = __builtin_fmaf(o[d][y], 0.f, x);
+        lost = x != 0.f && l == l;
+    }
+    if (__ballot(lost) != 0 || any_odd) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            float sum[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) sum[y] = 0.f;
+            for (int v = v0; v < v1; ++v) {
+                if (pairs && (v - v0) / 32 % 2 != wave % 2) continue;       // the other wave's half
+                const int tok = span.real(v);
+                const char* const from = value_row<HELD>(a, bs, s, kvh, tok);
+                if (from && tok <= pos && (tok >= first || tok < a.sinks)) {
+#pragma unroll
+                    for (int y = 0; y < 16; y += 4) add_not_finite<HELD>(sum + y, from, 32 * d + 2 * y + 4 * f);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[d][y] = sum[y] == 0.f ? o[d][y] : sum[y];
+        }
+    }
+    if (pairs) {
+        // the pair's sums, through the (now unused) stage
+        float* const x = reinterpret_cast<float*>(lds) + (wave / 2) * (16 * DT + 2) * 64;
+        if (wave % 2) {
+            x[lane] = m;
+            x[64 + lane] = l;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int y = 0; y < 16; ++y) x[(2 + 16 * d + y) * 64 + lane] = o[d][y];
+        }
+        __syncthreads();
+        if (wave % 2) return;
+        const float m_other = x[lane], m_new = fmaxf(m, m_other);
+        const float mine = exp2_of(m - m_new), other = exp2_of(m_other - m_new);
+        l = l * mine + x[64 + lane] * other;
+        m = m_new;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[d][y] = joined(o[d][y], mine, x[(2 + 16 * d + y) * 64 + lane], other);
+    }
+    if (pairs && runs == 1) {       // rows that no wave of the pairs has: past the last live one
+        const int from = (int)group_r0 + 64, to = (int)group_r0 + pl.rows < R ? (int)group_r0 + pl.rows : R;
+        for (int x = (wave / 2) * 64 + lane; x < (to - from) * (D / 8); x += 128) {
+            const int y = from + x / (D / 8), d = x % (D / 8) * 8;
+            const int64_t at = ((int64_t)s * a.M + y / g) * a.Hq + kvh * g + y % g;
+            *reinterpret_cast<u32x4_t*>(a.out + at * D + d) = u32x4_t{0, 0, 0, 0};
+            if (a.lse && d == 0) a.lse[at] = -INFINITY;
+        }
+    }
+    if (r >= R || in_group + n >= pl.rows) return;
+    const bool none = !live || l == 0.f;
+    if (runs == 1) {
+        const float inv = none ? 0.f : a.cache.v_scale / l;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                uint2 w = make_uint2(bf16_pair(o[d][4 * y] * inv, o[d][4 * y + 1] * inv),
+                                     bf16_pair(o[d][4 * y + 2] * inv, o[d][4 * y + 3] * inv));
+                if (none) w = make_uint2(0, 0);
+                *reinterpret_cast<uint2*>(a.out + row * D + 32 * d + 8 * y + 4 * f) = w;
+            }
+        if (a.lse && f == 0) a.lse[row] = none ? -INFINITY : (m + log2_of(l)) * kLn2;
+    } else if (live) {
+        float* const to = part_sums(a, pl, it.slot) + (in_group + n) * D;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                *reinterpret_cast<float4*>(to + 32 * d + 8 * y + 4 * f) =
+                    make_float4(o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]);
+        if (f == 0) part_stats(a, pl, it.slot)[in_group + n] = make_float2(m, l);
+    }
+}
+
+}  // namespace
+
+template <int D, Held HELD>
+void launch_chunk(const AttendArgs& a, const Plan& pl, const BlockSize& bs, uint32_t grid, hipStream_t stream) {
+    attend_chunk_kernel<D, HELD><<<grid, 256, 0, stream>>>(a, pl, bs);
+}
+template void launch_chunk<64, BF16>(const AttendArgs&, const Plan&, const BlockSize&, uint32_t, hipStream_t);
+template void launch_chunk<64, FP8>(const AttendArgs&, const Plan&, const BlockSize&, uint32_t, hipStream_t);
+template void launch_chunk<64, FP4>(const AttendArgs&, const Plan&, const BlockSize&, uint32_t, hipStream_t);
+template void launch_chunk<128, BF16>(const AttendArgs&, const Plan&, const BlockSize&, uint32_t, hipStream_t);
+template void launch_chunk<128, FP8>(const AttendArgs&, const Plan&, const BlockSize&, uint32_t, hipStream_t);
+template void launch_chunk<128, FP4>(const AttendArgs&, const Plan&, const BlockSize&, uint32_t, hipStream_t);
+
+}  // namespace attend
+}  // namespace pred

@@ -87,4 +87,8 @@ def test_null_handle_is_refused_before_any_device_work():
                                       None) == rk.PRED_ERR_NULL_ARG
     assert lib.pred_store(None, 1, 64, 1, 64, 1, 1, c, None) == rk.PRED_ERR_NULL_ARG
     assert lib.pred_load(None, c, 1, 1, 1, 1, None) == rk.PRED_ERR_NULL_ARG
+    assert lib.pred_attend_window(None, c, 1, 1, None, 1, 1, None, None, 4, 1, 1.0, 1, None, None, 0,
+                                  None) == rk.PRED_ERR_NULL_ARG
+    assert lib.pred_attend_window_workspace_bytes(None, 1, 1, 1, 4, 1) == 0
+    assert lib.pred_attend_window_kernel_name(None, c, 1) is None
     assert "NULL" in rk.pred_last_error()
