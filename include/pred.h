@@ -485,7 +485,7 @@ int pred_norm_rotate_backward(pred_t* p, const pred_norm* norm, const pred_rope*
                               const pred_bf16* dy, int64_t dy_stride, pred_bf16* dx, int64_t dx_stride, float* dweight,
                               void* workspace, size_t ws_bytes, void* stream);
 
-/* Workspace of pred_norm_rotate_backward with dweight, at most 4096 * head_dim
+/* Workspace of pred_norm_rotate_backward with dweight, at most 1024 * head_dim
  * bytes; 0 for a NULL handle or counts < 1.  Calls that may run at the same time
  * need workspaces of their own. */
 size_t pred_norm_rotate_workspace_bytes(pred_t* p, int64_t n_tokens, int32_t n_heads);

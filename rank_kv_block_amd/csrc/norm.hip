@@ -22,8 +22,14 @@
 namespace pred {
 namespace {
 
-// Heads a wave has in flight at once for each of its places.
-constexpr int kNormHeads = 4;
+// Neighbouring tokens of a 4-bit cache lie in one line, and so do their scales: an XCD (b % 8) takes consecutive
+// workgroups, so that its L2 gathers them.  The grid is a multiple of 8.
+__device__ inline uint32_t xcd_order(uint32_t b, uint32_t grid) { return b % 8 * (grid / 8) + b / 8; }
+
+// Heads a wave has in flight at once for each of its places (2048 tokens of 48
+// heads of 128, four of them side by side in a wave: 14.1 us with 6, 15.8 with 3,
+// 16.5 with 4, 16.3 with 12).
+constexpr int kNormHeads = 6;
 
 // A wave takes one token: a lane holds 8 consecutive values (a piece) of a head,
 // D / 8 lanes a head, heads side by side.  Half a rotation apart is another
@@ -47,30 +53,69 @@ __device__ inline float sum_of_head(float v, int pieces, int first) {
     }
 }
 
+// What a wave keeps in LDS: the cosines and sines of its token's pairs, each
+// worked out by one lane (every lane its own: 20 us instead of 14 for 2048
+// tokens of 32 + 8 + 8 heads, 110 instead of 78 for the gradient), and the
+// values that two lanes of a head exchange.
+constexpr int kPairs = 256;         // of a head of 512
+struct WaveLds {
+    float c[kPairs], s[kPairs];
+    float row[512];                 // 64 lanes of 8
+};
+
+__device__ inline void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// By all 64 lanes.
+__device__ inline void set_angles(const RopeArgs& a, int64_t pos, WaveLds& lds, int lane) {
+    for (int p = lane; p < a.rot / 2; p += 64) {
+        const CosSin cs = cos_sin(a, pos, p);
+        lds.c[p] = cs.c;
+        lds.s[p] = cs.s;
+    }
+    wave_sync();
+}
+
+__device__ inline void read8(const float* from, float* x) {
+    const float4 lo = *reinterpret_cast<const float4*>(from), hi = *reinterpret_cast<const float4*>(from + 4);
+    x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+}
+
 // The cosines and sines of a lane's 8 values: of pairs (2 i, 2 i + 1) if INTER,
 // else of each value, with the sine's sign.
 template <bool INTER>
 struct Angles {
     float c[INTER ? 4 : 8], s[INTER ? 4 : 8];
 
-    __device__ inline void set(const RopeArgs& a, int64_t pos, int d0) {
-        const int half = a.rot / 2;
+    __device__ inline void get(const WaveLds& lds, int rot, int d0) {
+        const int half = rot / 2;
+        if constexpr (INTER) {
 #pragma unroll
-        for (int j = 0; j < (INTER ? 4 : 8); ++j) {
-            const int d = INTER ? d0 + 2 * j : d0 + j;
-            c[j] = 1.f;
-            s[j] = 0.f;
-            if (d < a.rot) {
-                const CosSin cs = cos_sin(a, pos, INTER ? d / 2 : (d < half ? d : d - half));
-                c[j] = cs.c;
-                s[j] = INTER || d >= half ? cs.s : -cs.s;
+            for (int j = 0; j < 4; ++j) {
+                const int p = d0 / 2 + j < half ? d0 / 2 + j : 0;
+                c[j] = lds.c[p];
+                s[j] = lds.s[p];
+            }
+        } else if (rot % 16 == 0) {     // a piece's pairs are a piece
+            const int p = d0 >= rot ? 0 : (d0 < half ? d0 : d0 - half);
+            read8(lds.c + p, c);
+            read8(lds.s + p, s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] = d0 < half ? -s[j] : s[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int d = d0 + j, p = d >= rot ? 0 : (d < half ? d : d - half);
+                c[j] = lds.c[p];
+                s[j] = d < half ? -lds.s[p] : lds.s[p];
             }
         }
     }
 
-    // x turned; `row`: a place for the wave's 64 x 8 values, `first` the head's first lane.  Every lane of the head
-    // calls it.
-    __device__ inline void turn(float* x, int rot, int d0, float* row, int lane, int first) const {
+    // x turned; `first` is the head's first lane.  Every lane of the head calls it.
+    __device__ inline void turn(float* x, int rot, int d0, WaveLds& lds, int lane, int first) const {
         if constexpr (INTER) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -80,26 +125,22 @@ struct Angles {
                 x[2 * j + 1] = u * s[j] + w * c[j];
             }
         } else {
-            float4* const mine = reinterpret_cast<float4*>(row + 8 * lane);
+            float4* const mine = reinterpret_cast<float4*>(lds.row + 8 * lane);
             mine[0] = make_float4(x[0], x[1], x[2], x[3]);
             mine[1] = make_float4(x[4], x[5], x[6], x[7]);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
             const int half = rot / 2;
             float y[8];
-            if (rot % 16 == 0) {        // a piece's partners are a piece
-                const int at = 8 * first + (d0 >= rot ? d0 : (d0 < half ? d0 + half : d0 - half));
-                const float4 lo = *reinterpret_cast<const float4*>(row + at), hi = *reinterpret_cast<const float4*>(row + at + 4);
-                y[0] = lo.x, y[1] = lo.y, y[2] = lo.z, y[3] = lo.w, y[4] = hi.x, y[5] = hi.y, y[6] = hi.z, y[7] = hi.w;
+            if (rot % 16 == 0) {        // and its partners
+                read8(lds.row + 8 * first + (d0 >= rot ? d0 : (d0 < half ? d0 + half : d0 - half)), y);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int d = d0 + j;
-                    y[j] = row[8 * first + (d >= rot ? d : (d < half ? d + half : d - half))];
+                    y[j] = lds.row[8 * first + (d >= rot ? d : (d < half ? d + half : d - half))];
                 }
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            wave_sync();
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (d0 + j < rot) x[j] = x[j] * c[j] + y[j] * s[j];
@@ -160,17 +201,17 @@ __device__ inline const uint16_t* head_in(const RopeArgs& a, int64_t t, int h) {
 }
 
 template <int PIECES, bool INTER>
-__global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs n, int pieces_any, int chunks) {
-    __shared__ __attribute__((aligned(16))) float exchange[INTER ? 1 : 4][INTER ? 1 : 512];
+__global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs n, int pieces_any, int chunks, int deep) {
+    __shared__ __attribute__((aligned(16))) WaveLds all_lds[4];
     const RopeArgs& a = n.rows;
     const int pieces = PIECES ? PIECES : pieces_any;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + wave, t = unit / chunks;
+    const int64_t unit = (int64_t)xcd_order(blockIdx.x, gridDim.x) * 4 + wave, t = unit / chunks;
     if (t >= a.n_tokens) return;
     const int at_once = 64 / pieces, piece = lane % pieces, first = lane - piece, d0 = 8 * piece;
-    const int heads = a.Hq + 2 * a.Hk, h0 = (int)(unit % chunks) * at_once * kNormHeads + lane / pieces;
-    if (lane / pieces >= at_once) return;
-    float* const row = exchange[INTER ? 0 : wave];
+    const int heads = a.Hq + 2 * a.Hk, h0 = (int)(unit % chunks) * at_once * deep + lane / pieces;
+    WaveLds& lds = all_lds[wave];
+    const bool place = lane / pieces < at_once;
     const int64_t cache_off = token_offset(a, t);
 
     u32x4_t in[kNormHeads];
@@ -178,10 +219,12 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs n, int pieces
     for (int i = 0; i < kNormHeads; ++i) {
         const int h = h0 + i * at_once;
         in[i] = u32x4_t{0, 0, 0, 0};
-        if (h < heads) in[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(head_in(a, t, h) + d0));
+        if (i < deep && h < heads && place) in[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(head_in(a, t, h) + d0));
     }
+    if (a.rot) set_angles(a, a.positions[t], lds, lane);
+    if (!place) return;
     Angles<INTER> angles;
-    if (a.rot && h0 < a.Hq + a.Hk) angles.set(a, a.positions[t], d0);
+    if (a.rot) angles.get(lds, a.rot, d0);
     float qw[8], kw[8];
     if (n.q.on) load_weight(n.q, d0, qw);
     if (n.k.on) load_weight(n.k, d0, kw);
@@ -189,7 +232,7 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs n, int pieces
 #pragma unroll
     for (int i = 0; i < kNormHeads; ++i) {
         const int h = h0 + i * at_once;
-        if (h >= heads) continue;
+        if (i >= deep || h >= heads) continue;
         const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hk;
         float x[8];
         unpack8(in[i], x);
@@ -209,7 +252,7 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs n, int pieces
                 for (int j = 0; j < 8; ++j) x[j] *= r * kw[j];
             }
         }
-        if (a.rot && (is_q || is_k)) angles.turn(x, a.rot, d0, row, lane, first);
+        if (a.rot && (is_q || is_k)) angles.turn(x, a.rot, d0, lds, lane, first);
         if (is_q) {
             store8(x, a.out + t * a.out_stride + (int64_t)h * a.D, d0, false, 1.f);
         } else if (cache_off >= 0) {
@@ -225,45 +268,51 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(NormArgs n, int pieces
     }
 }
 
-// The gradient.  A wave walks (token, head) units a fixed distance apart; a lane
-// keeps the sums of g h of its 8 places, and a workgroup's come together in
-// LDS: `part` gets a row of D a workgroup, which a second launch adds in a fixed
-// order, so equal inputs give equal bits.
+// The gradient.  A workgroup a CU, of kGradWaves waves; a wave walks (token,
+// heads) units a fixed distance apart, a lane keeps the sums of g h of its 8
+// places, and a workgroup's come together in LDS: `part` gets a row of D a
+// workgroup, which a second launch adds in a fixed order, so equal inputs give
+// equal bits.
+constexpr int kGradWaves = 16;
+constexpr int kGradHeads = 2;        // as kNormHeads (78 us with 4, 76 with 2 and with 1)
+
 template <int PIECES, bool INTER>
-__global__ __launch_bounds__(256) void norm_rotate_backward_kernel(NormGradArgs n, int pieces_any, int chunks) {
-    __shared__ __attribute__((aligned(16))) float exchange[4][512];
+__global__ __launch_bounds__(64 * kGradWaves) void norm_rotate_backward_kernel(NormGradArgs n, int pieces_any, int chunks) {
+    __shared__ __attribute__((aligned(16))) WaveLds all_lds[kGradWaves];
     const RopeArgs& a = n.rows;
     const int pieces = PIECES ? PIECES : pieces_any;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int at_once = 64 / pieces, piece = lane % pieces, first = lane - piece, d0 = 8 * piece;
-    float* const row = exchange[wave];
+    WaveLds& lds = all_lds[wave];
     float acc[8], w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.f;
     const bool place = lane / pieces < at_once;
     if (place) load_weight(n.norm, d0, w);
-    for (int64_t unit = (int64_t)blockIdx.x * 4 + wave; unit < a.n_tokens * chunks && place; unit += (int64_t)gridDim.x * 4) {
+    const uint32_t units = (uint32_t)(a.n_tokens * chunks);
+    for (uint32_t unit = blockIdx.x * kGradWaves + wave; unit < units; unit += gridDim.x * kGradWaves) {
         const int64_t t = unit / chunks;
-        const int h0 = (int)(unit % chunks) * at_once * kNormHeads + lane / pieces;
-        u32x4_t xs[kNormHeads], gs[kNormHeads];
+        const int h0 = (int)(unit % chunks) * at_once * kGradHeads + lane / pieces;
+        u32x4_t xs[kGradHeads], gs[kGradHeads];
 #pragma unroll
-        for (int i = 0; i < kNormHeads; ++i) {
+        for (int i = 0; i < kGradHeads; ++i) {
             const int h = h0 + i * at_once;
             xs[i] = gs[i] = u32x4_t{0, 0, 0, 0};
-            if (h >= a.Hq) continue;
+            if (h >= a.Hq || !place) continue;
             xs[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(a.q + t * a.q_stride + (int64_t)h * a.D + d0));
             gs[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(n.dy + t * n.dy_stride + (int64_t)h * a.D + d0));
         }
+        if (a.rot) set_angles(a, a.positions[t], lds, lane);
         Angles<INTER> angles;
-        if (a.rot) angles.set(a, a.positions[t], d0);
+        if (a.rot) angles.get(lds, a.rot, d0);
 #pragma unroll
-        for (int i = 0; i < kNormHeads; ++i) {
+        for (int i = 0; i < kGradHeads; ++i) {
             const int h = h0 + i * at_once;
-            if (h >= a.Hq) continue;
+            if (h >= a.Hq || !place) continue;
             float x[8], g[8];
             unpack8(xs[i], x);
             unpack8(gs[i], g);
-            if (a.rot) angles.turn(g, a.rot, d0, row, lane, first);
+            if (a.rot) angles.turn(g, a.rot, d0, lds, lane, first);
             float ss = 0.f, ux = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -284,72 +333,100 @@ __global__ __launch_bounds__(256) void norm_rotate_backward_kernel(NormGradArgs 
         }
     }
     if (!n.dweight) return;
-    float4* const mine = reinterpret_cast<float4*>(row + 8 * lane);
+    float4* const mine = reinterpret_cast<float4*>(lds.row + 8 * lane);
     __syncthreads();
     mine[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     mine[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
     __syncthreads();
-    for (int d = threadIdx.x; d < a.D; d += 256) {
+    for (int d = threadIdx.x; d < a.D; d += 64 * kGradWaves) {
         float sum = 0.f;
-        for (int v = 0; v < 4; ++v)
-            for (int i = 0; i < at_once; ++i) sum += exchange[v][8 * (i * pieces) + d];
+        for (int v = 0; v < kGradWaves; ++v)
+            for (int i = 0; i < at_once; ++i) sum += all_lds[v].row[8 * (i * pieces) + d];
         n.part[(int64_t)blockIdx.x * a.D + d] = sum;
     }
 }
 
-// dweight [D]: 16 columns a workgroup, 16 threads a column.
-__global__ __launch_bounds__(256) void norm_weight_kernel(const float* part, int64_t parts, int D, float* dweight) {
-    __shared__ float sums[16][17];
+// dweight [D]: 16 columns a workgroup, 64 threads a column.
+__global__ __launch_bounds__(1024) void norm_weight_kernel(const float* part, int parts, int D, float* dweight) {
+    __shared__ float sums[64][17];
     const int d = blockIdx.x * 16 + threadIdx.x % 16, lane = threadIdx.x / 16;
     float sum = 0.f;
-    if (d < D)
-        for (int64_t i = lane; i < parts; i += 16) sum += part[i * D + d];
+    if (d < D) {
+#pragma unroll 4
+        for (int i = lane; i < parts; i += 64) sum += part[(int64_t)i * D + d];
+    }
     sums[lane][threadIdx.x % 16] = sum;
     __syncthreads();
     if (lane != 0 || d >= D) return;
-    for (int i = 1; i < 16; ++i) sum += sums[i][threadIdx.x];
+    for (int i = 1; i < 64; ++i) sum += sums[i][threadIdx.x];
     dweight[d] = sum;
 }
 
-// A lane 8 values of a cached token's head.
-__global__ __launch_bounds__(256) void load_kernel(LoadArgs a, int pieces) {
-    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x, per = (int64_t)2 * a.Hk * pieces, t = item / per;
+// A wave a token (or one of `parts` of a token), a lane 8 values of a head at a time, kLoads of them in flight.
+constexpr int kLoads = 4;
+
+__global__ __launch_bounds__(256) void load_kernel(LoadArgs a, int pieces, int parts) {
+    const int64_t unit = (int64_t)xcd_order(blockIdx.x, gridDim.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = unit / parts;
+    const int part = (int)(unit % parts);
     if (t >= a.n_tokens) return;
-    const int in = (int)(item % per), d0 = in % pieces * 8, h = in / pieces % a.Hk;
-    const bool is_k = in < a.Hk * pieces;
+    const int lane = threadIdx.x & 63;
     const int64_t slot = a.slots[t];
     if (slot < 0 || slot >= a.N * a.B) {
-        if (slot != -1 && in == 0) atomicOr(a.err, DEVERR_SLOT);
+        if (slot != -1 && lane == 0 && part == 0) atomicOr(a.err, DEVERR_SLOT);
         return;
     }
-    const int64_t off = slot / a.B * a.cache.block_stride + slot % a.B * a.cache.token_stride + h * a.cache.head_stride + d0;
-    const void* const from = is_k ? a.cache.k : a.cache.v;
-    u32x4_t w;
-    if (a.cache.fp4) {
-        const int bits = *reinterpret_cast<const int*>(static_cast<const uint8_t*>(from) + off / 2);
-        const float scale = __uint_as_float((uint32_t)(is_k ? a.cache.k_scales : a.cache.v_scales)[off / 32] << 23);
-        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(bits, scale, 0));
-        w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(bits, scale, 1));
-        w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(bits, scale, 2));
-        w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(bits, scale, 3));
-    } else if (a.cache.fp8) {
-        const uint2 bits = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(from) + off);
-        const float scale = is_k ? a.cache.k_scale : a.cache.v_scale;
-        auto pair = [&](uint32_t word, auto hi) {
-            const auto v = __builtin_amdgcn_cvt_pk_f32_fp8((int)word, decltype(hi)::value);
-            return pack2(v[0] * scale, v[1] * scale);
-        };
-        w[0] = pair(bits.x, std::false_type());
-        w[1] = pair(bits.x, std::true_type());
-        w[2] = pair(bits.y, std::false_type());
-        w[3] = pair(bits.y, std::true_type());
-    } else {
-        w = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(from) + off);
+    const int64_t token = slot / a.B * a.cache.block_stride + slot % a.B * a.cache.token_stride;
+    const int items = 2 * a.Hk * pieces;
+    for (int x0 = 64 * part + lane; x0 < items; x0 += 64 * kLoads * parts) {
+        u32x4_t w[kLoads];
+        uint32_t scale[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int x = x0 + 64 * parts * i;
+            if (x >= items) continue;
+            const int y = x / pieces, h = y < a.Hk ? y : y - a.Hk;
+            const void* const from = y < a.Hk ? a.cache.k : a.cache.v;
+            const int64_t off = token + h * a.cache.head_stride + x % pieces * 8;
+            if (a.cache.fp4) {
+                w[i][0] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(from) + off / 2);
+                scale[i] = (y < a.Hk ? a.cache.k_scales : a.cache.v_scales)[off / 32];
+            } else if (a.cache.fp8) {
+                const uint2 both = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(from) + off);
+                w[i][0] = both.x;
+                w[i][1] = both.y;
+            } else {
+                w[i] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(from) + off);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int x = x0 + 64 * parts * i;
+            if (x >= items) continue;
+            const int y = x / pieces, h = y < a.Hk ? y : y - a.Hk;
+            if (a.cache.fp4) {
+                const float f = __uint_as_float(scale[i] << 23);
+                const uint32_t bits = w[i][0];
+                w[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(bits, f, 0));
+                w[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(bits, f, 1));
+                w[i][2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(bits, f, 2));
+                w[i][3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(bits, f, 3));
+            } else if (a.cache.fp8) {
+                const float f = y < a.Hk ? a.cache.k_scale : a.cache.v_scale;
+                auto pair = [&](uint32_t word, auto hi) {
+                    const auto v = __builtin_amdgcn_cvt_pk_f32_fp8((int)word, decltype(hi)::value);
+                    return pack2(v[0] * f, v[1] * f);
+                };
+                w[i] = u32x4_t{pair(w[i][0], std::false_type()), pair(w[i][0], std::true_type()),
+                               pair(w[i][1], std::false_type()), pair(w[i][1], std::true_type())};
+            }
+            __builtin_nontemporal_store(w[i], reinterpret_cast<u32x4_t*>((y < a.Hk ? a.k_out : a.v_out) +
+                                                                         (t * a.Hk + h) * a.D + x % pieces * 8));
+        }
     }
-    *reinterpret_cast<u32x4_t*>((is_k ? a.k_out : a.v_out) + (t * a.Hk + h) * a.D + d0) = w;
 }
 
-int heads_a_wave(int D) { return 64 / (D / 8) * kNormHeads; }
+int heads_a_wave(int D, int at_once) { return 64 / (D / 8) * at_once; }
 
 // fn(lanes of a head where one of the variants has them, pairs side by side or not)
 template <typename F>
@@ -367,45 +444,55 @@ void norm_variant(int pieces, bool inter, F fn) {
 }  // namespace
 
 hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t stream) {
-    const int heads = a.rows.Hq + 2 * a.rows.Hk, per = heads_a_wave(a.rows.D), chunks = (heads + per - 1) / per;
-    if (a.rows.n_tokens > (0x7FFFFFFFll * 4 - 3) / chunks) return hipErrorInvalidConfiguration;
-    const uint32_t grid = (uint32_t)((a.rows.n_tokens * chunks + 3) / 4);
-    const int pieces = a.rows.D / 8;
+    const int heads = a.rows.Hq + 2 * a.rows.Hk, pieces = a.rows.D / 8;
+    // kNormHeads heads for each place of a wave, which share its angles and have their loads in flight together, or one
+    // where that would give no more waves than the chip has SIMDs: 48 heads of 128 of 64 tokens 4.9 us with one, 7.8 with
+    // six; 512 tokens 8.5 and 8.3, 2048 24.7 and 12.5; 16 heads into 4 bits without a rotation, 64 tokens 3.9 and 5.2,
+    // 1024 5.0 and 5.5, 4096 11.4 and 8.3
+    auto chunks_of = [&](int deep) { return (heads + heads_a_wave(a.rows.D, deep) - 1) / heads_a_wave(a.rows.D, deep); };
+    const int deep = a.rows.n_tokens * chunks_of(kNormHeads) <= 1024 ? 1 : kNormHeads, chunks = chunks_of(deep);
+    if (a.rows.n_tokens > 0x7FFFFFF0ll * 4 / chunks) return hipErrorInvalidConfiguration;
+    const uint32_t grid = (uint32_t)((a.rows.n_tokens * chunks + 31) / 32 * 8);
     norm_variant(pieces, a.rows.interleaved || !a.rows.rot, [&](auto p, auto inter) {
-        norm_rotate_kernel<decltype(p)::value, decltype(inter)::value><<<grid, 256, 0, stream>>>(a, pieces, chunks);
+        norm_rotate_kernel<decltype(p)::value, decltype(inter)::value><<<grid, 256, 0, stream>>>(a, pieces, chunks, deep);
     });
     return hipGetLastError();
 }
 
-// Workgroups of the gradient: up to 1024, four for each of 256 CUs, so that
-// their rows of sums stay few; a wave each unit below that.
+// Workgroups of the gradient, each with a row of sums: one for each of 256 CUs
+// (its waves fill a CU), a wave each unit below that.
 int64_t norm_grad_parts(int64_t n_tokens, int n_heads, int D) {
-    const int per = heads_a_wave(D), chunks = (n_heads + per - 1) / per;
-    const int64_t units = n_tokens > (1ll << 40) ? (1ll << 40) : n_tokens * chunks, groups = (units + 3) / 4;
-    return groups < 1024 ? groups : 1024;
+    const int per = heads_a_wave(D, kGradHeads), chunks = (n_heads + per - 1) / per;
+    const int64_t units = n_tokens > (1ll << 40) ? (1ll << 40) : n_tokens * chunks;
+    const int64_t groups = (units + kGradWaves - 1) / kGradWaves;
+    return groups < 256 ? groups : 256;
 }
 
 hipError_t launch_norm_rotate_backward(const NormGradArgs& a, hipStream_t stream) {
-    const int heads = a.rows.Hq, per = heads_a_wave(a.rows.D), chunks = (heads + per - 1) / per, pieces = a.rows.D / 8;
-    if (a.rows.n_tokens > (0x7FFFFFFFll * 4 - 3) / (chunks > 0 ? chunks : 1)) return hipErrorInvalidConfiguration;
+    const int heads = a.rows.Hq, per = heads_a_wave(a.rows.D, kGradHeads), chunks = (heads + per - 1) / per, pieces = a.rows.D / 8;
+    if (a.rows.n_tokens > 0x7FFFFFFFll / (chunks > 0 ? chunks : 1)) return hipErrorInvalidConfiguration;
     const int64_t parts = norm_grad_parts(a.rows.n_tokens, heads, a.rows.D);
     if (parts > 0) {
         norm_variant(pieces, a.rows.interleaved || !a.rows.rot, [&](auto p, auto inter) {
             norm_rotate_backward_kernel<decltype(p)::value, decltype(inter)::value>
-                <<<(uint32_t)parts, 256, 0, stream>>>(a, pieces, chunks);
+                <<<(uint32_t)parts, 64 * kGradWaves, 0, stream>>>(a, pieces, chunks);
         });
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (!a.dweight) return hipSuccess;
-    norm_weight_kernel<<<(a.rows.D + 15) / 16, 256, 0, stream>>>(a.part, parts, a.rows.D, a.dweight);
+    norm_weight_kernel<<<(a.rows.D + 15) / 16, 1024, 0, stream>>>(a.part, (int)parts, a.rows.D, a.dweight);
     return hipGetLastError();
 }
 
 hipError_t launch_load(const LoadArgs& a, hipStream_t stream) {
-    const int64_t per = (int64_t)2 * a.Hk * (a.D / 8);
-    if (a.n_tokens > (0x7FFFFFFFll * 256 - 255) / per) return hipErrorInvalidConfiguration;
-    load_kernel<<<(uint32_t)((a.n_tokens * per + 255) / 256), 256, 0, stream>>>(a, a.D / 8);
+    // a wave a token, or where these are few one for each 64 of its pieces: 16 heads of 128 in 4 bits, 64 tokens 3.3 us in
+    // parts and 4.9 without, 1024 4.3 and 5.3, 2048 5.7 and 5.6, 4096 7.6 and 6.9
+    const int pieces = a.D / 8, all = (2 * a.Hk * pieces + 63) / 64, parts = a.n_tokens < 2048 ? all : 1;
+    if (a.n_tokens > 0x7FFFFFF0ll * 4) return hipErrorInvalidConfiguration;
+    const int64_t grid = (a.n_tokens * parts + 31) / 32 * 8;
+    if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
+    load_kernel<<<(uint32_t)grid, 256, 0, stream>>>(a, pieces, parts);
     return hipGetLastError();
 }
 
