@@ -1448,8 +1448,10 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
     pl.rounds = most < 1 ? 1 : (most < kRounds ? (int)most : kRounds);
     if (pl.chunk) {
         pl.rounds = 1;
-        // groups that fill the chip as they are keep their tokens in one run (unit above any number of tokens)
-        if ((int64_t)a.S * a.Hk * pl.groups >= 4ll * pl.slots) pl.unit = 1 << 30;
+        // Groups that fill the chip keep their tokens in one run (unit above any number of tokens), unless some may walk
+        // much longer than others.
+        const int64_t items = (int64_t)a.S * a.Hk * pl.groups;
+        if (a.S == 1 ? items >= pl.slots : items >= 2ll * pl.slots && most_tokens(a, pl) <= 8192) pl.unit = 1 << 30;
     }
     return pl;
 }
