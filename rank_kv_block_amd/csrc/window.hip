@@ -117,24 +117,63 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
     };
     const int my_tok = threadIdx.x / CR, my_piece = threadIdx.x % CR;     // and tokens 256 / CR further on
     const bool mine_in = 256 / CR * NR <= 64 || my_tok < 64;     // (64 values in 4 bits: half of the threads have a piece)
+    // Keys and values of different tiles are on their way at a time.  `off` is where lane x's token lies (token x of the
+    // tile).
     u32x4_t ks[NR], vs[NR];
     uint32_t k_sc[NR], v_sc[NR];        // a piece's scale byte
-    auto load_tile = [&](int64_t off) {
+    auto place_of = [&](int64_t off, int x) -> int64_t {
+        const int from = my_tok + 256 / CR * x;
+        return (int64_t)__shfl((int)(off >> 32), from) << 32 | (uint32_t)__shfl((int)off, from);
+    };
+    auto load_keys = [&](int64_t off) {
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
-            const int from = my_tok + 256 / CR * x;
-            const int64_t o = ((int64_t)__shfl((int)(off >> 32), from) << 32 | (uint32_t)__shfl((int)off, from)) +
-                              16 * my_piece;
+            const int64_t o = place_of(off, x) + 16 * my_piece;
             ks[x] = *reinterpret_cast<const u32x4_t*>(kp + o);
+            if constexpr (HELD == FP4) k_sc[x] = a.cache.k_scales[(head_off + o) >> 4];
+        }
+    };
+    auto load_values = [&](int64_t off) {
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            const int64_t o = place_of(off, x) + 16 * my_piece;
             vs[x] = *reinterpret_cast<const u32x4_t*>(vp + o);
+            if constexpr (HELD == FP4) v_sc[x] = a.cache.v_scales[(head_off + o) >> 4];
+        }
+    };
+    // a thread's pieces as bf16 into LDS, `to` its first one's place
+    auto store_pieces = [&](char* tile, int to, const u32x4_t* w, const uint32_t* sc) {
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            constexpr int kStep = 256 / CR * T::kRow;
             if constexpr (HELD == FP4) {
-                k_sc[x] = a.cache.k_scales[(head_off + o) >> 4];
-                v_sc[x] = a.cache.v_scales[(head_off + o) >> 4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    *reinterpret_cast<u32x4_t*>(tile + (to ^ (16 * y)) + x * kStep) = fp4x8_to_bf16(w[x][y], sc[x]);
+            } else if constexpr (HELD == FP8) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    u32x4_t z;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        z[2 * e] = fp8x2_to_bf16<false>(w[x][2 * y + e]);
+                        z[2 * e + 1] = fp8x2_to_bf16<true>(w[x][2 * y + e]);
+                    }
+                    *reinterpret_cast<u32x4_t*>(tile + (to ^ (16 * y)) + x * kStep) = z;
+                }
+            } else {
+                *reinterpret_cast<u32x4_t*>(tile + to + x * kStep) = w[x];
             }
         }
     };
     const int k_to = T::key(my_tok, SPREAD * my_piece), v_to = T::value(my_tok, SPREAD * my_piece);
-    auto store_tile = [&](int buf, int t, uint64_t nowhere) {
+    char* const keys = lds;
+    char* const values = lds + 2 * T::kTile;
+    auto store_keys = [&](int buf) {
+        if (mine_in) store_pieces(keys + buf * T::kTile, k_to, ks, k_sc);
+    };
+    // t: the tile's first token; a value that not every row sees must be a number (a masked weight is 0)
+    auto store_values = [&](int buf, int t, uint64_t nowhere) {
         if (!mine_in) return;
         if (nowhere != 0 || !whole(t, 64, group_pos, group_first)) {
             bool odd = false;
@@ -158,57 +197,20 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
             }
             if (odd) any_odd = 1;
         }
-        char* const kt = lds + buf * T::kTile;
-        char* const vt = lds + (2 + buf) * T::kTile;
-#pragma unroll
-        for (int x = 0; x < NR; ++x) {
-            constexpr int kStep = 256 / CR * T::kRow;
-            if constexpr (HELD == FP4) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    *reinterpret_cast<u32x4_t*>(kt + (k_to ^ (16 * y)) + x * kStep) = fp4x8_to_bf16(ks[x][y], k_sc[x]);
-                    *reinterpret_cast<u32x4_t*>(vt + (v_to ^ (16 * y)) + x * kStep) = fp4x8_to_bf16(vs[x][y], v_sc[x]);
-                }
-            } else if constexpr (HELD == FP8) {
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    u32x4_t wk, wv;
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        wk[2 * z] = fp8x2_to_bf16<false>(ks[x][2 * y + z]);
-                        wk[2 * z + 1] = fp8x2_to_bf16<true>(ks[x][2 * y + z]);
-                        wv[2 * z] = fp8x2_to_bf16<false>(vs[x][2 * y + z]);
-                        wv[2 * z + 1] = fp8x2_to_bf16<true>(vs[x][2 * y + z]);
-                    }
-                    *reinterpret_cast<u32x4_t*>(kt + (k_to ^ (16 * y)) + x * kStep) = wk;
-                    *reinterpret_cast<u32x4_t*>(vt + (v_to ^ (16 * y)) + x * kStep) = wv;
-                }
-            } else {
-                *reinterpret_cast<u32x4_t*>(kt + k_to + x * kStep) = ks[x];
-                *reinterpret_cast<u32x4_t*>(vt + v_to + x * kStep) = vs[x];
-            }
-        }
+        store_pieces(values + buf * T::kTile, v_to, vs, v_sc);
     };
-    // straight into LDS: a lane fetches the piece that belongs in its place
+    // a bf16 tile straight into LDS: a lane fetches the piece that belongs in its place
     const int k_piece = my_piece ^ (D == 128 ? my_tok & 15 : (my_tok >> 1) & 7);
     const int v_piece = my_piece ^ (D == 128 ? (my_tok & 3) * 4 : ((my_tok >> 1) & 1) * 4);
-    auto direct_load = [&](char* to, const char* from) {
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t*)from,
-                                         (__attribute__((address_space(3))) uint32_t*)to, 16, 0, 0);
-    };
-    auto direct_tile = [&](int buf, int64_t off) {
+    auto direct_tile = [&](char* tile, const char* from, int piece, int64_t off) {
         int64_t at[NR];
 #pragma unroll
-        for (int x = 0; x < NR; ++x) {
-            const int from = my_tok + 256 / CR * x;
-            at[x] = (int64_t)__shfl((int)(off >> 32), from) << 32 | (uint32_t)__shfl((int)off, from);
-        }
+        for (int x = 0; x < NR; ++x) at[x] = place_of(off, x);
 #pragma unroll
-        for (int x = 0; x < NR; ++x) {
-            char* const to = lds + (wave * (64 / CR) + 256 / CR * x) * T::kRow + buf * T::kTile;
-            direct_load(to, kp + at[x] + 16 * k_piece);
-            direct_load(to + 2 * T::kTile, vp + at[x] + 16 * v_piece);
-        }
+        for (int x = 0; x < NR; ++x)
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) uint32_t*)(from + at[x] + 16 * piece),
+                (__attribute__((address_space(3))) uint32_t*)(tile + (wave * (64 / CR) + 256 / CR * x) * T::kRow), 16, 0, 0);
     };
     const int l16 = lane & 15;
     const int k_from = T::key(n, f);
@@ -222,53 +224,64 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
 
     if (threadIdx.x == 0) any_odd = 0;
     __syncthreads();
-    uint64_t nowhere = 0, nowhere_next = 0;
-    int slot = -1;
-    if (v0 < v1) {
-        slot = entry_of(span.real(v0));
-        load_tile(offset_of(span.real(v0), slot, nowhere));
-        slot = entry_of(span.real(v0 + 64));
-        store_tile(0, span.real(v0), nowhere);
-    }
-    __syncthreads();
+    // A tile's scores are worked out one tile ahead, beside the exponentials of this one: the matrix cores and the vector
+    // units each have work of a wave then.  So keys are a tile ahead of values in the stage.
     // HALVES = 2: the whole of every tile; 1: half `mine` of it
     auto walk = [&](auto halves_, const int mine) {
         constexpr int HALVES = decltype(halves_)::value;
+        f32x16_t x[HALVES];
+        auto scores = [&](int buf) {
+            const char* const kt = keys + buf * T::kTile + (HALVES == 1 ? 32 * mine * T::kRow : 0);
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                f32x16_t acc = f32x16_t{};
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const bf16x8_t key = __builtin_bit_cast(
+                        bf16x8_t, *reinterpret_cast<const u32x4_t*>(kt + (k_from ^ (32 * k)) + 32 * h * T::kRow));
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc, 0, 0, 0);
+                }
+                x[h] = acc;
+            }
+        };
+        // tiles 0 and 1 (which may not be there: then its places are all nowhere)
+        uint64_t nowhere, nowhere_1, nowhere_2 = 0;
+        int slot = entry_of(span.real(v0));
+        int64_t off = offset_of(span.real(v0), slot, nowhere);
+        slot = entry_of(span.real(v0 + 64));
+        int64_t off_1 = offset_of(span.real(v0 + 64), slot, nowhere_1);
+        slot = entry_of(span.real(v0 + 128));
+        load_keys(off);
+        load_values(off);
+        store_keys(0);
+        store_values(0, span.real(v0), nowhere);
+        load_keys(off_1);
+        store_keys(1);
+        __syncthreads();
+        if (wave_live) scores(0);
+        __syncthreads();        // the third tile's keys take the place of the first's
         for (int v = v0, buf = 0; v < v1; v += 64, buf ^= 1) {
-            const bool more = v + 64 < v1;
-            const int t = span.real(v), next = span.real(v + 64);
+            const bool more = v + 64 < v1, more_2 = v + 128 < v1;
+            const int t = span.real(v), next = span.real(v + 64), next_2 = span.real(v + 128);
+            int64_t off_2 = 0;
             bool direct = false;
-            int64_t off = 0;
             if (more) {
-                off = offset_of(next, slot, nowhere_next);
-                direct = HELD == BF16 && nowhere_next == 0 && whole(next, 64, group_pos, group_first);
-                if (direct) direct_tile(buf ^ 1, off);
-                else if (HELD != BF16) load_tile(off);
-                slot = entry_of(span.real(v + 128));
+                direct = HELD == BF16 && nowhere_1 == 0 && whole(next, 64, group_pos, group_first);
+                if (direct) direct_tile(values + (buf ^ 1) * T::kTile, vp, v_piece, off_1);
+                else if (HELD != BF16) load_values(off_1);
+            }
+            if (more_2) {
+                off_2 = offset_of(next_2, slot, nowhere_2);
+                if (HELD == BF16) direct_tile(keys + buf * T::kTile, kp, k_piece, off_2);
+                else load_keys(off_2);
+                slot = entry_of(span.real(v + 192));
             }
             uint64_t wrong = nowhere;       // invalid entries: tokens past the run's end are none
             if (t + 64 > end) wrong &= (1ull << (end - t)) - 1;
             if (wrong) wrong &= __ballot(t + lane < a.sinks || t + lane > group_pos - a.window);     // of tokens that some row sees
             if (wrong && wave == 0 && lane == 0) atomicOr(a.err, DEVERR_TABLE);
-            const int th = t + 32 * mine;
-            // no row of the wave sees any of it
-            const bool past = th > wave_last || (th + 32 * HALVES <= wave_pos - a.window + 1 && th >= a.sinks);
-            if (wave_live && !past) {
-                float x[HALVES][16];
-                const char* const kt = lds + buf * T::kTile + (HALVES == 1 ? 32 * mine * T::kRow : 0);
-                const char* const vt = kt + 2 * T::kTile;
-#pragma unroll
-                for (int h = 0; h < HALVES; ++h) {
-                    f32x16_t acc = f32x16_t{};
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        const bf16x8_t key = __builtin_bit_cast(
-                            bf16x8_t, *reinterpret_cast<const u32x4_t*>(kt + (k_from ^ (32 * k)) + 32 * h * T::kRow));
-                        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key, q[k], acc, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int y = 0; y < 16; ++y) x[h][y] = acc[y];
-                }
+            if (wave_live) {
+                const int th = t + 32 * mine;
                 if (nowhere != 0 || !whole(th, 32 * HALVES, wave_pos, wave_first)) {
 #pragma unroll
                     for (int h = 0; h < HALVES; ++h) {
@@ -295,23 +308,26 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[d] *= alpha;
                 }
+                u32x4_t w[HALVES][2];       // the weights as second operands
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    float part_l[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        x[h][y] = exp2_of(__builtin_fmaf(x[h][y], scale, -m));
+                        part_l[y / 8] += x[h][y];
+                    }
+                    l += part_l[0] + part_l[1];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) w[h][y / 4][y % 4] = bf16_pair(x[h][2 * y], x[h][2 * y + 1]);
+                }
+                scores(buf ^ 1);        // of the next tile (of what lies there, if there is none)
+                const char* const vt = values + buf * T::kTile + (HALVES == 1 ? 32 * mine * T::kRow : 0);
 #pragma unroll
                 for (int h = 0; h < HALVES; ++h)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float* const w = x[h] + 8 * y;
-                        float part_l[2] = {0.f, 0.f};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            w[e] = exp2_of(__builtin_fmaf(w[e], scale, -m));
-                            part_l[e / 4] += w[e];
-                        }
-                        l += part_l[0] + part_l[1];
-                        u32x4_t wh;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) wh[e] = bf16_pair(w[2 * e], w[2 * e + 1]);
                         // 8 tokens' values of one d: two transpose reads
-                        bf16x8_t val[DT];
 #pragma unroll
                         for (int d = 0; d < DT; ++d) {
                             struct { i16x4_t p[2]; } both;
@@ -319,25 +335,31 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
                             for (int z = 0; z < 2; ++z)
                                 both.p[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                     (lds_i16x4_t*)(vt + (v_from ^ (64 * d)) + (32 * h + 16 * y + 8 * z) * T::kRow));
-                            val[d] = __builtin_bit_cast(bf16x8_t, both);
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, both),
+                                                                           __builtin_bit_cast(bf16x8_t, w[h][y]), o[d], 0, 0, 0);
                         }
-#pragma unroll
-                        for (int d = 0; d < DT; ++d)
-                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(val[d], __builtin_bit_cast(bf16x8_t, wh), o[d], 0, 0, 0);
                     }
             }
-            if (direct) {
+            if (HELD == BF16) {
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // in LDS before the barrier
-            } else if (more) {
-                if (HELD == BF16) load_tile(off);
-                store_tile(buf ^ 1, next, nowhere_next);
+                if (more && !direct) {
+                    load_values(off_1);
+                    store_values(buf ^ 1, next, nowhere_1);
+                }
+            } else {
+                if (more) store_values(buf ^ 1, next, nowhere_1);
+                if (more_2) store_keys(buf);
             }
-            nowhere = nowhere_next;
+            nowhere = nowhere_1;
+            nowhere_1 = nowhere_2;
+            off_1 = off_2;
             __syncthreads();
         }
     };
-    if (pairs) walk(std::integral_constant<int, 1>(), wave % 2);
-    else walk(std::integral_constant<int, 2>(), 0);
+    if (v0 < v1) {
+        if (pairs) walk(std::integral_constant<int, 1>(), wave % 2);
+        else walk(std::integral_constant<int, 2>(), 0);
+    }
 
     l = sum_over_f(l);
     bool lost = false;
