@@ -568,7 +568,7 @@ const char* pred_attend_kernel_name(pred_t* p, const pred_kv_cache* cache, int32
  * prompt).  With d = row_len, row i < d is token p = kv_len - d + i and sees the
  * `window` newest tokens up to itself, p - window + 1 .. p, and the sequence's first
  * n_sinks up to itself; window INT32_MAX hides nothing.
- *   n_rows    [1, 2^24]
+ *   n_rows    [1, 2^24], at most 2^30 queries per kv head
  *   row_len   device, [n_seqs] int32 in [0, min(n_rows, kv_len)], or NULL for that upper limit
  *   window    >= 1;  n_sinks >= 0
  * The other arguments, and what is said of rows past row_len, of masked tokens,

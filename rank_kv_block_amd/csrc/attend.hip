@@ -1432,6 +1432,9 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
     Plan pl;
     pl.chunk = kind == Kind::Chunk;
     pl.rows = tree ? 128 : 16;
+    // the chunk kernel's larger groups, a workgroup a CU, where they fill the chip
+    const bool wide = pl.chunk && queries > 128 && (int64_t)a.S * a.Hk * ((queries + 255) / 256) >= a.n_cu;
+    if (wide) pl.rows = 256;
     pl.groups = (queries + pl.rows - 1) / pl.rows;
     if (pl.rows > queries) pl.rows = queries;       // of one group
     // whole tiles (four waves take one each in the stream kernel), or whole blocks where a block's sum spans tiles
@@ -1442,7 +1445,7 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
     // are of uneven length where a run ends early, so more rounds than one even them out (64 sequences, FP8: 503 us
     // with 2, 463 with 4, 449 with 6), but a run has to be worth its start and its partial results (8 sequences of 5k
     // tokens, 13 rows: 75 us with 1, 91 with 2, 109 with 4).
-    pl.slots = 2 * a.n_cu;
+    pl.slots = (wide ? 1 : 2) * a.n_cu;
     pl.run = tree ? 2048 : 2560;
     const double most = (double)a.S * most_tokens(a, pl) * pl.groups * a.Hk / pl.slots / pl.run;
     pl.rounds = most < 1 ? 1 : (most < kRounds ? (int)most : kRounds);

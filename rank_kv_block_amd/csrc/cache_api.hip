@@ -184,12 +184,15 @@ bool attend_counts_ok(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_block
            n_blocks <= kMostTokens / p->d.block_size;
 }
 
-// Rows of a sequence in a call with a window.
-constexpr int kMostRows = 1 << 24;
+// Rows of a sequence in a call with a window: up to 2^24, and up to 2^30 queries of a kv head.
+bool window_rows_ok(pred_t* p, int32_t n_rows) {
+    return n_rows >= 1 && n_rows <= 1 << 24 && (int64_t)n_rows * (p->d.num_q_heads / p->d.num_kv_heads) <= 1 << 30;
+}
 
-int check_window(int32_t n_rows, int32_t window, int32_t n_sinks, const char* what) {
-    if (n_rows < 1 || n_rows > kMostRows)
-        return fail(PRED_ERR_OUT_OF_RANGE, "%s: n_rows (%d) outside [1, 2^24]", what, n_rows);
+int check_window(pred_t* p, int32_t n_rows, int32_t window, int32_t n_sinks, const char* what) {
+    if (!window_rows_ok(p, n_rows))
+        return fail(PRED_ERR_OUT_OF_RANGE, "%s: n_rows (%d) outside [1, 2^24], or more than 2^30 queries per kv head", what,
+                    n_rows);
     if (window < 1 || n_sinks < 0)
         return fail(PRED_ERR_OUT_OF_RANGE, "%s: window (%d) must be >= 1 and n_sinks (%d) >= 0", what, window, n_sinks);
     return PRED_OK;
@@ -564,7 +567,7 @@ int pred_attend(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32
 
 size_t pred_attend_window_workspace_bytes(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_blocks, int32_t window,
                                           int32_t n_sinks) {
-    if (!p || n_seqs < 1 || n_rows < 1 || n_rows > kMostRows || n_blocks < 1 || n_blocks > kMostTokens / p->d.block_size ||
+    if (!p || n_seqs < 1 || !window_rows_ok(p, n_rows) || n_blocks < 1 || n_blocks > kMostTokens / p->d.block_size ||
         window < 1 || n_sinks < 0)
         return 0;
     pred::AttendArgs a = attend_shape(p, n_seqs, n_rows, n_blocks);
@@ -579,7 +582,7 @@ const char* pred_attend_window_kernel_name(pred_t* p, const pred_kv_cache* cache
         return nullptr;
     }
     pred::CacheView view;
-    if (check_cache(p, cache, &view, what) || check_window(n_rows, 1, 0, what)) return nullptr;
+    if (check_cache(p, cache, &view, what) || check_window(p, n_rows, 1, 0, what)) return nullptr;
     if (p->d.head_dim > kMostHead) {
         fail(PRED_ERR_UNSUPPORTED, "%s: head_dim (%d) above %d", what, p->d.head_dim, kMostHead);
         return nullptr;
@@ -596,7 +599,7 @@ int pred_attend_window(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q
                        const int32_t* row_len, int32_t window, int32_t n_sinks, float scale, pred_bf16* out, float* lse,
                        void* workspace, size_t ws_bytes, void* stream) {
     int rc = check_handle(p, "attend_window");
-    if (rc == 0) rc = check_window(n_rows, window, n_sinks, "attend_window");
+    if (rc == 0) rc = check_window(p, n_rows, window, n_sinks, "attend_window");
     if (rc) return rc;
     pred::AttendArgs a = attend_shape(p, n_seqs, n_rows, n_blocks);
     set_window(&a, window, n_sinks);
