@@ -359,6 +359,22 @@ struct TreeLds {
     }
 };
 
+// A staged piece of a narrower type becomes 2 (e4m3) or 4 (4 bits) pieces side by side in an LDS row, written one a step:
+// in step y the one at `to ^ (16 * y)`.  The permutation of the values' rows is of groups of four pieces, so in one order
+// for all lanes a step's writes would fall on few banks (a 4-bit cache: 4 lanes of 16 on one, 39% of the chunk kernel's LDS
+// cycles).  So lanes of neighbouring rows take their pieces in orders of their own: the place is turned by the row's low
+// bits (`to ^ (16 * turn)`), and the piece's words with it.
+template <Held HELD>
+__device__ inline u32x4_t turned(u32x4_t w, int turn) {
+    if constexpr (HELD == FP4) {
+        if (turn & 1) w = u32x4_t{w[1], w[0], w[3], w[2]};
+        if (turn & 2) w = u32x4_t{w[2], w[3], w[0], w[1]};
+    } else if constexpr (HELD == FP8) {
+        if (turn) w = u32x4_t{w[2], w[3], w[0], w[1]};
+    }
+    return w;
+}
+
 // max / sum over the two lanes of a query
 __device__ inline float max_over_f(float x) {
     auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);

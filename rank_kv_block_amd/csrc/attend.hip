@@ -1010,7 +1010,8 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
         }
     };
     // 256 / CR is a multiple of 16, so a thread's rows share their permutation and lie a fixed step apart
-    const int k_to = T::key(my_tok, SPREAD * my_piece), v_to = T::value(my_tok, SPREAD * my_piece);
+    const int turn = my_tok & (SPREAD - 1);     // of a thread's values: see turned()
+    const int k_to = T::key(my_tok, SPREAD * my_piece), v_to = T::value(my_tok, SPREAD * my_piece) ^ (16 * turn);
     auto store_tile = [&](int buf, int t, uint64_t nowhere) {
         if (!mine_in) return;
         if (t + 64 > ctx || nowhere != 0) {
@@ -1039,6 +1040,8 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
         }
         char* const kt = lds + buf * T::kTile + k_to;
         char* const vt = lds + (2 + buf) * T::kTile + v_to;
+#pragma unroll
+        for (int x = 0; x < NR; ++x) vs[x] = turned<HELD>(vs[x], turn);
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             constexpr int kStep = 256 / CR * T::kRow;
@@ -1432,9 +1435,6 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
     Plan pl;
     pl.chunk = kind == Kind::Chunk;
     pl.rows = tree ? 128 : 16;
-    // the chunk kernel's larger groups, a workgroup a CU, where they fill the chip
-    const bool wide = pl.chunk && queries > 128 && (int64_t)a.S * a.Hk * ((queries + 255) / 256) >= a.n_cu;
-    if (wide) pl.rows = 256;
     pl.groups = (queries + pl.rows - 1) / pl.rows;
     if (pl.rows > queries) pl.rows = queries;       // of one group
     // whole tiles (four waves take one each in the stream kernel), or whole blocks where a block's sum spans tiles
@@ -1445,7 +1445,7 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
     // are of uneven length where a run ends early, so more rounds than one even them out (64 sequences, FP8: 503 us
     // with 2, 463 with 4, 449 with 6), but a run has to be worth its start and its partial results (8 sequences of 5k
     // tokens, 13 rows: 75 us with 1, 91 with 2, 109 with 4).
-    pl.slots = (wide ? 1 : 2) * a.n_cu;
+    pl.slots = 2 * a.n_cu;
     pl.run = tree ? 2048 : 2560;
     const double most = (double)a.S * most_tokens(a, pl) * pl.groups * a.Hk / pl.slots / pl.run;
     pl.rounds = most < 1 ? 1 : (most < kRounds ? (int)most : kRounds);

@@ -40,21 +40,16 @@ struct ChunkWork {
 // instructions again, and these are what long chunks are bound by): an output is
 // 2^-8 of the weighted mean of the absolute values off at most.  Where the values
 // are of either sign that is about what the output's own rounding to bf16 adds.
-template <int D, Held HELD, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void attend_chunk_kernel(AttendArgs a, Plan pl, BlockSize bs) {
+template <int D, Held HELD>
+__global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan pl, BlockSize bs) {
     using T = TreeLds<D>;
     constexpr int RB = (int)(HELD == FP4 ? D / 2 : (HELD == FP8 ? D : 2 * D));      // bytes of a cache row
     constexpr int CR = RB / 16;                 // 16-byte pieces of it
-    // Threads that stage keys, and values: all do both, or where a tile has few pieces half of them each.
-    constexpr bool APART = WAVES == 8 && 64 * CR <= 256;
-    constexpr int STAGERS = APART ? 256 : 64 * WAVES;
-    constexpr int NR = (64 * CR + STAGERS - 1) / STAGERS;       // pieces a thread stages
-    constexpr int STEP = STAGERS / CR;          // tokens from one of them to the next: a multiple of 16
+    constexpr int NR = (64 * CR + 255) / 256;   // pieces a thread stages, of keys and of values
+    constexpr int STEP = 256 / CR;              // tokens from one of them to the next: a multiple of 16
     constexpr int SPREAD = 2 * D / RB;          // pieces of an LDS row that one becomes
     constexpr int KS = D / 16, DT = D / 32;
-    // keys 0, keys 1, values 0, values 1; then the pairs' sums
-    constexpr int kSums = WAVES / 2 * (16 * DT + 2) * 64 * (int)sizeof(float);
-    __shared__ __attribute__((aligned(16))) char lds[4 * T::kTile > kSums ? 4 * T::kTile : kSums];
+    __shared__ __attribute__((aligned(16))) char lds[4 * T::kTile];     // keys 0, keys 1, values 0, values 1
     __shared__ int any_odd;         // a value of a tile that is not seen whole is not finite
 
     Item it = item_of(a, pl, blockIdx.x, ChunkWork{a, pl});
@@ -81,7 +76,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_chunk_kernel(AttendArgs 
     const int n = lane & 31, f = lane >> 5;
     const int g = a.Hq / a.Hk, R = a.M * g;
     const int64_t group_r0 = (int64_t)pl.rows * it.group;
-    const bool pairs = (int64_t)drafted * g - group_r0 <= 16 * WAVES;
+    const bool pairs = (int64_t)drafted * g - group_r0 <= 64;
     const int in_group = (pairs ? wave / 2 : wave) * 32, r0 = (int)group_r0 + in_group, r = r0 + n, i = r / g;
     const bool live = r < R && in_group + n < pl.rows && i < drafted;
     const bool wave_live = r0 < R && in_group < pl.rows && r0 / g < drafted;       // rows of a wave die from the end
@@ -121,9 +116,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_chunk_kernel(AttendArgs 
         nowhere = __ballot(none);
         return none ? 0 : bytes_of<HELD>(slot * a.cache.block_stride + (int64_t)(tok - bs.block(tok) * bs.B) * a.cache.token_stride);
     };
-    const int stager = threadIdx.x % STAGERS, my_tok = stager / CR, my_piece = stager % CR;        // and tokens STEP further on
+    const int my_tok = threadIdx.x / CR, my_piece = threadIdx.x % CR;       // and tokens STEP further on
     const bool mine_in = STEP * NR <= 64 || my_tok < 64;     // (64 values in 4 bits: half of the threads have a piece)
-    const bool of_keys = !APART || threadIdx.x < 256, of_values = !APART || threadIdx.x >= 256;
     // Keys and values of different tiles are on their way at a time.  `off` is where lane x's token lies (token x of the
     // tile).
     u32x4_t ks[NR], vs[NR];
@@ -133,7 +127,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_chunk_kernel(AttendArgs 
         return (int64_t)__shfl((int)(off >> 32), from) << 32 | (uint32_t)__shfl((int)off, from);
     };
     auto load_keys = [&](int64_t off) {
-        if (!of_keys) return;
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             const int64_t o = place_of(off, x) + 16 * my_piece;
@@ -142,7 +135,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_chunk_kernel(AttendArgs 
         }
     };
     auto load_values = [&](int64_t off) {
-        if (!of_values) return;
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             const int64_t o = place_of(off, x) + 16 * my_piece;
@@ -175,28 +167,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_chunk_kernel(AttendArgs 
             }
         }
     };
-    // A piece of a narrower type becomes SPREAD pieces side by side, one a step.  The permutation of the values' rows is of
-    // groups of four, so lanes of neighbouring rows take their pieces in an order of their own, and a step's fall on
-    // different banks (in one order: 4 lanes of 16 on one, 39% of the kernel's LDS cycles over a 4-bit cache).
-    const int turn = my_tok & (SPREAD - 1);
+    const int turn = my_tok & (SPREAD - 1);     // of a thread's values: see turned()
     const int k_to = T::key(my_tok, SPREAD * my_piece), v_to = T::value(my_tok, SPREAD * my_piece) ^ (16 * turn);
-    auto turned = [&](u32x4_t w) {
-        if constexpr (HELD == FP4) {
-            if (turn & 1) w = u32x4_t{w[1], w[0], w[3], w[2]};
-            if (turn & 2) w = u32x4_t{w[2], w[3], w[0], w[1]};
-        } else if constexpr (HELD == FP8) {
-            if (turn) w = u32x4_t{w[2], w[3], w[0], w[1]};
-        }
-        return w;
-    };
     char* const keys = lds;
     char* const values = lds + 2 * T::kTile;
     auto store_keys = [&](int buf) {
-        if (of_keys && mine_in) store_pieces(keys + buf * T::kTile, k_to, ks, k_sc);
+        if (mine_in) store_pieces(keys + buf * T::kTile, k_to, ks, k_sc);
     };
     // t: the tile's first token; a value that not every row sees must be a number (a masked weight is 0)
     auto store_values = [&](int buf, int t, uint64_t nowhere) {
-        if (!of_values || !mine_in) return;
+        if (!mine_in) return;
         if (nowhere != 0 || !whole(t, 64, group_pos, group_first)) {
             bool odd = false;
 #pragma unroll
@@ -220,7 +200,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_chunk_kernel(AttendArgs 
             if (odd) any_odd = 1;
         }
 #pragma unroll
-        for (int x = 0; x < NR; ++x) vs[x] = turned(vs[x]);
+        for (int x = 0; x < NR; ++x) vs[x] = turned<HELD>(vs[x], turn);
         store_pieces(values + buf * T::kTile, v_to, vs, v_sc);
     };
     // a bf16 tile straight into LDS: a lane fetches the piece that belongs in its place
@@ -347,22 +327,28 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_chunk_kernel(AttendArgs 
                 }
                 scores(buf ^ 1);        // of the next tile (of what lies there, if there is none)
                 const char* const vt = values + buf * T::kTile + (HALVES == 1 ? 32 * mine * T::kRow : 0);
+                // 16 tokens a step, two transpose reads for 8 tokens' values of one d, a step ahead of the products
+                bf16x8_t val[2][DT];
+                auto read_values = [&](int step) {
 #pragma unroll
-                for (int h = 0; h < HALVES; ++h)
+                    for (int d = 0; d < DT; ++d) {
+                        struct { i16x4_t p[2]; } both;
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        // 8 tokens' values of one d: two transpose reads
-#pragma unroll
-                        for (int d = 0; d < DT; ++d) {
-                            struct { i16x4_t p[2]; } both;
-#pragma unroll
-                            for (int z = 0; z < 2; ++z)
-                                both.p[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                    (lds_i16x4_t*)(vt + (v_from ^ (64 * d)) + (32 * h + 16 * y + 8 * z) * T::kRow));
-                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, both),
-                                                                           __builtin_bit_cast(bf16x8_t, w[h][y]), o[d], 0, 0, 0);
-                        }
+                        for (int z = 0; z < 2; ++z)
+                            both.p[z] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                (lds_i16x4_t*)(vt + (v_from ^ (64 * d)) + (16 * step + 8 * z) * T::kRow));
+                        val[step & 1][d] = __builtin_bit_cast(bf16x8_t, both);
                     }
+                };
+                read_values(0);
+#pragma unroll
+                for (int step = 0; step < 2 * HALVES; ++step) {
+                    if (step + 1 < 2 * HALVES) read_values(step + 1);
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            val[step & 1][d], __builtin_bit_cast(bf16x8_t, w[step / 2][step % 2]), o[d], 0, 0, 0);
+                }
             }
             if (HELD == BF16) {
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // in LDS before the barrier
@@ -437,8 +423,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_chunk_kernel(AttendArgs 
             for (int y = 0; y < 16; ++y) o[d][y] = joined(o[d][y], mine, x[(2 + 16 * d + y) * 64 + lane], other);
     }
     if (pairs && runs == 1) {       // rows that no wave of the pairs has: past the last live one
-        const int from = (int)group_r0 + 16 * WAVES, to = (int)group_r0 + pl.rows < R ? (int)group_r0 + pl.rows : R;
-        for (int x = (wave / 2) * 64 + lane; x < (to - from) * (D / 8); x += 32 * WAVES) {
+        const int from = (int)group_r0 + 64, to = (int)group_r0 + pl.rows < R ? (int)group_r0 + pl.rows : R;
+        for (int x = (wave / 2) * 64 + lane; x < (to - from) * (D / 8); x += 128) {
             const int y = from + x / (D / 8), d = x % (D / 8) * 8;
             const int64_t at = ((int64_t)s * a.M + y / g) * a.Hq + kvh * g + y % g;
             *reinterpret_cast<u32x4_t*>(a.out + at * D + d) = u32x4_t{0, 0, 0, 0};
@@ -475,8 +461,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attend_chunk_kernel(AttendArgs 
 
 template <int D, Held HELD>
 void launch_chunk(const AttendArgs& a, const Plan& pl, const BlockSize& bs, uint32_t grid, hipStream_t stream) {
-    if (pl.rows > 128) attend_chunk_kernel<D, HELD, 8><<<grid, 512, 0, stream>>>(a, pl, bs);
-    else attend_chunk_kernel<D, HELD, 4><<<grid, 256, 0, stream>>>(a, pl, bs);
+    attend_chunk_kernel<D, HELD><<<grid, 256, 0, stream>>>(a, pl, bs);
 }
 template void launch_chunk<64, BF16>(const AttendArgs&, const Plan&, const BlockSize&, uint32_t, hipStream_t);
 template void launch_chunk<64, FP8>(const AttendArgs&, const Plan&, const BlockSize&, uint32_t, hipStream_t);
