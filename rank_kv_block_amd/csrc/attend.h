@@ -99,6 +99,8 @@ struct Plan {
                     // group
     int run;        // shorter runs than this are not worth a round more: an item's start and its partial results
     int unit;       // a run is a multiple of this many tokens
+    int shortest;   // and at least this long, a multiple of unit too
+    int tries;      // at fitting the items into one round
     int rows;       // queries of a group
     int groups;     // groups of a kv head's queries
     bool chunk;     // of the chunk kernel: a group has a span of its own
@@ -176,15 +178,16 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
             for (int o = 32; o >= 1; o >>= 1) count += __shfl_xor(count, o);
         return (uint32_t)__builtin_amdgcn_readfirstlane(count) * a.Hk;
     };
-    int run = (int)(wanted < pl.unit ? pl.unit : (wanted < 0x7FFFFFFF ? wanted : 0x7FFFFFFF));
+    int run = (int)(wanted < pl.shortest ? pl.shortest : (wanted < 0x7FFFFFFF ? wanted : 0x7FFFFFFF));
     uint32_t all = items_of(run);
     // Every sequence's last run is a part of one, so the items are a few more than wanted.  Where they pass one round
     // by up to a quarter, runs a little longer do without the second, nearly empty one (8 sequences of 5k tokens, 13
     // rows: 78 us without, 70 with; with more rounds there is nothing to gain).
     const uint32_t one = (uint32_t)pl.slots;
     int longer = run;
-    for (uint32_t tries = 0, now = all; tries < 2 && all > one && all - one <= one / 4; ++tries) {
-        longer = (int)(((int64_t)longer * now / one + pl.unit) / pl.unit * pl.unit);
+    for (uint32_t tries = 0, now = all; tries < (uint32_t)pl.tries && all > one && all - one <= one / 4; ++tries) {
+        const int64_t fits = ((int64_t)longer * now / one + pl.unit) / pl.unit * pl.unit;
+        longer = (int)(fits < 0x40000000 ? fits : 0x40000000 / pl.unit * pl.unit);
         now = items_of(longer);
         if (now <= one) {
             run = longer;

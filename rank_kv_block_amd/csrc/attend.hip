@@ -1449,18 +1449,29 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
     pl.run = tree ? 2048 : 2560;
     const double most = (double)a.S * most_tokens(a, pl) * pl.groups * a.Hk / pl.slots / pl.run;
     pl.rounds = most < 1 ? 1 : (most < kRounds ? (int)most : kRounds);
+    // (16 trees of 16 rows over up to 16416 tokens in 4 bits, where two tries leave 560 items for 512 places: 210 us, with
+    // six 166.  bf16 and e4m3 caches without a window keep two, and with it the runs that they had.)
+    pl.tries = a.cache.fp4 || a.window ? 6 : 2;
     if (pl.chunk) {
         pl.rounds = 1;
         // Groups that fill the chip keep their tokens in one run (unit above any number of tokens), unless some may walk
         // much longer than others.
         const int64_t items = (int64_t)a.S * a.Hk * pl.groups;
-        if (a.S == 1 ? items >= pl.slots : items >= 2ll * pl.slots && most_tokens(a, pl) <= 8192) pl.unit = 1 << 30;
+        if (a.S == 1 ? items >= pl.slots : items >= 2ll * pl.slots && most_tokens(a, pl) <= 8192) {
+            pl.unit = 1 << 30;
+            pl.tries = 0;       // and nothing is left to fit
+        }
     }
+    pl.shortest = pl.unit;
+    // A window of up to three of the shortest runs stays in one: the join's launch costs more than its split saves (one
+    // sequence of 4 heads of 64 with 200 tokens in sight 11.1 -> 8.2 us, 32 heads of 128 14.0 -> 11.4, eight sequences
+    // 13.8 -> 14.4; with 500 tokens the one run is no shorter, 11.2, or longer, 14.1 -> 16.9).
+    if (a.window && !pl.chunk && !tree && most_tokens(a, pl) <= 3 * pl.unit) pl.shortest = 3 * pl.unit;
     return pl;
 }
 
 // Whether a sequence can have more than one run, so that there are partial results.
-bool may_split(const AttendArgs& a, const Plan& pl) { return most_tokens(a, pl) > pl.unit; }
+bool may_split(const AttendArgs& a, const Plan& pl) { return most_tokens(a, pl) > pl.shortest; }
 
 size_t plan_bytes(const AttendArgs& a, const Plan& pl) {
     return may_split(a, pl) ? (size_t)(share_bytes(a.S) + most_items(a, pl) * pl.rows * (a.D + 2) * (int64_t)sizeof(float)) : 0;

@@ -84,6 +84,11 @@ NORMS = [
     (300, 40, 128, 128, True, "none", (), -150, 0.0),
     (7, 6, 128, 0, False, "none", (), 0, 1.0),
     (2, 5, 24, 0, False, "none", (), 0, None),
+    # tokens enough for a wave to take several heads of each place
+    (1100, 13, 128, 128, False, "none", (), -7, 1.0),
+    (1500, 17, 64, 32, True, "none", (), 100000, 0.0),
+    (2300, 3, 256, 0, False, "none", (), 0, 0.0),
+    (1200, 5, 80, 20, False, "none", (), 31, None),
 ]
 
 
@@ -249,6 +254,10 @@ STORES = [
     (9, 4, 1, 64, 16, 64, False, "fp4", "heads", False),
     (9, 4, 2, 256, 16, 0, False, "fp4", "heads", False),
     (9, 4, 2, 32, 16, 32, False, "fp4", "tokens", False),
+    (2300, 8, 2, 64, 16, 64, True, "fp4", "heads", True),
+    (700, 40, 8, 128, 16, 128, False, "bf16", "tokens", True),
+    (1100, 3, 3, 96, 5, 22, False, "fp8", "padded", False),
+    (1100, 7, 7, 32, 16, 0, False, "fp4", "padded", True),
 ]
 
 
@@ -375,7 +384,8 @@ def test_rotate_store_into_4_bits(D, rot, inter, layout):
 
 
 @pytest.mark.parametrize("layout", ["tokens", "heads", "padded"])
-@pytest.mark.parametrize("n,Hk,D,B", [(1, 1, 64, 16), (50, 8, 128, 16), (33, 3, 96, 7), (20, 2, 32, 1), (9, 1, 512, 8), (9, 40, 64, 8)])
+@pytest.mark.parametrize("n,Hk,D,B", [(1, 1, 64, 16), (50, 8, 128, 16), (33, 3, 96, 7), (20, 2, 32, 1), (9, 1, 512, 8), (9, 40, 64, 8),
+                                       (2100, 3, 64, 16), (2050, 2, 128, 16)])
 def test_store_and_load_4_bits(n, Hk, D, B, layout):
     """Bit for bit: values of every size, ties, zeros of both signs, groups that are all zero, tiny or not finite."""
     _say("store 4", n, Hk, D, B, layout)
@@ -431,7 +441,8 @@ def test_store_and_load_4_bits(n, Hk, D, B, layout):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
-@pytest.mark.parametrize("n,Hk,D,B,layout", [(1, 1, 64, 16, "tokens"), (45, 8, 128, 16, "heads"), (45, 3, 80, 7, "padded")])
+@pytest.mark.parametrize("n,Hk,D,B,layout", [(1, 1, 64, 16, "tokens"), (45, 8, 128, 16, "heads"), (45, 3, 80, 7, "padded"),
+                                              (2077, 5, 64, 16, "heads")])
 def test_store_and_load(n, Hk, D, B, layout, dtype):
     g = torch.Generator().manual_seed(n + D)
     N = n // B + 3

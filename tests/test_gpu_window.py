@@ -116,6 +116,11 @@ CASES = [
     (1, 33, 300, 1, 128, 16, 10, "bf16", "tokens", 50, 4, "chunk"),
     (2, 65, 8, 1, 128, 24, 30, "bf16", "heads", 300, 4, "chunk"),
     (2, 65, 8, 1, 128, 1, 400, "bf16", "tokens", 63, 4, "chunk"),
+    # groups that fill the chip: no walk is split
+    (1, 2100, 32, 8, 128, 16, 160, "bf16", "heads", 700, 4, "chunk"),
+    (1, 2055, 32, 8, 64, 32, 70, "fp4", "tokens", ALL, 0, "chunk"),
+    (5, 1000, 28, 7, 64, 16, 64, "fp8", "tokens", 90, 4, "chunk"),
+    (4, 1030, 32, 8, 128, 16, 70, "fp4", "heads", 300, 4, "chunk"),
     (2, 5, 6, 2, 80, 16, 20, "bf16", "tokens", 100, 4, "plain"),
     (2, 40, 4, 2, 256, 16, 9, "fp8", "heads", 20, 3, "plain"),
     (2, 9, 4, 2, 96, 7, 19, "fp4", "padded", 50, 10, "plain"),
