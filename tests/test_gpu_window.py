@@ -328,6 +328,57 @@ def test_long_contexts_in_runs(Hq, Hk, D, B, M, kind, window):
         assert torch.equal(first, c.out)
 
 
+@pytest.mark.parametrize("S,M,Hq,Hk,D,B,n,kind,window,sinks", [
+    (150, 1, 8, 2, 128, 16, 12, "bf16", 60, 4), (65, 3, 8, 2, 64, 16, 9, "fp8", 50, 0), (130, 20, 4, 2, 64, 16, 12, "fp4", 33, 5),
+    (300, 1, 4, 1, 128, 16, 60, "fp4", 700, 4), (129, 40, 2, 1, 128, 32, 12, "bf16", ALL, 0)])
+def test_many_sequences(S, M, Hq, Hk, D, B, n, kind, window, sinks):
+    """More sequences than a wave has lanes."""
+    _say("window many", S, M, Hq, Hk, D, B, n, kind, window, sinks)
+    c = make(kind, S, M, Hq, Hk, D, B, n)
+    with _handle(Hq, Hk, D, B, c.N) as p:
+        c.run(p, window, sinks)
+        rk.pred_device_error(p.handle)
+        c.check(p, window, sinks)
+
+
+@pytest.mark.parametrize("kind,N", [("bf16", 80000), ("fp4", 300000)])
+@pytest.mark.parametrize("M", [1, 40])
+def test_far_pages(kind, N, M):
+    """A sequence scattered over more than 4 GiB of keys: the bits of the same pages close together, with the window and
+    without; tokens stored and read back there."""
+    Hq, Hk, D, B, n = 16, 8, 128, 32, 250
+    c = make(kind, 1, M, Hq, Hk, D, B, n)
+    near = c.tables[0].long()
+    far = torch.linspace(600, N - 1, n).long().cuda()
+    slots = (near[-3:, None] * B + torch.arange(B, device="cuda")).flatten()
+    x, y = (torch.randn((3 * B, Hk, D), generator=c.g).bfloat16().cuda() for _ in range(2))
+
+    def run(slots):
+        with _handle(Hq, Hk, D, B, c.N) as p:
+            got = []
+            for window in (3000, ALL):
+                c.run(p, window, 4)
+                got += [c.out.clone(), c.lse.clone()]
+            Case.run(c, p, False)
+            got += [c.out.clone(), c.lse.clone()]
+            back = [torch.zeros_like(x) for _ in range(4)]
+            rk.pred_load(p.handle, c.kv, slots, *back[:2])
+            rk.pred_store(p.handle, x, y, slots, c.kv)
+            rk.pred_load(p.handle, c.kv, slots, *back[2:])
+            rk.pred_device_error(p.handle)
+            return got + back
+
+    small = c.bits if kind == "fp4" else (c.k, c.v)
+    big = [torch.zeros((N, *t.shape[1:]), dtype=t.dtype, device="cuda") for t in small]
+    for t, b in zip(small, big):
+        b[far] = t[near]
+    want = run(slots)
+    c.N, c.tables = N, far.int().view(1, n)
+    c.kv = rk.KVCache(*big[:2], 1.0, 1.0, *big[2:])
+    for a, b in zip(run((far[-3:, None] * B + torch.arange(B, device="cuda")).flatten()), want):
+        assert torch.equal(a, b)
+
+
 def test_no_table_no_lengths():
     for M in (1, 70):
         c = make("bf16", 2, M, 8, 2, 128, 16, 9, identity=True, ragged=False, drafts=[M, M])
@@ -392,6 +443,29 @@ def test_steps_in_a_graph_and_on_another_stream():
             torch.cuda.synchronize()
             for a, b in zip([t for c in (one, many) for t in (c.out, c.lse)], want):
                 assert torch.equal(a, b), i
+
+
+def test_two_calls_at_once():
+    """Two batches of one handle on two streams, each with its workspace, many times over: the bits of one after another."""
+    Hq, Hk, D, B, n = 8, 2, 128, 16, 300
+    cases = [make(kind, 2, M, Hq, Hk, D, B, n, lens=[n * B, n * B - 9], drafts=[M, M], seed=M)
+             for M, kind in ((1, "bf16"), (40, "fp4"), (1, "fp4"), (33, "bf16"))]
+    with _handle(Hq, Hk, D, B, cases[0].N) as p:
+        want = []
+        for c in cases:
+            c.run(p, 3000, 4)
+            want.append((c.out.clone(), c.lse.clone()))
+            c.ws = torch.empty((rk.pred_attend_window_workspace_bytes(p.handle, 2, c.M, n, 3000, 4),), dtype=torch.uint8, device="cuda")
+            c.out.zero_()
+            c.lse.zero_()
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in cases]
+        for _ in range(10):
+            for c, s in zip(cases, streams):
+                rk.pred_attend_window(p.handle, c.kv, c.q, c.tables, c.lens, c.drafts, 3000, 4, c.scale, c.out, c.lse, c.ws, stream=s)
+        torch.cuda.synchronize()
+        for c, (out, lse) in zip(cases, want):
+            assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
 
 
 def test_refusals():
