@@ -116,6 +116,7 @@ struct Item {
     Share share;
     int slot;       // index of its partial results; -1: no item
     bool last;      // the last group: it also writes what the rows of dead groups get
+    int spare, spares;      // a workgroup behind an XCD's last item: which of how many
 };
 
 __device__ inline int runs_of(int len, int run) { return len > run ? (len + run - 1) / run : 1; }
@@ -197,6 +198,8 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
     const uint32_t each = (all + 7) / 8, f = b % 8 * each + b / 8;
     Item it{};
     it.slot = -1;
+    it.spare = (int)(b - 8 * each);
+    it.spares = (int)(gridDim.x - 8 * each);
     if (b / 8 >= each || f >= all) return it;
     int before = 0;
     for (int s0 = 0; s0 < a.S; s0 += 64) {

@@ -1547,7 +1547,8 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     AttendArgs b = a;
     if (!split) b.ws = nullptr;
     // an XCD's items are numbered from the whole's eighth, rounded up
-    const int64_t grid = (most_items(a, pl) + 7) / 8 * 8;
+    // (and the chunk kernel's dead groups take workgroups behind the last)
+    const int64_t grid = (most_items(a, pl) + 7) / 8 * 8 + (pl.chunk ? 8 : 0);
     if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
     auto launch = [&](auto held) {
         if (a.D == 64) launch_fast<64, decltype(held)::value>(b, kind, pl, (uint32_t)grid, stream);

@@ -8,18 +8,57 @@ namespace pred {
 namespace attend {
 namespace {
 
-// A sequence's work: the most that a group of it walks, and all groups, those
-// without a live row among them (they write what such rows get).
+__device__ inline int live_groups(const AttendArgs& a, const Plan& pl, int drafted) {
+    return (int)(((int64_t)drafted * (a.Hq / a.Hk) + pl.rows - 1) / pl.rows);
+}
+
+// A sequence's work: the most that a group of it walks, and the groups that have
+// a live row.
 struct ChunkWork {
     const AttendArgs& a;
     const Plan& pl;
     __device__ inline void operator()(int s, int& len, int& groups) const {
         const int tokens = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B);
         const int some = (a.sinks + 63) / 64 * 64 + a.window + pl.rows / (a.Hq / a.Hk) + 1 + 64;
-        len = draft_len_of(a, s, tokens) == 0 ? 0 : (some < tokens ? some : tokens);
-        groups = pl.groups;
+        groups = live_groups(a, pl, draft_len_of(a, s, tokens));
+        len = groups == 0 ? 0 : (some < tokens ? some : tokens);
     }
 };
+
+// What the rows of groups without a live row get, by the workgroups behind the
+// last item.  (As items between the others they left the XCDs work of uneven
+// length: three prompts, two of them of 3/4 of n_rows, 304 us, now %PROMPTS%.)
+__device__ inline void dead_groups(const AttendArgs& a, const Plan& pl, int spare, int spares) {
+    const int lane = threadIdx.x & 63, g = a.Hq / a.Hk;
+    const int64_t R = (int64_t)a.M * g;
+    int64_t before = 0;     // of the sequences so far, kv heads counted
+    for (int s0 = 0; s0 < a.S; s0 += 64) {
+        int live = pl.groups;
+        if (s0 + lane < a.S)
+            live = live_groups(a, pl, draft_len_of(a, s0 + lane, kv_len_of(a.kv_len, s0 + lane, (int64_t)a.n * a.B)));
+        uint64_t some = __ballot(live < pl.groups);
+        for (; some != 0; some &= some - 1) {
+            const int at = __builtin_ctzll(some), s = s0 + at, first = __builtin_amdgcn_readlane(live, at);
+            const int64_t dead = (int64_t)(pl.groups - first) * a.Hk;
+            for (int64_t x = (spare + spares - before % spares) % spares; x < dead; x += spares) {
+                const int kvh = (int)(x % a.Hk), group = first + (int)(x / a.Hk);
+                for (int y = threadIdx.x; y < pl.rows * (a.D / 8); y += 256) {
+                    const int64_t r = (int64_t)pl.rows * group + y / (a.D / 8);
+                    if (r >= R) break;
+                    const int64_t row = ((int64_t)s * a.M + r / g) * a.Hq + kvh * g + r % g;
+                    *reinterpret_cast<u32x4_t*>(a.out + row * a.D + y % (a.D / 8) * 8) = u32x4_t{0, 0, 0, 0};
+                    if (a.lse && y % (a.D / 8) == 0) a.lse[row] = -INFINITY;
+                }
+                if (group == 0 && kvh == 0 && threadIdx.x == 0) {       // the sequence has no item
+                    const int len = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B);
+                    check_lengths(a, s, len, 0);
+                    if (a.ws) shares_of(a)[s] = Share{len, 1, 1 << 30, 1, 0};
+                }
+            }
+            before += dead;
+        }
+    }
+}
 
 // ---------------------------------------------------------------- chunk kernel
 //
@@ -53,7 +92,10 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
     __shared__ int any_odd;         // a value of a tile that is not seen whole is not finite
 
     Item it = item_of(a, pl, blockIdx.x, ChunkWork{a, pl});
-    if (it.slot < 0) return;
+    if (it.slot < 0) {
+        if (it.spare >= 0) dead_groups(a, pl, it.spare, it.spares);
+        return;
+    }
     {   // the longest walks first
         const int other = it.share.groups - 1 - it.group;
         it.slot += other - it.group;
@@ -142,7 +184,7 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
             if constexpr (HELD == FP4) v_sc[x] = a.cache.v_scales[(head_off + o) >> 4];
         }
     };
-    // a thread's pieces as bf16 into LDS, `to` its first one's place
+    // a thread's pieces of a narrow type as bf16 into LDS, `to` its first one's place
     auto store_pieces = [&](char* tile, int to, const u32x4_t* w, const uint32_t* sc) {
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
@@ -151,7 +193,7 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
                     *reinterpret_cast<u32x4_t*>(tile + (to ^ (16 * y)) + x * kStep) = fp4x8_to_bf16(w[x][y], sc[x]);
-            } else if constexpr (HELD == FP8) {
+            } else {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     u32x4_t z;
@@ -162,8 +204,6 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
                     }
                     *reinterpret_cast<u32x4_t*>(tile + (to ^ (16 * y)) + x * kStep) = z;
                 }
-            } else {
-                *reinterpret_cast<u32x4_t*>(tile + to + x * kStep) = w[x];
             }
         }
     };
@@ -191,9 +231,9 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
                     }
                 }
 #pragma unroll
-                for (int y = 0; y < 4 && HELD != FP4; ++y) {
+                for (int y = 0; y < 4 && HELD == FP8; ++y) {
                     const uint32_t w = none ? 0u : vs[x][y];
-                    vs[x][y] = HELD == FP8 ? finite_only_fp8(w) : finite_only(w);
+                    vs[x][y] = finite_only_fp8(w);
                     odd |= vs[x][y] != w;
                 }
             }
@@ -215,6 +255,24 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
             __builtin_amdgcn_global_load_lds(
                 (const __attribute__((address_space(1))) uint32_t*)(from + at[x] + 16 * piece),
                 (__attribute__((address_space(3))) uint32_t*)(tile + (wave * (64 / CR) + STEP * x) * T::kRow), 16, 0, 0);
+    };
+    // values of such a tile, where this thread's pieces have come in: as store_values
+    auto clean_values = [&](int buf, int t, uint64_t nowhere) {
+        if (nowhere == 0 && whole(t, 64, group_pos, group_first)) return;
+        bool odd = false;
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            u32x4_t* const at = reinterpret_cast<u32x4_t*>(values + buf * T::kTile + (wave * (64 / CR) + STEP * x) * T::kRow + 16 * lane);
+            const bool none = (nowhere >> (my_tok + STEP * x)) & 1;
+            const u32x4_t in = *at;
+            u32x4_t w;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[y] = none ? 0u : finite_only(in[y]);
+            const bool differs = (w[0] != in[0]) | (w[1] != in[1]) | (w[2] != in[2]) | (w[3] != in[3]);
+            odd |= differs && !none;
+            if (differs) *at = w;
+        }
+        if (odd) any_odd = 1;
     };
     const int l16 = lane & 15;
     const int k_from = T::key(n, f);
@@ -250,17 +308,24 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
         };
         // tiles 0 and 1 (which may not be there: then its places are all nowhere)
         uint64_t nowhere, nowhere_1, nowhere_2 = 0;
-        int slot = entry_of(span.real(v0));
-        int64_t off = offset_of(span.real(v0), slot, nowhere);
-        slot = entry_of(span.real(v0 + 64));
-        int64_t off_1 = offset_of(span.real(v0 + 64), slot, nowhere_1);
-        slot = entry_of(span.real(v0 + 128));
-        load_keys(off);
-        load_values(off);
-        store_keys(0);
-        store_values(0, span.real(v0), nowhere);
-        load_keys(off_1);
-        store_keys(1);
+        const int slot_0 = entry_of(span.real(v0)), slot_1 = entry_of(span.real(v0 + 64));
+        int slot = entry_of(span.real(v0 + 128));
+        const int64_t off = offset_of(span.real(v0), slot_0, nowhere);
+        int64_t off_1 = offset_of(span.real(v0 + 64), slot_1, nowhere_1);
+        if constexpr (HELD == BF16) {
+            direct_tile(keys, kp, k_piece, off);
+            direct_tile(values, vp, v_piece, off);
+            direct_tile(keys + T::kTile, kp, k_piece, off_1);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            clean_values(0, span.real(v0), nowhere);
+        } else {
+            load_keys(off);
+            load_values(off);
+            store_keys(0);
+            load_keys(off_1);
+            store_values(0, span.real(v0), nowhere);
+            store_keys(1);
+        }
         __syncthreads();
         if (wave_live) scores(0);
         __syncthreads();        // the third tile's keys take the place of the first's
@@ -268,11 +333,9 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
             const bool more = v + 64 < v1, more_2 = v + 128 < v1;
             const int t = span.real(v), next = span.real(v + 64), next_2 = span.real(v + 128);
             int64_t off_2 = 0;
-            bool direct = false;
             if (more) {
-                direct = HELD == BF16 && nowhere_1 == 0 && whole(next, 64, group_pos, group_first);
-                if (direct) direct_tile(values + (buf ^ 1) * T::kTile, vp, v_piece, off_1);
-                else if (HELD != BF16) load_values(off_1);
+                if (HELD == BF16) direct_tile(values + (buf ^ 1) * T::kTile, vp, v_piece, off_1);
+                else load_values(off_1);
             }
             if (more_2) {
                 off_2 = offset_of(next_2, slot, nowhere_2);
@@ -352,10 +415,7 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
             }
             if (HELD == BF16) {
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // in LDS before the barrier
-                if (more && !direct) {
-                    load_values(off_1);
-                    store_values(buf ^ 1, next, nowhere_1);
-                }
+                if (more) clean_values(buf ^ 1, next, nowhere_1);
             } else {
                 if (more) store_values(buf ^ 1, next, nowhere_1);
                 if (more_2) store_keys(buf);
