@@ -104,6 +104,7 @@ struct Plan {
     int rows;       // queries of a group
     int groups;     // groups of a kv head's queries
     bool chunk;     // of the chunk kernel: a group has a span of its own
+    bool whole;     // no walk is split
 };
 
 // One sequence's share: `first` items (counting one kv head) before its own.
@@ -195,7 +196,8 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
             all = now;
         }
     }
-    const uint32_t each = (all + 7) / 8, f = b % 8 * each + b / 8;
+    const uint32_t each = (all + 7) / 8, f = b % 8 * each + b / 8, of_head = all / a.Hk;
+    const uint32_t at_f = pl.whole ? f % of_head : f / a.Hk;        // among one kv head's items
     Item it{};
     it.slot = -1;
     it.spare = (int)(b - 8 * each);
@@ -211,7 +213,7 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
             const int x = __shfl_up(upto, o);
             if (lane >= o) upto += x;
         }
-        const uint64_t past = __ballot((uint32_t)(before + upto) * a.Hk > f);
+        const uint64_t past = __ballot((uint32_t)(before + upto) > at_f);
         if (past) {
             const int at = __builtin_ctzll(past);
             it.s = s0 + at;
@@ -226,12 +228,18 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
     // the sequence's runs, evened out
     const int even_run = (it.share.len + it.share.runs - 1) / it.share.runs;
     it.share.run = it.share.runs == 1 ? run : (even_run + pl.unit - 1) / pl.unit * pl.unit;
-    uint32_t in = f - (uint32_t)it.share.first * a.Hk;
     it.slot = (int)f;
-    it.group = (int)(in % it.share.groups);
-    in /= it.share.groups;
-    it.kvh = (int)(in % a.Hk);
-    it.split = (int)(in / a.Hk);
+    if (pl.whole) {
+        it.group = (int)(at_f - (uint32_t)it.share.first);
+        it.kvh = (int)(f / of_head);
+        it.split = 0;
+    } else {
+        uint32_t in = f - (uint32_t)it.share.first * a.Hk;
+        it.group = (int)(in % it.share.groups);
+        in /= it.share.groups;
+        it.kvh = (int)(in % a.Hk);
+        it.split = (int)(in / a.Hk);
+    }
     it.last = it.group == it.share.groups - 1;
     return it;
 }
