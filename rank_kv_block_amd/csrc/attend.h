@@ -104,7 +104,6 @@ struct Plan {
     int rows;       // queries of a group
     int groups;     // groups of a kv head's queries
     bool chunk;     // of the chunk kernel: a group has a span of its own
-    bool whole;     // no walk is split
 };
 
 // One sequence's share: `first` items (counting one kv head) before its own.
@@ -136,7 +135,9 @@ struct DraftWork {
 // Workgroup b of the grid, worked out by every wave alike.  Item f = ((first_s +
 // split * groups) * Hk ..): an XCD (b % 8) takes consecutive items, so the
 // groups that read the same bytes, and the heads whose bytes lie side by side,
-// meet in one L2.
+// meet in one L2.  In the chunk kernel, whose walks are of uneven length, kv heads
+// come first, so that an XCD has its part of every sequence (four prompts of
+// uneven length without a window: 513 us by sequence, 400 by head).
 template <typename Work>
 __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, Work work_of) {
     const int lane = threadIdx.x & 63;
@@ -197,7 +198,7 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
         }
     }
     const uint32_t each = (all + 7) / 8, f = b % 8 * each + b / 8, of_head = all / a.Hk;
-    const uint32_t at_f = pl.whole ? f % of_head : f / a.Hk;        // among one kv head's items
+    const uint32_t at_f = pl.chunk ? f % of_head : f / a.Hk;        // among one kv head's items
     Item it{};
     it.slot = -1;
     it.spare = (int)(b - 8 * each);
@@ -228,13 +229,16 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
     // the sequence's runs, evened out
     const int even_run = (it.share.len + it.share.runs - 1) / it.share.runs;
     it.share.run = it.share.runs == 1 ? run : (even_run + pl.unit - 1) / pl.unit * pl.unit;
-    it.slot = (int)f;
-    if (pl.whole) {
-        it.group = (int)(at_f - (uint32_t)it.share.first);
+    const uint32_t before_it = (uint32_t)it.share.first * a.Hk;
+    if (pl.chunk) {
+        const uint32_t in = at_f - (uint32_t)it.share.first;
+        it.group = (int)(in % it.share.groups);
+        it.split = (int)(in / it.share.groups);
         it.kvh = (int)(f / of_head);
-        it.split = 0;
+        it.slot = (int)(before_it + (it.split * a.Hk + it.kvh) * it.share.groups + it.group);
     } else {
-        uint32_t in = f - (uint32_t)it.share.first * a.Hk;
+        uint32_t in = f - before_it;
+        it.slot = (int)f;
         it.group = (int)(in % it.share.groups);
         in /= it.share.groups;
         it.kvh = (int)(in % a.Hk);

@@ -1452,7 +1452,6 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
     // (16 trees of 16 rows over up to 16416 tokens in 4 bits, where two tries leave 560 items for 512 places: 210 us, with
     // six 166.  bf16 and e4m3 caches without a window keep two, and with it the runs that they had.)
     pl.tries = a.cache.fp4 || a.window ? 6 : 2;
-    pl.whole = false;
     if (pl.chunk) {
         pl.rounds = 1;
         // Groups that fill the chip keep their tokens in one run (unit above any number of tokens), unless some may walk
@@ -1460,7 +1459,6 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
         const int64_t items = (int64_t)a.S * a.Hk * pl.groups;
         if (a.S == 1 ? items >= pl.slots : items >= 2ll * pl.slots && most_tokens(a, pl) <= 8192) {
             pl.unit = 1 << 30;
-            pl.whole = true;
             pl.tries = 0;       // and nothing is left to fit
         }
     }
