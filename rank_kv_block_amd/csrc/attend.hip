@@ -1425,7 +1425,8 @@ Kind kind_of(const AttendArgs& a) {
 int64_t most_tokens(const AttendArgs& a, const Plan& pl) {
     const int64_t all = (int64_t)a.n * a.B;
     if (!a.window) return all;
-    const int64_t rows = pl.chunk ? pl.rows / (a.Hq / a.Hk) + 2 : a.M, some = (int64_t)a.sinks + a.window + rows + 2 * 64;
+    const int64_t rows = pl.chunk ? pl.rows / (a.Hq / a.Hk) + 2 : a.M, tile = pl.chunk ? 64 : 32;
+    const int64_t some = (int64_t)a.sinks + a.window + rows + 2 * tile;      // (from and to a tile's edge)
     return some < all ? some : all;
 }
 
