@@ -445,8 +445,8 @@ int pred_rotate(pred_t* p, const pred_rope* rope, const pred_bf16* x, int64_t x_
  * scale, a float32 quotient, clamped to +-448 and rounded to the nearest (ties to
  * even), NaN kept.  An FP4 cache takes values rounded to bf16: the scale of 32 is
  * the smallest power of two, at least 2^-125 and at most 2^125, that keeps the
- * largest of them within 6, each value then the nearest (ties to the even pattern); a value that
- * is not finite makes its 32 values NaN.
+ * largest of them within 6, each value then the nearest (ties to the even
+ * pattern); a value that is not finite makes its 32 values NaN.
  * rope->backward must be 0, and the cache's k and v must not overlap (one
  * address for both is PRED_ERR_OUT_OF_RANGE). */
 int pred_rotate_store(pred_t* p, const pred_rope* rope, const pred_bf16* q, int64_t q_stride, const pred_bf16* k,

@@ -333,6 +333,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
 //           8 x J matrix that it transposes in registers with byte permutes.
 //           Tile j is then d = J p + j, and lane (n, c) ends with d = J (4 c +
 //           v) + j, J values side by side.
+// A 4-bit row is 64 bytes and its scales 4: lanes load a piece's scale beside it
+// and convert to bf16 in registers, exactly.
 // The weights enter as two bf16 terms (value and rest), so an output carries
 // about 16 bits of them; the matrix units are idle either way.
 //
@@ -346,7 +348,14 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
 // but streaming reads reaches 7.1.  About 18 us of a call are its start (lengths,
 // table, first tiles) and end: 1024 tokens of one head of 64 take 8.0 us.  17 to
 // 32 queries are two groups: 131072 tokens with 32 queries a head take 142 us and
-// move 771 MB, with 16 queries 95 us and 538 MB.
+// move 771 MB, with 16 queries 95 us and 538 MB.  4-bit caches: 131072 tokens (143
+// MB) 42 us, 64 sequences of up to 32768 (1.45 GB) 287, 5.1 TB/s; with a window of
+// 4096 184 us in bf16 (1.07 GB, 5.8 TB/s), 110 in e4m3, 69 in 4 bits.  Loads and
+// softmax without the products take 254 of the 287 us: pages of 1 KiB a head and
+// their scales 64 bytes at a time are what bounds it.  Tried on it and not kept: two
+// or three tiles ahead (39 us for 42, but 325 to 350 for 287), values turned by LDS
+// transpose reads (314), loads of masked tiles too (bf16 97 -> 100), addresses from a
+// scalar base (no change), three or four waves a SIMD (no change, spills).
 template <int D, Held HELD>
 struct StreamLayout {
     static constexpr int RB = (int)(HELD == FP4 ? D / 2 : (HELD == FP8 ? D : 2 * D));       // bytes of a row
@@ -1397,7 +1406,8 @@ constexpr int kRounds = 8;              // most workgroups a CU's places get one
 // Queries per kv head of the stream kernel.  Two groups of 16 read most bytes twice: over 131072 tokens of one sequence
 // 32 queries take 142 us with it, and 40 take 111 with the tree kernel; where they cross below 32 has not been measured.
 constexpr int kStreamQueries = 32;
-// and with a window: one group
+// and with a window: one group (16 queries over 16 sequences' windows of 4096: 58 us and 57 with the chunk kernel, from
+// a 4-bit cache 30 and 48; of one sequence 17 and 20, of 64 187 and 206)
 constexpr int kWindowQueries = 16;
 
 Kind kind_of(const AttendArgs& a) {
@@ -1455,10 +1465,14 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
     pl.tries = a.cache.fp4 || a.window ? 6 : 2;
     if (pl.chunk) {
         pl.rounds = 1;
-        // Groups that fill the chip keep their tokens in one run (unit above any number of tokens), unless some may walk
-        // much longer than others.
+        // Walks stay whole (unit above any number of tokens) where they are up to 8192 tokens, so that one of a few
+        // groups is not much longer than the others, and fill half of the chip's places, or, of one sequence, are alike
+        // and fill three quarters: the join and its sums cost more than the empty places.  In us, split and whole: one
+        // sequence of 32 heads with 1100 rows (280 groups of 512 places), window 1024 71 and 63, 4096 163 and 155,
+        // none and a context of 32768 916 and 1030; 1600 rows (400) 84 and 58, 180 and 157, 1088 and 1030; 4096 tokens of
+        // three sequences with up to 400 rows (300) 64 and 49, 3 x 4100 rows with a window of 1024 264 and 211.
         const int64_t items = (int64_t)a.S * a.Hk * pl.groups;
-        if (a.S == 1 ? items >= pl.slots : items >= 2ll * pl.slots && most_tokens(a, pl) <= 8192) {
+        if (most_tokens(a, pl) <= 8192 ? 2 * items >= pl.slots : a.S == 1 && 4 * items >= 3 * pl.slots) {
             pl.unit = 1 << 30;
             pl.tries = 0;       // and nothing is left to fit
         }

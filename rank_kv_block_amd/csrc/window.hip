@@ -27,7 +27,7 @@ struct ChunkWork {
 
 // What the rows of groups without a live row get, by the workgroups behind the
 // last item.  (As items between the others they left the XCDs work of uneven
-// length: three prompts, two of them of 3/4 of n_rows, 304 us, now %PROMPTS%.)
+// length: three prompts of 4100, 2470 and 2370 rows of n_rows 4100, 304 us, 249 so.)
 __device__ inline void dead_groups(const AttendArgs& a, const Plan& pl, int spare, int spares) {
     const int lane = threadIdx.x & 63, g = a.Hq / a.Hk;
     const int64_t R = (int64_t)a.M * g;
@@ -69,16 +69,37 @@ __device__ inline void dead_groups(const AttendArgs& a, const Plan& pl, int spar
 // (n = lane % 32, f = lane / 32) owns query n.
 //
 // A group walks only the tiles that some row of it sees (Span): the sinks' and
-// from its first row's window on, up to its last row.  A wave skips a tile that
-// none of its rows sees.  Tiles that every row of the group sees whole need no
-// masks, and those of a bf16 cache go straight into LDS; in the others values
-// that are not finite are taken out on the way (the tree kernel's drafted tokens).
+// from its first row's window on, up to its last row.  Tiles that every row of
+// the group sees whole need no masks; in the others values that are not finite
+// become 0 (the tree kernel's drafted tokens).  bf16 goes straight into LDS and
+// is cleaned there; narrow types are converted in registers on the way.
+//
+// A step: the loads of the next tile's values and of the keys of the one after it
+// are issued; this tile's exponentials, and beside them, for the matrix cores,
+// the next tile's scores; then the product with this tile's values, each read
+// from LDS a step ahead.  So a wave has work for the vector units and for the
+// matrix cores at a time (2048 rows of 8 queries for each of 8 heads of 128 on a
+// window of 4096 tokens: 458 us with scores and exponentials of the same tile,
+// 400 so; 400 -> 380 with the bank conflicts below taken out, -> 375 with values
+// a step ahead).
 //
 // The weights enter the value product as one bf16 term, 2^-8 of a weight off at
 // most (the stream and tree kernels' two terms would be half as many matrix
-// instructions again, and these are what long chunks are bound by): an output is
-// 2^-8 of the weighted mean of the absolute values off at most.  Where the values
-// are of either sign that is about what the output's own rounding to bf16 adds.
+// instructions again): an output is 2^-8 of the weighted mean of the absolute
+// values off at most.  Where the values are of either sign that is about what the
+// output's own rounding to bf16 adds (error against 64 bits 0.0023 relative, 0.0017
+// with the rounding alone).
+//
+// Bound: the instructions of two waves a SIMD (the registers' limit).  Measured,
+// that call (275 GFLOP of pairs that are seen) with the clock up: 330 us from a 4-bit
+// cache, 834 TFLOP/s, 332 from bf16, 343 from e4m3, some 15% more on a card that was
+// idle; a matrix product of the library's reaches 1217.  Three prompts of up to 4100
+// rows, 4 queries for each of 8 heads, window 1024: 222 to 296 us by their lengths.
+// Short walks pay about 14 us of an item's start and end (18 tiles: 651 TFLOP/s).
+// Tried and not kept: instruction orders laid down by hand, products k by k through
+// both halves, wave priorities (all slower), eight waves of 32 queries (2%), 64
+// queries a wave with one wave a SIMD (530 us, spills).  The stage's part of the
+// time is about a quarter (286 us where its loads were left out).
 template <int D, Held HELD>
 __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan pl, BlockSize bs) {
     using T = TreeLds<D>;
