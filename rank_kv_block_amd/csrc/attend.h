@@ -198,13 +198,13 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
             all = now;
         }
     }
-    const uint32_t each = (all + 7) / 8, f = b % 8 * each + b / 8, of_head = all / a.Hk;
-    const uint32_t at_f = pl.chunk ? f % of_head : f / a.Hk;        // among one kv head's items
+    const uint32_t each = (all + 7) / 8, f = b % 8 * each + b / 8;
     Item it{};
     it.slot = -1;
     it.spare = (int)(b - 8 * each);
     it.spares = (int)(gridDim.x - 8 * each);
     if (b / 8 >= each || f >= all) return it;
+    const uint32_t of_head = all / a.Hk, at_f = pl.chunk ? f % of_head : f / a.Hk;      // among one kv head's items
     int before = 0;
     for (int s0 = 0; s0 < a.S; s0 += 64) {
         int len, groups;

@@ -379,6 +379,24 @@ def test_far_pages(kind, N, M):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M,kind", [(1, "bf16"), (1, "fp4"), (40, "bf16"), (300, "fp4")])
+def test_nobody_has_anything(M, kind):
+    """Lengths of zero, no row of any sequence, a table of no blocks: zeros and -inf everywhere, no error."""
+    S, Hq, Hk, D, B, n = 70, 8, 2, 128, 16, 3
+    c = make(kind, S, M, Hq, Hk, D, B, n, lens=[0] * S, drafts=[0] * S)
+    with _handle(Hq, Hk, D, B, c.N) as p:
+        for lens in (c.lens, torch.full_like(c.lens, 20)):
+            c.lens = lens
+            c.run(p, 30, 4)
+            assert torch.all(c.out == 0) and torch.all(torch.isneginf(c.lse))
+        c.out.fill_(9.0)
+        c.lse.fill_(9.0)
+        c.lens.zero_()
+        rk.pred_attend_window(p.handle, c.kv, c.q, c.tables[:, :0].contiguous(), c.lens, None, 30, 4, c.scale, c.out, c.lse, None)
+        rk.pred_device_error(p.handle)
+        assert torch.all(c.out == 0) and torch.all(torch.isneginf(c.lse))
+
+
 def test_no_table_no_lengths():
     for M in (1, 70):
         c = make("bf16", 2, M, 8, 2, 128, 16, 9, identity=True, ragged=False, drafts=[M, M])
