@@ -157,20 +157,23 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
             read(s0 + lane, len, groups);
         }
     };
-    int64_t total = 0;
-    for (int s0 = 0; s0 < a.S; s0 += 64) {
-        int len, groups;
-        sequence(s0, len, groups);
-        total += (int64_t)len * groups;
-    }
-    if (a.S > 1)
-        for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o);
-    // (lane 0 has a single sequence's) the same in every lane from here on, in scalar registers
-    total = ((int64_t)__builtin_amdgcn_readfirstlane((int)(total >> 32)) << 32 |
-             (uint32_t)__builtin_amdgcn_readfirstlane((int)total)) * a.Hk;
-    const int64_t per_slot = total / pl.slots, rounds = per_slot / pl.run;
-    const int64_t items = (int64_t)pl.slots * (rounds < 1 ? 1 : (rounds < pl.rounds ? rounds : pl.rounds));
-    const int64_t wanted = ((total + items - 1) / items + pl.unit - 1) / pl.unit * pl.unit;
+    auto wanted_run = [&]() {
+        int64_t total = 0;
+        for (int s0 = 0; s0 < a.S; s0 += 64) {
+            int len, groups;
+            sequence(s0, len, groups);
+            total += (int64_t)len * groups;
+        }
+        if (a.S > 1)
+            for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o);
+        // (lane 0 has a single sequence's) the same in every lane from here on, in scalar registers
+        total = ((int64_t)__builtin_amdgcn_readfirstlane((int)(total >> 32)) << 32 |
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)total)) * a.Hk;
+        const int64_t per_slot = total / pl.slots, rounds = per_slot / pl.run;
+        const int64_t items = (int64_t)pl.slots * (rounds < 1 ? 1 : (rounds < pl.rounds ? rounds : pl.rounds));
+        const int64_t wanted = ((total + items - 1) / items + pl.unit - 1) / pl.unit * pl.unit;
+        return (int)(wanted < pl.shortest ? pl.shortest : (wanted < 0x7FFFFFFF ? wanted : 0x7FFFFFFF));
+    };
     auto items_of = [&](int run) {
         int count = 0;      // of one kv head
         for (int s0 = 0; s0 < a.S; s0 += 64) {
@@ -182,7 +185,7 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
             for (int o = 32; o >= 1; o >>= 1) count += __shfl_xor(count, o);
         return (uint32_t)__builtin_amdgcn_readfirstlane(count) * a.Hk;
     };
-    int run = (int)(wanted < pl.shortest ? pl.shortest : (wanted < 0x7FFFFFFF ? wanted : 0x7FFFFFFF));
+    int run = pl.tries ? wanted_run() : pl.shortest;     // (without tries walks stay whole)
     uint32_t all = items_of(run);
     // Every sequence's last run is a part of one, so the items are a few more than wanted.  Where they pass one round
     // by up to a quarter, runs a little longer do without the second, nearly empty one (8 sequences of 5k tokens, 13
