@@ -1546,7 +1546,9 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     if (rows > 0x7FFFFFFF / a.Hq) return hipErrorInvalidConfiguration;
     const uint32_t row_grid = (uint32_t)(rows * a.Hq);
     const Kind kind = kind_of(a);
+    auto threads_fit = [](int64_t threads) { return threads <= 0xFFFFFFFFll; };     // of a launch
     if (kind == Kind::Plain) {
+        if (!threads_fit(256ll * row_grid)) return hipErrorInvalidConfiguration;
         const Held held = held_of(a.cache);
         auto launch = [&](auto held) {
             if (a.window) attend_plain_kernel<decltype(held)::value, true><<<row_grid, 256, 0, stream>>>(a);
@@ -1564,7 +1566,9 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     // an XCD's items are numbered from the whole's eighth, rounded up
     // (and the chunk kernel's dead groups take workgroups behind the last)
     const int64_t grid = (most_items(a, pl) + 7) / 8 * 8 + (pl.chunk ? 8 : 0);
-    if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
+    // the join's launch too, before anything is enqueued (its kernel of 256 threads a row is for few rows)
+    if (!grid_fits(grid) || !threads_fit(256 * grid) || (split && !threads_fit((int64_t)row_grid * (a.D / 4) + 256)))
+        return hipErrorInvalidConfiguration;
     auto launch = [&](auto held) {
         if (a.D == 64) launch_fast<64, decltype(held)::value>(b, kind, pl, (uint32_t)grid, stream);
         else launch_fast<128, decltype(held)::value>(b, kind, pl, (uint32_t)grid, stream);

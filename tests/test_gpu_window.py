@@ -463,6 +463,23 @@ def test_steps_in_a_graph_and_on_another_stream():
                 assert torch.equal(a, b), i
 
 
+def test_more_rows_than_a_launch_has_threads():
+    """2^24 rows of heads for the kernel that gives each a workgroup of 256: refused, and nothing written."""
+    Hq, D, B, M = 64, 32, 16, 1 << 18
+    q = torch.zeros((1, M, Hq, D), dtype=BF16, device="cuda")
+    out = torch.full_like(q, 9.0)
+    k, v = (torch.zeros((1, B, 1, D), dtype=BF16, device="cuda") for _ in range(2))
+    lens, tab = torch.ones((1,), dtype=torch.int32, device="cuda"), torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    with _handle(Hq, 1, D, B, 1) as p:
+        with pytest.raises(rk.PredError):
+            rk.pred_attend_window(p.handle, rk.KVCache(k, v), q, tab, lens, None, 5, 0, 1.0, out)
+        assert torch.all(out == 9.0)
+        rows = M - 1
+        rk.pred_attend_window(p.handle, rk.KVCache(k, v), q[:, :rows], tab, lens, None, 5, 0, 1.0, out[:, :rows])
+        rk.pred_device_error(p.handle)
+        assert torch.all(out[:, :rows] == 0) and torch.all(out[:, rows:] == 9.0)
+
+
 def test_two_calls_at_once():
     """Two batches of one handle on two streams, each with its workspace, many times over: the bits of one after another."""
     Hq, Hk, D, B, n = 8, 2, 128, 16, 300
