@@ -426,6 +426,9 @@ __global__ __launch_bounds__(256) void load_kernel(LoadArgs a, int pieces, int p
     }
 }
 
+// of a launch, which has at most 2^32 - 1 threads (and these grids are rounded up to 32 waves)
+constexpr int64_t kMostWaves = (1ll << 26) - 32;
+
 int heads_a_wave(int D, int at_once) { return 64 / (D / 8) * at_once; }
 
 // fn(lanes of a head where one of the variants has them, pairs side by side or not)
@@ -451,7 +454,7 @@ hipError_t launch_norm_rotate(const NormArgs& a, hipStream_t stream) {
     // 1024 5.0 and 5.5, 4096 11.4 and 8.3
     auto chunks_of = [&](int deep) { return (heads + heads_a_wave(a.rows.D, deep) - 1) / heads_a_wave(a.rows.D, deep); };
     const int deep = a.rows.n_tokens * chunks_of(kNormHeads) <= 1024 ? 1 : kNormHeads, chunks = chunks_of(deep);
-    if (a.rows.n_tokens > 0x7FFFFFF0ll * 4 / chunks) return hipErrorInvalidConfiguration;
+    if (a.rows.n_tokens > kMostWaves / chunks) return hipErrorInvalidConfiguration;
     const uint32_t grid = (uint32_t)((a.rows.n_tokens * chunks + 31) / 32 * 8);
     norm_variant(pieces, a.rows.interleaved || !a.rows.rot, [&](auto p, auto inter) {
         norm_rotate_kernel<decltype(p)::value, decltype(inter)::value><<<grid, 256, 0, stream>>>(a, pieces, chunks, deep);
@@ -489,9 +492,8 @@ hipError_t launch_load(const LoadArgs& a, hipStream_t stream) {
     // a wave a token, or where these are few one for each 64 of its pieces: 16 heads of 128 in 4 bits, 64 tokens 3.3 us in
     // parts and 4.9 without, 1024 4.3 and 5.3, 2048 5.7 and 5.6, 4096 7.6 and 6.9
     const int pieces = a.D / 8, all = (2 * a.Hk * pieces + 63) / 64, parts = a.n_tokens < 2048 ? all : 1;
-    if (a.n_tokens > 0x7FFFFFF0ll * 4) return hipErrorInvalidConfiguration;
+    if (a.n_tokens > kMostWaves / parts) return hipErrorInvalidConfiguration;
     const int64_t grid = (a.n_tokens * parts + 31) / 32 * 8;
-    if (!grid_fits(grid)) return hipErrorInvalidConfiguration;
     load_kernel<<<(uint32_t)grid, 256, 0, stream>>>(a, pieces, parts);
     return hipGetLastError();
 }

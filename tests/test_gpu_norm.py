@@ -538,6 +538,26 @@ def test_other_stream_and_nothing_to_do():
         assert torch.equal(out, want)
 
 
+def test_as_many_tokens_as_a_launch_has_waves():
+    """A wave a token: 2^26 - 32 of them run, one more is refused and nothing is written."""
+    n = 2 ** 26 - 32
+    x = torch.ones((n + 1, 1, 8), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(x, 9.0)
+    slots = torch.zeros((n + 1,), dtype=torch.int64, device="cuda")
+    k, v = (torch.full((1, 1, 1, 8), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    with _handle(1, 1, 8, 1, 1) as p:
+        norm, kv = rk.Norm(None, 1e-6), rk.KVCache(k, v)
+        for call in (lambda n: rk.pred_norm_rotate(p.handle, norm, None, x[:n], None, out[:n]),
+                     lambda n: rk.pred_load(p.handle, kv, slots[:n], out[:n], x[:n])):
+            out.fill_(9.0)
+            with pytest.raises(rk.PredError):
+                call(n + 1)
+            assert torch.all(out == 9.0) and torch.all(x == 1.0)
+            call(n)
+            rk.pred_device_error(p.handle)
+            assert torch.all(out[n:] == 9.0) and (out[:n] - out[0]).abs().max() == 0 and out[0, 0, 0] in (1.0, 3.0)
+
+
 def test_refusals():
     D, B, Hk, N = 64, 16, 2, 8
     z = dict(device="cuda")
