@@ -89,9 +89,10 @@ class _Args:
         self._place(t, what, _BF16)
         if t.shape != (n, heads, dim):
             raise ValueError(f"{what} must be [{n}, {heads}, {dim}], not {list(t.shape)}")
-        if n and heads and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)):
+        token, head, value = t.stride()     # (one call of it: each by itself takes as long as all)
+        if n and heads and ((dim > 1 and value != 1) or (heads > 1 and head != dim)):
             raise ValueError(f"{what}: a token's heads must be contiguous")
-        return t.data_ptr(), t.stride(0) if n > 1 else heads * dim
+        return t.data_ptr(), token if n > 1 else heads * dim
 
     def buffer(self, t, what):
         """(pointer, bytes) of a workspace."""
