@@ -64,7 +64,8 @@ __global__ __launch_bounds__(256) void attend_plain_kernel(AttendArgs a) {
         const int64_t slot = a.tables ? a.tables[(int64_t)s * a.n + b] : b;
         const bool good = slot >= 0 && slot < a.N;
         if (WINDOW && (b * a.B > pos || (b * a.B >= a.sinks && (b + 1) * a.B <= first))) continue;     // no token of it seen
-        if (!good && lane == 0) atomicOr(a.err, DEVERR_TABLE);
+        // (with a window the entries that count are those of tokens some row sees, and each live row meets its own)
+        if (!good && lane == 0 && (!WINDOW || live)) atomicOr(a.err, DEVERR_TABLE);
         float bm = kLowest, bl = 0.f;
         for (int t0 = 0; good && live && t0 < a.B && b * a.B + t0 < len; t0 += 64) {
             const int t = b * a.B + t0 + lane;
