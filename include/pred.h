@@ -574,9 +574,10 @@ const char* pred_attend_kernel_name(pred_t* p, const pred_kv_cache* cache, int32
  * The other arguments, and what is said of rows past row_len, of masked tokens,
  * of values that are not finite and of lengths and entries out of range, are
  * pred_attend's.  Entries of blocks of which no row sees a token need not be
- * valid: those blocks may have been given back.  With more than 16 queries per
- * kv head (n_rows * num_q_heads / num_kv_heads) a weight enters its product with
- * a value as one bf16 term. */
+ * valid: those blocks may have been given back.  A weight enters its product with a
+ * value as in pred_attend up to 16 queries per kv head (n_rows * num_q_heads /
+ * num_kv_heads); above that, in the chunk kernel, as one bf16 term, so an output is
+ * off by up to 2^-8 of the weighted mean of the absolute values more. */
 int pred_attend_window(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q, int32_t n_rows,
                        const int32_t* block_tables, int64_t n_blocks, int32_t n_seqs, const int32_t* kv_len,
                        const int32_t* row_len, int32_t window, int32_t n_sinks, float scale, pred_bf16* out, float* lse,

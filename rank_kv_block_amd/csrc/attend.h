@@ -45,6 +45,17 @@ __device__ inline uint32_t bf16_pair(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){lo, hi}, bf16x2_t));
 }
 
+// x less its bf16 value, half HI of `pair`: exact, as one dot product.  The
+// factor -1 is kept in a register: as an operand (-1, 0) the compiler writes
+// the inline constant -1.0, which the instruction takes for (0, -1).
+template <bool HI>
+__device__ inline float rest_of(float x, uint32_t pair) {
+    uint32_t minus_one = HI ? 0xBF800000u : 0x0000BF80u;
+    asm("" : "+s"(minus_one));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, pair), __builtin_bit_cast(bf16x2_t, minus_one), x,
+                                           false);
+}
+
 __device__ inline uint16_t to_bf16(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
 
 __device__ inline float fp8_value(uint32_t byte) { return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0); }
@@ -365,6 +376,11 @@ __device__ inline const char* value_row(const AttendArgs& a, const BlockSize& bs
     if constexpr (HELD == FP4) return reinterpret_cast<const char*>(a.cache.v_scales) + at / 32;
     return static_cast<const char*>(a.cache.v) + bytes_of<HELD>(at);
 }
+
+// Queries per kv head that the stream kernel takes with a window: one group (16 queries over 16 sequences' windows of
+// 4096: 58 us and 57 with the chunk kernel, from a 4-bit cache 30 and 48; of one sequence 17 and 20, of 64 187 and 206).
+// Up to so many a weight has two bf16 terms in the chunk kernel too.
+constexpr int kWindowQueries = 16;
 
 // LDS tiles of the tree and chunk kernels.
 template <int D>

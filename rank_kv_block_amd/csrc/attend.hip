@@ -384,17 +384,6 @@ __device__ inline float sum_over_c(float x) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// x less its bf16 value, half HI of `pair`: exact, as one dot product.  The
-// factor -1 is kept in a register: as an operand (-1, 0) the compiler writes
-// the inline constant -1.0, which the instruction takes for (0, -1).
-template <bool HI>
-__device__ inline float rest_of(float x, uint32_t pair) {
-    uint32_t minus_one = HI ? 0xBF800000u : 0x0000BF80u;
-    asm("" : "+s"(minus_one));
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, pair), __builtin_bit_cast(bf16x2_t, minus_one), x,
-                                           false);
-}
-
 // The blocks of one sequence as a wave walks it: 64 blocks at a time, a lane
 // each holding where its block lies (bytes from the head's start of the cache).
 // Entries that are invalid, or of blocks the sequence does not use, stand for
@@ -1407,10 +1396,6 @@ constexpr int kRounds = 8;              // most workgroups a CU's places get one
 // Queries per kv head of the stream kernel.  Two groups of 16 read most bytes twice: over 131072 tokens of one sequence
 // 32 queries take 142 us with it, and 40 take 111 with the tree kernel; where they cross below 32 has not been measured.
 constexpr int kStreamQueries = 32;
-// and with a window: one group (16 queries over 16 sequences' windows of 4096: 58 us and 57 with the chunk kernel, from
-// a 4-bit cache 30 and 48; of one sequence 17 and 20, of 64 187 and 206)
-constexpr int kWindowQueries = 16;
-
 Kind kind_of(const AttendArgs& a) {
     const Held held = held_of(a.cache);
     auto bytes = [held](int64_t x) { return held == FP4 ? bytes_of<FP4>(x) : (held == FP8 ? bytes_of<FP8>(x) : bytes_of<BF16>(x)); };

@@ -83,12 +83,15 @@ __device__ inline void dead_groups(const AttendArgs& a, const Plan& pl, int spar
 // 400 so; 400 -> 380 with the bank conflicts below taken out, -> 375 with values
 // a step ahead).
 //
-// The weights enter the value product as one bf16 term, 2^-8 of a weight off at
-// most (the stream and tree kernels' two terms would be half as many matrix
-// instructions again): an output is 2^-8 of the weighted mean of the absolute
-// values off at most.  Where the values are of either sign that is about what the
-// output's own rounding to bf16 adds (error against 64 bits 0.0023 relative, 0.0017
-// with the rounding alone).
+// With more than kWindowQueries queries per kv head the weights enter the value
+// product as one bf16 term, 2^-8 of a weight off at most (the stream and tree
+// kernels' two terms would be half as many matrix instructions again): an output is
+// 2^-8 of the weighted mean of the absolute values off at most.  Where the values
+// are of either sign that is about what the output's own rounding to bf16 adds
+// (error against 64 bits 0.0023 relative, 0.0017 with the rounding alone).  Fewer
+// queries, which come here where the cache's layout is not the stream kernel's, have
+// two terms as they have there, so that a call's precision goes by its queries (one
+// token of 32 heads of 64 over 131072 in 4 bits: 61 us with one term, 68 with two).
 //
 // Bound: the instructions of two waves a SIMD (the registers' limit).  Measured,
 // that call (275 GFLOP of pairs that are seen) with the clock up: 330 us from a 4-bit
@@ -309,9 +312,9 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
     __syncthreads();
     // A tile's scores are worked out one tile ahead, beside the exponentials of this one: the matrix cores and the vector
     // units each have work of a wave then.  So keys are a tile ahead of values in the stage.
-    // HALVES = 2: the whole of every tile; 1: half `mine` of it
-    auto walk = [&](auto halves_, const int mine) {
-        constexpr int HALVES = decltype(halves_)::value;
+    // HALVES = 2: the whole of every tile; 1: half `mine` of it.  TERMS: of a weight
+    auto walk = [&](auto halves_, const int mine, auto terms_) {
+        constexpr int HALVES = decltype(halves_)::value, TERMS = decltype(terms_)::value;
         f32x16_t x[HALVES];
         auto scores = [&](int buf) {
             const char* const kt = keys + buf * T::kTile + (HALVES == 1 ? 32 * mine * T::kRow : 0);
@@ -396,7 +399,7 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[d] *= alpha;
                 }
-                u32x4_t w[HALVES][2];       // the weights as second operands
+                u32x4_t w[HALVES][2], rest[HALVES][2];      // the weights as second operands, and their second terms
 #pragma unroll
                 for (int h = 0; h < HALVES; ++h) {
                     float part_l[2] = {0.f, 0.f};
@@ -407,7 +410,12 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
                     }
                     l += part_l[0] + part_l[1];
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) w[h][y / 4][y % 4] = bf16_pair(x[h][2 * y], x[h][2 * y + 1]);
+                    for (int y = 0; y < 8; ++y) {
+                        const uint32_t pair = bf16_pair(x[h][2 * y], x[h][2 * y + 1]);
+                        w[h][y / 4][y % 4] = pair;
+                        if constexpr (TERMS == 2)
+                            rest[h][y / 4][y % 4] = bf16_pair(rest_of<false>(x[h][2 * y], pair), rest_of<true>(x[h][2 * y + 1], pair));
+                    }
                 }
                 scores(buf ^ 1);        // of the next tile (of what lies there, if there is none)
                 const char* const vt = values + buf * T::kTile + (HALVES == 1 ? 32 * mine * T::kRow : 0);
@@ -432,6 +440,12 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
                     for (int d = 0; d < DT; ++d)
                         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                             val[step & 1][d], __builtin_bit_cast(bf16x8_t, w[step / 2][step % 2]), o[d], 0, 0, 0);
+                    if constexpr (TERMS == 2) {
+#pragma unroll
+                        for (int d = 0; d < DT; ++d)
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                val[step & 1][d], __builtin_bit_cast(bf16x8_t, rest[step / 2][step % 2]), o[d], 0, 0, 0);
+                    }
                 }
             }
             if (HELD == BF16) {
@@ -448,8 +462,11 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
         }
     };
     if (v0 < v1) {
-        if (pairs) walk(std::integral_constant<int, 1>(), wave % 2);
-        else walk(std::integral_constant<int, 2>(), 0);
+        constexpr std::integral_constant<int, 1> one{};
+        constexpr std::integral_constant<int, 2> two{};
+        if (!pairs) walk(two, 0, one);
+        else if (R > kWindowQueries) walk(one, wave % 2, one);
+        else walk(one, wave % 2, two);
     }
 
     l = sum_over_f(l);
