@@ -568,7 +568,8 @@ const char* pred_attend_kernel_name(pred_t* p, const pred_kv_cache* cache, int32
  * prompt).  With d = row_len, row i < d is token p = kv_len - d + i and sees the
  * `window` newest tokens up to itself, p - window + 1 .. p, and the sequence's first
  * n_sinks up to itself; window INT32_MAX hides nothing.
- *   n_rows    [1, 2^24], at most 2^30 queries per kv head
+ *   n_rows    [1, 2^24], at most 2^30 queries per kv head; where a row sees up to 8192 tokens the work is divided by
+ *             it, so a call of few rows is best made with few n_rows (16 rows, window 4096: 27 us, of 2048 99)
  *   row_len   device, [n_seqs] int32 in [0, min(n_rows, kv_len)], or NULL for that upper limit
  *   window    >= 1;  n_sinks >= 0
  * The other arguments, and what is said of rows past row_len, of masked tokens,
@@ -584,8 +585,12 @@ int pred_attend_window(pred_t* p, const pred_kv_cache* cache, const pred_bf16* q
                        void* workspace, size_t ws_bytes, void* stream);
 
 /* Workspace of pred_attend_window for this shape on this handle; 0 for a NULL
- * handle or arguments that the call refuses.  Calls that may run at the same time
- * need workspaces of their own. */
+ * handle or arguments that the call refuses, and where no walk is split: short
+ * windows, and prompts of many rows that see up to 8192 tokens.  Calls that may run
+ * at the same time need workspaces of their own.  On 256 CUs one sequence needs at
+ * most 57 MiB.  Of several of which a row may see more than 8192 tokens it grows
+ * with n_seqs * n_rows, by 4 * (head_dim + 2) bytes for each query: 413 MiB for two
+ * prompts of 12000 rows (32 query and 8 kv heads of 128), 3.1 GiB for two of 100000. */
 size_t pred_attend_window_workspace_bytes(pred_t* p, int32_t n_seqs, int32_t n_rows, int64_t n_blocks, int32_t window,
                                           int32_t n_sinks);
 

@@ -115,7 +115,10 @@ struct Plan {
     int rows;       // queries of a group
     int groups;     // groups of a kv head's queries
     bool chunk;     // of the chunk kernel: a group has a span of its own
+    int whole_from; // and this many live items (or more) have whole walks; 0: what the run says
+    int64_t parts;  // items that may have partial results
 };
+constexpr int kWhole = 1 << 30;     // a run above any number of tokens
 
 // One sequence's share: `first` items (counting one kv head) before its own.
 struct Share {
@@ -134,6 +137,7 @@ __device__ inline int runs_of(int len, int run) { return len > run ? (len + run 
 
 // The tokens a group of sequence s walks and its groups, by the lengths alone.
 struct DraftWork {
+    static constexpr bool kChunk = false;
     const AttendArgs& a;
     const Plan& pl;
     __device__ inline void operator()(int s, int& len, int& groups) const {
@@ -196,14 +200,15 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
             for (int o = 32; o >= 1; o >>= 1) count += __shfl_xor(count, o);
         return (uint32_t)__builtin_amdgcn_readfirstlane(count) * a.Hk;
     };
-    int run = pl.tries ? wanted_run() : pl.shortest;     // (without tries walks stay whole)
+    const bool whole = Work::kChunk && (pl.tries == 0 || (pl.whole_from > 0 && items_of(kWhole) >= (uint32_t)pl.whole_from));
+    int run = whole ? kWhole : wanted_run();
     uint32_t all = items_of(run);
     // Every sequence's last run is a part of one, so the items are a few more than wanted.  Where they pass one round
     // by up to a quarter, runs a little longer do without the second, nearly empty one (8 sequences of 5k tokens, 13
     // rows: 78 us without, 70 with; with more rounds there is nothing to gain).
     const uint32_t one = (uint32_t)pl.slots;
     int longer = run;
-    for (uint32_t tries = 0, now = all; tries < (uint32_t)pl.tries && all > one && all - one <= one / 4; ++tries) {
+    for (uint32_t tries = 0, now = all; !whole && tries < (uint32_t)pl.tries && all > one && all - one <= one / 4; ++tries) {
         const int64_t fits = ((int64_t)longer * now / one + pl.unit) / pl.unit * pl.unit;
         longer = (int)(fits < 0x40000000 ? fits : 0x40000000 / pl.unit * pl.unit);
         now = items_of(longer);
@@ -218,7 +223,7 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
     it.spare = (int)(b - 8 * each);
     it.spares = (int)(gridDim.x - 8 * each);
     if (b / 8 >= each || f >= all) return it;
-    const uint32_t of_head = all / a.Hk, at_f = pl.chunk ? f % of_head : f / a.Hk;      // among one kv head's items
+    const uint32_t of_head = all / a.Hk, at_f = Work::kChunk ? f % of_head : f / a.Hk;      // among one kv head's items
     int before = 0;
     for (int s0 = 0; s0 < a.S; s0 += 64) {
         int len, groups;
@@ -245,7 +250,7 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
     const int even_run = (it.share.len + it.share.runs - 1) / it.share.runs;
     it.share.run = it.share.runs == 1 ? run : (even_run + pl.unit - 1) / pl.unit * pl.unit;
     const uint32_t before_it = (uint32_t)it.share.first * a.Hk;
-    if (pl.chunk) {
+    if constexpr (Work::kChunk) {
         const uint32_t in = at_f - (uint32_t)it.share.first;
         it.group = (int)(in % it.share.groups);
         it.split = (int)(in / it.share.groups);
@@ -263,18 +268,15 @@ __device__ inline Item item_of(const AttendArgs& a, const Plan& pl, uint32_t b, 
     return it;
 }
 
-// Workspace: each sequence's share, then [items, rows, D] sums, then [items,
+// Workspace: each sequence's share, then [parts, rows, D] sums, then [parts,
 // rows] (maximum, total).
 __device__ inline Share* shares_of(const AttendArgs& a) { return static_cast<Share*>(a.ws); }
 __host__ __device__ inline int64_t share_bytes(int64_t S) { return (S * (int64_t)sizeof(Share) + 15) / 16 * 16; }
 __device__ inline float* part_sums(const AttendArgs& a, const Plan& pl, int64_t slot) {
     return reinterpret_cast<float*>(static_cast<char*>(a.ws) + share_bytes(a.S)) + slot * pl.rows * a.D;
 }
-__host__ __device__ inline int64_t most_items(const AttendArgs& a, const Plan& pl) {
-    return (int64_t)pl.slots * pl.rounds + (int64_t)a.S * a.Hk * pl.groups;
-}
 __device__ inline float2* part_stats(const AttendArgs& a, const Plan& pl, int64_t slot) {
-    return reinterpret_cast<float2*>(part_sums(a, pl, most_items(a, pl))) + slot * pl.rows;
+    return reinterpret_cast<float2*>(part_sums(a, pl, pl.parts)) + slot * pl.rows;
 }
 
 // Turns a product q k into units of log2: above 0, so that a masked -inf stays

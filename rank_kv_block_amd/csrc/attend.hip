@@ -198,39 +198,41 @@ __device__ inline void join_store(const AttendArgs& a, int D, uint32_t row, int 
 template <int D>
 __global__ __launch_bounds__(256) void attend_join_rows_kernel(AttendArgs a, Plan pl, uint32_t rows) {
     constexpr int lanes = D / 4, kAhead = 4;
-    const uint32_t row = blockIdx.x * (256 / lanes) + threadIdx.x / lanes;
     const int d4 = threadIdx.x % lanes;
-    if (row >= rows) return;
-    const JoinRow j = join_row(a, pl, row);
-    float m = kLowest, l = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = 0; x0 < j.runs; x0 += kAhead) {
-        float4 o[kAhead];
-        float2 st[kAhead];
+    if (pl.whole_from > 0 && shares_of(a)[0].runs == 1) return;      // (one sequence's walks)
+    for (uint32_t row = blockIdx.x * (256 / lanes) + threadIdx.x / lanes; row < rows; row += gridDim.x * (256 / lanes)) {
+        const JoinRow j = join_row(a, pl, row);
+        if (!j.wanted) continue;
+        float m = kLowest, l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x0 = 0; x0 < j.runs; x0 += kAhead) {
+            float4 o[kAhead];
+            float2 st[kAhead];
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-            st[e] = make_float2(kLowest, 0.f);
-            o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x0 + e >= j.runs) continue;
-            const int64_t slot = j.slot + (x0 + e) * j.step;
-            st[e] = part_stats(a, pl, slot)[j.in_group];
-            o[e] = reinterpret_cast<const float4*>(part_sums(a, pl, slot) + j.in_group * D)[d4];
+            for (int e = 0; e < kAhead; ++e) {
+                st[e] = make_float2(kLowest, 0.f);
+                o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (x0 + e >= j.runs) continue;
+                const int64_t slot = j.slot + (x0 + e) * j.step;
+                st[e] = part_stats(a, pl, slot)[j.in_group];
+                o[e] = reinterpret_cast<const float4*>(part_sums(a, pl, slot) + j.in_group * D)[d4];
+            }
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) top = fmaxf(top, st[e].x);
+            const float alpha = exp2_of(m - top);
+            m = top;
+            l *= alpha;
+            v = make_float4(v.x * alpha, v.y * alpha, v.z * alpha, v.w * alpha);
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const float f = exp2_of(st[e].x - top);
+                l += f * st[e].y;
+                v = make_float4(v.x + f * o[e].x, v.y + f * o[e].y, v.z + f * o[e].z, v.w + f * o[e].w);
+            }
         }
-        float top = m;
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) top = fmaxf(top, st[e].x);
-        const float alpha = exp2_of(m - top);
-        m = top;
-        l *= alpha;
-        v = make_float4(v.x * alpha, v.y * alpha, v.z * alpha, v.w * alpha);
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-            const float f = exp2_of(st[e].x - top);
-            l += f * st[e].y;
-            v = make_float4(v.x + f * o[e].x, v.y + f * o[e].y, v.z + f * o[e].z, v.w + f * o[e].w);
-        }
+        join_store(a, D, row, d4, join_not_finite(a, pl, j, D, d4, v), l, m);
     }
-    if (j.wanted) join_store(a, D, row, d4, join_not_finite(a, pl, j, D, d4, v), l, m);
 }
 
 // Rows of many runs: a workgroup each, wave w taking runs w, w + 4, ..: a lane
@@ -462,6 +464,7 @@ __device__ inline void stream_load(uint32_t* dst, const char* base, uint32_t off
 
 // A sequence's work where a window limits it.
 struct WindowWork {
+    static constexpr bool kChunk = false;
     const AttendArgs& a;
     __device__ inline void operator()(int s, int& len, int& groups) const {
         const int tokens = kv_len_of(a.kv_len, s, (int64_t)a.n * a.B), drafted = draft_len_of(a, s, tokens);
@@ -1426,6 +1429,11 @@ int64_t most_tokens(const AttendArgs& a, const Plan& pl) {
     return some < all ? some : all;
 }
 
+// Items of a call, and so its workgroups, at most.
+int64_t most_items(const AttendArgs& a, const Plan& pl) {
+    return (int64_t)pl.slots * pl.rounds + (int64_t)a.S * a.Hk * pl.groups;
+}
+
 Plan plan_of(const AttendArgs& a, Kind kind) {
     const bool tree = kind != Kind::Stream;
     const int queries = queries_of(a);
@@ -1449,18 +1457,25 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
     // (16 trees of 16 rows over up to 16416 tokens in 4 bits, where two tries leave 560 items for 512 places: 210 us, with
     // six 166.  bf16 and e4m3 caches without a window keep two, and with it the runs that they had.)
     pl.tries = a.cache.fp4 || a.window ? 6 : 2;
+    pl.whole_from = 0;
     if (pl.chunk) {
         pl.rounds = 1;
-        // Walks stay whole (unit above any number of tokens) where they are up to 8192 tokens, so that one of a few
-        // groups is not much longer than the others, and fill half of the chip's places, or, of one sequence, are alike
-        // and fill three quarters: the join and its sums cost more than the empty places.  In us, split and whole: one
-        // sequence of 32 heads with 1100 rows (280 groups of 512 places), window 1024 71 and 63, 4096 163 and 155,
-        // none and a context of 32768 916 and 1030; 1600 rows (400) 84 and 58, 180 and 157, 1088 and 1030; 4096 tokens of
-        // three sequences with up to 400 rows (300) 64 and 49, 3 x 4100 rows with a window of 1024 264 and 211.
+        // Walks stay whole where they are up to 8192 tokens, so that one of a few groups is not much longer than the others,
+        // and all groups fill half of the chip's places, or, of one sequence, are alike and the live ones fill three
+        // quarters: the join and its sums cost more than the empty places.  In us, split and whole: one sequence of 32 heads
+        // with 1100 rows (280 groups of 512 places), window 1024 71 and 63, 4096 163 and 155, none and a context of 32768
+        // 916 and 1030; 1600 rows (400) 84 and 58, 180 and 157, 1088 and 1030; 4096 tokens of three sequences with up to 400
+        // rows (300) 64 and 49, 3 x 4100 rows with a window of 1024 264 and 211.
+        // How many are live is known on the device only.  Above 8192 tokens that decides, at the price of a join that may
+        // find nothing to do: 16 live rows of n_rows 2048 over 131072 tokens took 3281 us where n_rows decided, 138 so.
+        // Up to 8192 n_rows does (16 rows alone and of 2048: 27 and 99 us with a window of 4096), so that whole prompts need
+        // neither join nor workspace.
         const int64_t items = (int64_t)a.S * a.Hk * pl.groups;
-        if (most_tokens(a, pl) <= 8192 ? 2 * items >= pl.slots : a.S == 1 && 4 * items >= 3 * pl.slots) {
-            pl.unit = 1 << 30;
-            pl.tries = 0;       // and nothing is left to fit
+        if (most_tokens(a, pl) > 8192) {
+            if (a.S == 1 && 4 * items >= 3 * pl.slots) pl.whole_from = (3 * pl.slots + 3) / 4;
+        } else if (2 * items >= pl.slots) {
+            pl.unit = kWhole;
+            pl.tries = 0;       // nothing is left to fit
         }
     }
     pl.shortest = pl.unit;
@@ -1468,6 +1483,9 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
     // sequence of 4 heads of 64 with 200 tokens in sight 11.1 -> 8.2 us, 32 heads of 128 14.0 -> 11.4, eight sequences
     // 13.8 -> 14.4; with 500 tokens the one run is no shorter, 11.2, or longer, 14.1 -> 16.9).
     if (a.window && !pl.chunk && !tree && most_tokens(a, pl) <= 3 * pl.unit) pl.shortest = 3 * pl.unit;
+    pl.parts = most_items(a, pl);
+    if (pl.whole_from > 0 && (int64_t)pl.slots * pl.rounds + pl.whole_from < pl.parts)      // (more live items have none)
+        pl.parts = (int64_t)pl.slots * pl.rounds + pl.whole_from;
     return pl;
 }
 
@@ -1475,7 +1493,7 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
 bool may_split(const AttendArgs& a, const Plan& pl) { return most_tokens(a, pl) > pl.shortest; }
 
 size_t plan_bytes(const AttendArgs& a, const Plan& pl) {
-    return may_split(a, pl) ? (size_t)(share_bytes(a.S) + most_items(a, pl) * pl.rows * (a.D + 2) * (int64_t)sizeof(float)) : 0;
+    return may_split(a, pl) ? (size_t)(share_bytes(a.S) + pl.parts * pl.rows * (a.D + 2) * (int64_t)sizeof(float)) : 0;
 }
 
 template <int D, Held HELD>
@@ -1501,7 +1519,12 @@ template <int D>
 void launch_join(const AttendArgs& a, const Plan& pl, uint32_t rows, hipStream_t stream) {
     constexpr uint32_t per = 256 / (D / 4);
     if ((int64_t)pl.slots * pl.rounds > 8ll * a.S * a.Hk * pl.groups) attend_join_kernel<D><<<rows, 256, 0, stream>>>(a, pl);
-    else attend_join_rows_kernel<D><<<(rows + per - 1) / per, 256, 0, stream>>>(a, pl, rows);
+    else {
+        // Where walks may turn out whole, places' worth of workgroups that take the rows in turns: nothing to do is then
+        // soon done (12000 rows of 32 heads: 20 us with a workgroup for each 8 of them, 4 so, of a call of 1288).
+        const uint32_t all = (rows + per - 1) / per, some = 8u * (uint32_t)pl.slots;
+        attend_join_rows_kernel<D><<<pl.whole_from > 0 && some < all ? some : all, 256, 0, stream>>>(a, pl, rows);
+    }
 }
 
 }  // namespace

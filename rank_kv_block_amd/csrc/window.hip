@@ -15,6 +15,7 @@ __device__ inline int live_groups(const AttendArgs& a, const Plan& pl, int draft
 // A sequence's work: the most that a group of it walks, and the groups that have
 // a live row.
 struct ChunkWork {
+    static constexpr bool kChunk = true;
     const AttendArgs& a;
     const Plan& pl;
     __device__ inline void operator()(int s, int& len, int& groups) const {

@@ -58,3 +58,70 @@ def test_two_terms_a_weight_up_to_16_queries(monkeypatch, S, M, Hq, Hk, D, B, n,
         rk.pred_device_error(p.handle)
         monkeypatch.setattr(rk, "pred_attend_window_kernel_name", lambda *a: "attend_stream_kernel")
         c.check(p, window, sinks)
+
+
+def _time(f, calls=10):
+    """us a call, the best of three."""
+    best = float("inf")
+    for _ in range(3):
+        f()
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(calls):
+            f()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) / calls * 1e3)
+    return best
+
+
+def test_few_live_rows_of_many():
+    """A captured step of 2048 rows whose last chunk has 16 of them, on a long context: the work is split as it is for a call
+    of 16 rows, which takes a thirtieth of one group's whole walk (3281 and 120 us when walks were left whole by n_rows); a
+    call in which all rows live keeps its walks whole.  Each against the oracle."""
+    Hq, Hk, D, B, n = 32, 8, 128, 16, 8192
+    few = make("bf16", 1, 16, Hq, Hk, D, B, n, lens=[n * B - 5], drafts=[16])
+    with _handle(Hq, Hk, D, B, few.N) as p:
+        few.run(p, ALL, 0)
+        q = torch.zeros((1, 2048, Hq, D), dtype=torch.bfloat16, device="cuda")
+        q[:, :16] = few.q
+        q[:, 16:] = float("nan")
+        out, lse = torch.full_like(q, 9.0), torch.full((1, 2048, Hq), 9.0, device="cuda")
+
+        def call(M, q, out, lse, ws):
+            rk.pred_attend_window(p.handle, few.kv, q, few.tables, few.lens, few.drafts, ALL, 0, few.scale, out, lse, ws)
+
+        ws = [torch.empty((max(1, rk.pred_attend_window_workspace_bytes(p.handle, 1, M, n, ALL, 0)),), dtype=torch.uint8, device="cuda")
+              for M in (16, 2048)]
+        call(2048, q, out, lse, ws[1])
+        rk.pred_device_error(p.handle)
+        few.check(p, ALL, 0)
+        few.out.copy_(out[:, :16])
+        few.lse.copy_(lse[:, :16])
+        few.check(p, ALL, 0)
+        assert torch.all(out[:, 16:] == 0) and torch.all(torch.isneginf(lse[:, 16:]))
+        alone = _time(lambda: call(16, few.q, few.out, few.lse, ws[0]))
+        among = _time(lambda: call(2048, q, out, lse, ws[1]))
+        print("16 rows", alone, "us, 16 of 2048", among, "us", flush=True)
+        assert among < 4 * alone
+
+
+@pytest.mark.parametrize("live", [1, 20, 33, 300, 1400, 1535, 1536, 1600, 2048])
+def test_rows_of_one_long_sequence(live):
+    """Live rows to either side of where the walks of one long sequence stay whole (384 groups of 512 places: 1536 rows)."""
+    Hq, Hk, D, B, n, M = 8, 8, 64, 16, 520, 2048 * 4
+    live *= 4
+    c = make("bf16", 1, M, Hq, Hk, D, B, n + 100, lens=[n * B + (live > n * B) * 100], drafts=[live])
+    with _handle(Hq, Hk, D, B, c.N) as p:
+        need = rk.pred_attend_window_workspace_bytes(p.handle, 1, M, c.n, ALL, 0)
+        assert 0 < need < 100 << 20
+        c.run(p, ALL, 0)
+        rk.pred_device_error(p.handle)
+        c.check(p, ALL, 0)
+
+
+def test_workspace_of_long_prompts():
+    """The partial results of one sequence are those of calls that can be split: no more for 2^20 rows than for 2^13."""
+    with _handle(32, 8, 128, 16, 4) as p:
+        sizes = [rk.pred_attend_window_workspace_bytes(p.handle, 1, M, 1 << 21, ALL, 0) for M in (1 << 11, 1 << 13, 1 << 20)]
+        assert 0 < sizes[0] <= sizes[1] == sizes[2] < 100 << 20
