@@ -432,6 +432,9 @@ int pred_load(pred_t* p, const pred_kv_cache* cache, int64_t n_tokens, const int
     const int64_t out_stride = (int64_t)d.num_kv_heads * d.head_dim;
     if ((rc = check_rows(p, k_out, out_stride, d.num_kv_heads, "load", "k_out"))) return rc;
     if ((rc = check_rows(p, v_out, out_stride, d.num_kv_heads, "load", "v_out"))) return rc;
+    // a lane counts 8 values of a token at a time, up to five times as far as the token goes, in 32 bits
+    if (out_stride > 1ll << 30)
+        return fail(PRED_ERR_UNSUPPORTED, "load: %d heads of %d are more than 2^30 values", d.num_kv_heads, d.head_dim);
     pred::LoadArgs a{};
     a.cache = view;
     a.slots = slots;
