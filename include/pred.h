@@ -507,8 +507,8 @@ int pred_store(pred_t* p, const pred_bf16* k, int64_t k_stride, const pred_bf16*
  * stand for, rounded to bf16 (exact for bf16 and FP4 caches), into k_out and
  * v_out, device, [n_tokens, num_kv_heads, head_dim] bf16, 16-byte aligned.  A
  * token whose slot is -1 or outside the cache leaves its rows as they were; the
- * latter raises the device error word.
- * num_kv_heads * head_dim <= 2^30 (PRED_ERR_UNSUPPORTED). */
+ * latter raises the device error word.  k_out and v_out must not overlap
+ * (PRED_ERR_OUT_OF_RANGE); num_kv_heads * head_dim <= 2^30 (PRED_ERR_UNSUPPORTED). */
 int pred_load(pred_t* p, const pred_kv_cache* cache, int64_t n_tokens, const int64_t* slots, pred_bf16* k_out,
               pred_bf16* v_out, void* stream);
 

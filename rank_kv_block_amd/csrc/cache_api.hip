@@ -435,6 +435,10 @@ int pred_load(pred_t* p, const pred_kv_cache* cache, int64_t n_tokens, const int
     // a lane counts 8 values of a token at a time, up to five times as far as the token goes, in 32 bits
     if (out_stride > 1ll << 30)
         return fail(PRED_ERR_UNSUPPORTED, "load: %d heads of %d are more than 2^30 values", d.num_kv_heads, d.head_dim);
+    // (more tokens than a launch takes are refused by it)
+    const uint64_t bytes = 2ull * out_stride * (n_tokens < 1ll << 26 ? n_tokens : 1ll << 26);
+    const uint64_t at_k = (uint64_t)(uintptr_t)k_out, at_v = (uint64_t)(uintptr_t)v_out;
+    if (at_k < at_v + bytes && at_v < at_k + bytes) return fail(PRED_ERR_OUT_OF_RANGE, "load: k_out overlaps v_out");
     pred::LoadArgs a{};
     a.cache = view;
     a.slots = slots;
