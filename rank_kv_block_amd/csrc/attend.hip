@@ -1012,7 +1012,7 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
         }
     };
     // 256 / CR is a multiple of 16, so a thread's rows share their permutation and lie a fixed step apart
-    const int turn = my_tok & (SPREAD - 1);     // of a thread's values: see turned()
+    const int turn = HELD == FP4 ? my_tok & (SPREAD - 1) : 0;       // of a thread's values: see turned()
     const int k_to = T::key(my_tok, SPREAD * my_piece), v_to = T::value(my_tok, SPREAD * my_piece) ^ (16 * turn);
     auto store_tile = [&](int buf, int t, uint64_t nowhere) {
         if (!mine_in) return;
@@ -1042,8 +1042,10 @@ __global__ __launch_bounds__(256, 2) void attend_tree_kernel(AttendArgs a, Plan 
         }
         char* const kt = lds + buf * T::kTile + k_to;
         char* const vt = lds + (2 + buf) * T::kTile + v_to;
+        if constexpr (HELD == FP4) {
 #pragma unroll
-        for (int x = 0; x < NR; ++x) vs[x] = turned<HELD>(vs[x], turn);
+            for (int x = 0; x < NR; ++x) vs[x] = turned(vs[x], turn);
+        }
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
             constexpr int kStep = 256 / CR * T::kRow;
@@ -1479,9 +1481,11 @@ Plan plan_of(const AttendArgs& a, Kind kind) {
         }
     }
     pl.shortest = pl.unit;
-    // A window of up to three of the shortest runs stays in one: the join's launch costs more than its split saves (one
-    // sequence of 4 heads of 64 with 200 tokens in sight 11.1 -> 8.2 us, 32 heads of 128 14.0 -> 11.4, eight sequences
-    // 13.8 -> 14.4; with 500 tokens the one run is no shorter, 11.2, or longer, 14.1 -> 16.9).
+    // A window of up to three of the shortest runs stays in one: the join's launch costs more than its split saves.  A call
+    // of 1, 8, 64 sequences with 150 / 256 / 310 tokens in sight, us split and whole: 4 heads of 64 11 to 13 and 9 to 11
+    // throughout; 32 heads of 128 14.5 and 12.7 / 14.2 / 12.9, 14.8 and 13.1 / 15.2 / 14.3, 21 / 26 / 28 and 19 / 24 / 25; the
+    // same in 4 bits 12.7 and 9.8 / 10.7 / 10.3, 13.0 and 10.3 / 11.6 / 11.4, 15 / 16 / 17 and 12 / 14 / 14.  With 500 tokens
+    // the one run is no shorter (4 heads 11.2) or longer (32 heads 14.1 and 16.9).
     if (a.window && !pl.chunk && !tree && most_tokens(a, pl) <= 3 * pl.unit) pl.shortest = 3 * pl.unit;
     pl.parts = most_items(a, pl);
     if (pl.whole_from > 0 && (int64_t)pl.slots * pl.rounds + pl.whole_from < pl.parts)      // (more live items have none)

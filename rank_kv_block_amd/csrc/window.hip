@@ -232,7 +232,7 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
             }
         }
     };
-    const int turn = my_tok & (SPREAD - 1);     // of a thread's values: see turned()
+    const int turn = HELD == FP4 ? my_tok & (SPREAD - 1) : 0;       // of a thread's values: see turned()
     const int k_to = T::key(my_tok, SPREAD * my_piece), v_to = T::value(my_tok, SPREAD * my_piece) ^ (16 * turn);
     char* const keys = lds;
     char* const values = lds + 2 * T::kTile;
@@ -264,8 +264,10 @@ __global__ __launch_bounds__(256, 2) void attend_chunk_kernel(AttendArgs a, Plan
             }
             if (odd) any_odd = 1;
         }
+        if constexpr (HELD == FP4) {
 #pragma unroll
-        for (int x = 0; x < NR; ++x) vs[x] = turned<HELD>(vs[x], turn);
+            for (int x = 0; x < NR; ++x) vs[x] = turned(vs[x], turn);
+        }
         store_pieces(values + buf * T::kTile, v_to, vs, v_sc);
     };
     // a bf16 tile straight into LDS: a lane fetches the piece that belongs in its place
