@@ -351,9 +351,10 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, Plan pl)
 // but streaming reads reaches 7.1.  About 18 us of a call are its start (lengths,
 // table, first tiles) and end: 1024 tokens of one head of 64 take 8.0 us.  17 to
 // 32 queries are two groups: 131072 tokens with 32 queries a head take 142 us and
-// move 771 MB, with 16 queries 95 us and 538 MB.  4-bit caches: 131072 tokens (143
-// MB) 42 us, 64 sequences of up to 32768 (1.45 GB) 287, 5.1 TB/s; with a window of
-// 4096 184 us in bf16 (1.07 GB, 5.8 TB/s), 110 in e4m3, 69 in 4 bits.  Loads and
+// move 771 MB, with 16 queries 95 us and 538 MB (up to 15% more by where the cache lies
+// in memory).  4-bit caches: 131072 tokens (143
+// MB) 41 us, 64 sequences of up to 32768 (1.45 GB) 287, 5.1 TB/s; with a window of
+// 4096 183 us in bf16 (1.07 GB, 5.8 TB/s), 107 in e4m3, 65 in 4 bits.  Loads and
 // softmax without the products take 254 of the 287 us: pages of 1 KiB a head and
 // their scales 64 bytes at a time are what bounds it.  Tried on it and not kept: two
 // or three tiles ahead (39 us for 42, but 325 to 350 for 287), values turned by LDS

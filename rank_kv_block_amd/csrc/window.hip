@@ -81,8 +81,9 @@ __device__ inline void dead_groups(const AttendArgs& a, const Plan& pl, int spar
 // from LDS a step ahead.  So a wave has work for the vector units and for the
 // matrix cores at a time (2048 rows of 8 queries for each of 8 heads of 128 on a
 // window of 4096 tokens: 458 us with scores and exponentials of the same tile,
-// 400 so; 400 -> 380 with the bank conflicts below taken out, -> 375 with values
-// a step ahead).
+// 400 so; 400 -> 380 with the order in which turned() writes 4-bit values, which
+// leaves 23% of LDS's cycles to bank conflicts for 38%, -> 375 with values a step
+// ahead).
 //
 // With more than kWindowQueries queries per kv head the weights enter the value
 // product as one bf16 term, 2^-8 of a weight off at most (the stream and tree
@@ -95,10 +96,11 @@ __device__ inline void dead_groups(const AttendArgs& a, const Plan& pl, int spar
 // token of 32 heads of 64 over 131072 in 4 bits: 61 us with one term, 68 with two).
 //
 // Bound: the instructions of two waves a SIMD (the registers' limit).  Measured,
-// that call (275 GFLOP of pairs that are seen) with the clock up: 330 us from a 4-bit
-// cache, 834 TFLOP/s, 332 from bf16, 343 from e4m3, some 15% more on a card that was
-// idle; a matrix product of the library's reaches 1217.  Three prompts of up to 4100
-// rows, 4 queries for each of 8 heads, window 1024: 222 to 296 us by their lengths.
+// that call (275 GFLOP of pairs that are seen), one after another: 329 us from a
+// 4-bit cache, 836 TFLOP/s, 339 from bf16, 337 from e4m3, up to 8% more where a
+// profiler's pauses let the clock fall; a matrix product of the library's reaches
+// 1217.  Three prompts, 4 queries for each of 8 heads, window 1024: 207 us with 4100,
+// 2469 and 2365 rows, 280 with 4100, 4095 and 3907.
 // Short walks pay about 14 us of an item's start and end (18 tiles: 651 TFLOP/s).
 // Tried and not kept: instruction orders laid down by hand, products k by k through
 // both halves, wave priorities (all slower), eight waves of 32 queries (2%), 64
