@@ -120,6 +120,21 @@ def test_rows_of_one_long_sequence(live):
         c.check(p, ALL, 0)
 
 
+def test_no_live_row_of_many():
+    """A step made for many rows of one long sequence in which it has none, then some: the join finds what this call left."""
+    Hq, Hk, D, B, n, M = 8, 8, 64, 16, 620, 2048 * 4
+    c = make("bf16", 1, M, Hq, Hk, D, B, n, lens=[n * B - 7], drafts=[0])
+    with _handle(Hq, Hk, D, B, c.N) as p:
+        ws = torch.full((rk.pred_attend_window_workspace_bytes(p.handle, 1, M, n, ALL, 0),), 0x7F, dtype=torch.uint8, device="cuda")
+        for live in (0, 40, M, 0, 200):
+            c.drafts.fill_(live)
+            c.out.fill_(9.0)
+            c.lse.fill_(9.0)
+            rk.pred_attend_window(p.handle, c.kv, c.q, c.tables, c.lens, c.drafts, ALL, 0, c.scale, c.out, c.lse, ws)
+            rk.pred_device_error(p.handle)
+            c.check(p, ALL, 0)
+
+
 def test_workspace_of_long_prompts():
     """The partial results of one sequence are those of calls that can be split: no more for 2^20 rows than for 2^13."""
     with _handle(32, 8, 128, 16, 4) as p:
