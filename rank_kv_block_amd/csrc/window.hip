@@ -87,8 +87,9 @@ __device__ inline void dead_groups(const AttendArgs& a, const Plan& pl, int spar
 //
 // With more than kWindowQueries queries per kv head the weights enter the value
 // product as one bf16 term, 2^-8 of a weight off at most (the stream and tree
-// kernels' two terms would be half as many matrix instructions again): an output is
-// 2^-8 of the weighted mean of the absolute values off at most.  Where the values
+// kernels' two terms are half as many matrix instructions again: the call above 415 us
+// for 325 from bf16, three prompts 244 for 202): an output is 2^-8 of the weighted
+// mean of the absolute values off at most.  Where the values
 // are of either sign that is about what the output's own rounding to bf16 adds
 // (error against 64 bits 0.0023 relative, 0.0017 with the rounding alone).  Fewer
 // queries, which come here where the cache's layout is not the stream kernel's, have
