@@ -5,6 +5,7 @@ fallback implementation behind these names.
 """
 
 import ctypes
+import importlib.util
 import os
 
 # PRED_LIBRARY selects another build of the same library (e.g. the host-side
@@ -188,6 +189,13 @@ def load():
         raise RuntimeError(
             f"{LIB_PATH} is not built: run `python -c 'import __graft_entry__ as g; g.build()'` "
             "(hipcc --offload-arch=gfx950) first")
+    # PyTorch brings a HIP runtime of its own under the system's name.  Whichever is loaded first serves both; a process with
+    # two of them finds no device in one.
+    torch = importlib.util.find_spec("torch")
+    if torch is not None:
+        runtime = os.path.join(torch.submodule_search_locations[0], "lib", "libamdhip64.so")
+        if os.path.exists(runtime):
+            ctypes.CDLL(runtime)
     lib = ctypes.CDLL(LIB_PATH)
     for name, (res, args) in SIGNATURES.items():
         fn = getattr(lib, name)
